@@ -25,7 +25,8 @@ from . import _lib
 from ._lib import KERNELS, Q4Error
 
 __all__ = ["Q4Weight", "linear", "linear_noalloc", "linear_grouped", "pack", "pack_nibbles", "quantize", "quantize_pack", "concat_n", "split_n", "packed_sizes", "workspace_bytes", "get_crossover",
-           "set_crossover", "segments", "Q4Error", "library_path"]
+           "set_crossover", "segments", "Q4Error", "library_path",
+           "Int8Matrix", "quantize_int8", "pack_int8", "quantize_pack_int8", "linear_int8"]
 
 
 def library_path() -> str:
@@ -262,6 +263,139 @@ def linear_grouped(x: torch.Tensor, weights, outs=None, workspace: torch.Tensor 
         st = lib.q4_linear_grouped(x.data_ptr(), dtype, items, len(weights), M, K, ws_ptr, ws_len, _stream(dev))
     _lib.check(st, "q4_linear_grouped")
     return outs
+
+
+@dataclass
+class Int8Matrix:
+    """A packed matrix of 8-bit codes with one scale for each row (weights, or
+    activations that several products share): ``codes`` int8
+    [q4_int8_packed_bytes], ``scales`` float32 [rows], both on one GPU."""
+    codes: torch.Tensor
+    scales: torch.Tensor
+    rows: int
+    K: int
+
+    @property
+    def device(self) -> torch.device:
+        return self.codes.device
+
+
+_DTYPES = {torch.float32: _lib.Q4_F32, torch.bfloat16: _lib.Q4_BF16, torch.float16: _lib.Q4_F16}
+
+
+def _int8_bytes(rows: int, K: int) -> int:
+    n = int(_lib.load().q4_int8_packed_bytes(rows, K))
+    if n == 0:
+        raise ValueError("bad shape %d x %d (K must be a positive multiple of 32, at most 131040)" % (rows, K))
+    return n
+
+
+def _need_int8(w, name: str, device=None):
+    if not isinstance(w, Int8Matrix):
+        raise TypeError("%s must be an Int8Matrix (see pack_int8)" % name)
+    _need(w.codes, name + ".codes", (torch.int8,), 1, device)
+    _need(w.scales, name + ".scales", (torch.float32,), 1, w.codes.device)
+    if w.codes.numel() != _int8_bytes(w.rows, w.K) or w.scales.numel() != w.rows:
+        raise ValueError("%s does not hold %d x %d packed codes and %d scales" % (name, w.rows, w.K, w.rows))
+
+
+def quantize_int8(w: torch.Tensor):
+    """Dense rows [R, K] (float32, bfloat16 or float16, on a GPU) -> canonical
+    (codes int8 [R, K], scales float32 [R]) for ``pack_int8``.  For each row
+    s = absmax / 127 rounded once to float32, code =
+    clamp(round_half_even(w / s), -127, 127); a row with an infinity or NaN
+    gets s = NaN and codes 0 (include/q4.h)."""
+    lib = _lib.load()
+    _need(w, "w", tuple(_DTYPES), 2)
+    R, K = w.shape
+    codes = torch.empty((R, K), dtype=torch.int8, device=w.device)
+    scales = torch.empty(R, dtype=torch.float32, device=w.device)
+    with torch.cuda.device(w.device):
+        st = lib.q4_int8_quantize(w.data_ptr(), _DTYPES[w.dtype], codes.data_ptr(), scales.data_ptr(), R, K,
+                                  _stream(w.device))
+    _lib.check(st, "q4_int8_quantize")
+    return codes, scales
+
+
+def pack_int8(codes: torch.Tensor, scales: torch.Tensor) -> Int8Matrix:
+    """codes int8 [R, K], scales float32 [R] -> Int8Matrix (the scales tensor
+    is kept as given)."""
+    lib = _lib.load()
+    _need(codes, "codes", (torch.int8,), 2)
+    _need(scales, "scales", (torch.float32,), 1, codes.device)
+    R, K = codes.shape
+    if scales.numel() != R:
+        raise ValueError("scales must be [%d]" % R)
+    packed = torch.empty(_int8_bytes(R, K), dtype=torch.int8, device=codes.device)
+    with torch.cuda.device(codes.device):
+        st = lib.q4_int8_pack(codes.data_ptr(), packed.data_ptr(), R, K, _stream(codes.device))
+    _lib.check(st, "q4_int8_pack")
+    return Int8Matrix(packed, scales, R, K)
+
+
+def quantize_pack_int8(w: torch.Tensor) -> Int8Matrix:
+    """quantize_int8() and pack_int8() in one kernel: dense rows [R, K] ->
+    Int8Matrix (a weight, or activations for several ``linear_int8`` calls)."""
+    lib = _lib.load()
+    _need(w, "w", tuple(_DTYPES), 2)
+    R, K = w.shape
+    packed = torch.empty(_int8_bytes(R, K), dtype=torch.int8, device=w.device)
+    scales = torch.empty(R, dtype=torch.float32, device=w.device)
+    with torch.cuda.device(w.device):
+        st = lib.q4_int8_quantize_pack(w.data_ptr(), _DTYPES[w.dtype], packed.data_ptr(), scales.data_ptr(), R, K,
+                                       _stream(w.device))
+    _lib.check(st, "q4_int8_quantize_pack")
+    return Int8Matrix(packed, scales, R, K)
+
+
+def linear_int8(x, w: Int8Matrix, out: torch.Tensor | None = None, out_dtype: torch.dtype = torch.float32,
+                workspace: torch.Tensor | bool | None = True) -> torch.Tensor:
+    """y[m, n] = (sum_k qx[m, k] qw[n, k]) sx[m] sw[n] on the current stream of
+    x's device.
+
+    x: bfloat16 or float16 [M, K], quantized row by row within the call, or an
+    Int8Matrix (``quantize_pack_int8``) that several products share; the bits
+    are the same.  out_dtype: float32, bfloat16 or float16 (``out``'s own if
+    given).  workspace: True allocates what the call needs; a uint8 tensor is
+    used as given; False/None for calls that need none.
+    """
+    lib = _lib.load()
+    dense = not isinstance(x, Int8Matrix)
+    if dense:
+        _need(x, "x", (torch.bfloat16, torch.float16), 2)
+        M, K = x.shape
+    else:
+        _need_int8(x, "x")
+        M, K = x.rows, x.K
+    dev = x.device
+    _need_int8(w, "w", dev)
+    N = w.rows
+    if K != w.K:
+        raise ValueError("x has K=%d, weight has K=%d" % (K, w.K))
+    if out is None:
+        if out_dtype not in _DTYPES:
+            raise TypeError("out_dtype must be one of %s" % (tuple(_DTYPES),))
+        out = torch.empty((M, N), dtype=out_dtype, device=dev)
+    else:
+        _need(out, "out", tuple(_DTYPES), 2, dev)
+        if tuple(out.shape) != (M, N):
+            raise ValueError("out must be [%d, %d]" % (M, N))
+    kind = _DTYPES[x.dtype] if dense else _lib.Q4_I8
+    ws_ptr, ws_len = None, 0
+    if isinstance(workspace, torch.Tensor):
+        _need(workspace, "workspace", (torch.uint8,), 1, dev)
+        ws_ptr, ws_len = workspace.data_ptr(), workspace.numel()
+    elif workspace:
+        need = lib.q4_int8_workspace_bytes(M, N, K, kind)
+        if need:
+            ws = torch.empty(need, dtype=torch.uint8, device=dev)
+            ws_ptr, ws_len = ws.data_ptr(), need
+    with torch.cuda.device(dev):
+        st = lib.q4_int8_linear(x.data_ptr() if dense else x.codes.data_ptr(), kind,
+                                None if dense else x.scales.data_ptr(), w.codes.data_ptr(), w.scales.data_ptr(),
+                                out.data_ptr(), _DTYPES[out.dtype], M, N, K, ws_ptr, ws_len, _stream(dev))
+    _lib.check(st, "q4_int8_linear")
+    return out
 
 
 def get_crossover() -> int:

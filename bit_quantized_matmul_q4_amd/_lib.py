@@ -25,6 +25,7 @@ Q4_ERR_SCRATCH = -7
 Q4_F16 = 0
 Q4_BF16 = 1
 Q4_F32 = 2
+Q4_I8 = 3
 
 Q4_AUTO = 0
 Q4_GEMV = 1
@@ -35,6 +36,8 @@ KERNELS = {"auto": Q4_AUTO, "gemv": Q4_GEMV, "gemm": Q4_GEMM}
 EXPORTS = (
     "q4_linear", "q4_linear_f16", "q4_linear_ex", "q4_linear_noalloc", "q4_linear_grouped", "q4_workspace_bytes",
     "q4_pack", "q4_pack_nibbles", "q4_quantize",
+    "q4_int8_packed_bytes", "q4_int8_quantize", "q4_int8_quantize_pack", "q4_int8_pack", "q4_int8_workspace_bytes",
+    "q4_int8_linear",
     "q4_packed_code_bytes", "q4_packed_scale_bytes",
     "q4_get_crossover", "q4_set_crossover", "q4_segments", "q4_strerror",
     "q4_last_hip_error", "q4_abi_version",
@@ -87,6 +90,18 @@ def _declare(lib):
     lib.q4_packed_code_bytes.restype = sz
     lib.q4_packed_scale_bytes.argtypes = [i, i]
     lib.q4_packed_scale_bytes.restype = sz
+    lib.q4_int8_packed_bytes.argtypes = [i, i]
+    lib.q4_int8_packed_bytes.restype = sz
+    lib.q4_int8_quantize.argtypes = [vp, i, vp, vp, i, i, vp]
+    lib.q4_int8_quantize.restype = i
+    lib.q4_int8_quantize_pack.argtypes = [vp, i, vp, vp, i, i, vp]
+    lib.q4_int8_quantize_pack.restype = i
+    lib.q4_int8_pack.argtypes = [vp, vp, i, i, vp]
+    lib.q4_int8_pack.restype = i
+    lib.q4_int8_workspace_bytes.argtypes = [i, i, i, i]
+    lib.q4_int8_workspace_bytes.restype = sz
+    lib.q4_int8_linear.argtypes = [vp, i, vp, vp, vp, vp, i, i, i, i, vp, sz, vp]
+    lib.q4_int8_linear.restype = i
     lib.q4_get_crossover.argtypes = []
     lib.q4_get_crossover.restype = i
     lib.q4_set_crossover.argtypes = [i]

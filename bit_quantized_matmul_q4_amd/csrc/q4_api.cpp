@@ -88,6 +88,21 @@ int check_shape(long long M, long long N, long long K)
     return Q4_OK;
 }
 
+// Shapes of the 8-bit product: the 32-bit sums stay exact (K 2^14 < 2^31, for
+// codes down to -128), and every launch stays below 2^32 threads.
+int check_int8(long long rows, long long N, long long K)
+{
+    if (rows < 1 || N < 1 || K < 32 || K % 32 != 0 || K > Q4_INT8_MAX_K)
+        return Q4_ERR_SHAPE;
+    const long long lim = 1LL << 26;
+    if (rows > lim || N > lim || rows > (1LL << 36) / N)
+        return Q4_ERR_SHAPE;
+    return Q4_OK;
+}
+
+// The launchers' element kinds.
+int elem_kind(int dtype) { return dtype == Q4_F32 ? 2 : dtype == Q4_BF16 ? 1 : 0; }
+
 int hip_status(hipError_t e)
 {
     if (e == hipSuccess)
@@ -336,6 +351,82 @@ int q4_linear_grouped(const void *x, int x_dtype, const q4_group_item *items, in
             return st;
     }
     return Q4_OK;
+}
+
+size_t q4_int8_packed_bytes(int rows, int K)
+{
+    return check_int8(rows, 1, K) == Q4_OK ? q4::int8_packed_bytes(rows, K) : 0;
+}
+
+static int int8_quantize_impl(const void *w, int w_dtype, int8_t *codes, bool packed, float *scales, int rows, int K,
+                              void *stream)
+{
+    if (!w || !codes || !scales)
+        return Q4_ERR_NULL;
+    if (w_dtype != Q4_F16 && w_dtype != Q4_BF16 && w_dtype != Q4_F32)
+        return Q4_ERR_ENUM;
+    const int sh = check_int8(rows, 1, K);
+    if (sh != Q4_OK)
+        return sh;
+    if (!aligned(w, 16) || !aligned(codes, 16) || !aligned(scales, 4))
+        return Q4_ERR_ALIGN;
+    return hip_status(
+        q4::launch_int8_quantize(w, elem_kind(w_dtype), codes, packed, scales, rows, K, (hipStream_t)stream));
+}
+
+int q4_int8_quantize(const void *w, int w_dtype, int8_t *codes, float *scales, int rows, int K, void *stream)
+{
+    return int8_quantize_impl(w, w_dtype, codes, false, scales, rows, K, stream);
+}
+
+int q4_int8_quantize_pack(const void *w, int w_dtype, void *packed, float *scales, int rows, int K, void *stream)
+{
+    return int8_quantize_impl(w, w_dtype, (int8_t *)packed, true, scales, rows, K, stream);
+}
+
+int q4_int8_pack(const int8_t *codes, void *packed, int rows, int K, void *stream)
+{
+    if (!codes || !packed)
+        return Q4_ERR_NULL;
+    const int sh = check_int8(rows, 1, K);
+    if (sh != Q4_OK)
+        return sh;
+    if (!aligned(codes, 16) || !aligned(packed, 16))
+        return Q4_ERR_ALIGN;
+    return hip_status(q4::launch_int8_pack(codes, (int8_t *)packed, rows, K, (hipStream_t)stream));
+}
+
+size_t q4_int8_workspace_bytes(int M, int N, int K, int x_dtype)
+{
+    if (check_int8(M, N, K) != Q4_OK || (x_dtype != Q4_F16 && x_dtype != Q4_BF16 && x_dtype != Q4_I8))
+        return 0;
+    return q4::int8_workspace_bytes(x_dtype != Q4_I8, M, N, K);
+}
+
+int q4_int8_linear(const void *x, int x_dtype, const float *x_scales, const void *Wq, const float *w_scales, void *y,
+                   int y_dtype, int M, int N, int K, void *workspace, size_t workspace_bytes, void *stream)
+{
+    if (!x || !Wq || !w_scales || !y || (x_dtype == Q4_I8 && !x_scales))
+        return Q4_ERR_NULL;
+    if (x_dtype != Q4_F16 && x_dtype != Q4_BF16 && x_dtype != Q4_I8)
+        return Q4_ERR_ENUM;
+    if (y_dtype != Q4_F16 && y_dtype != Q4_BF16 && y_dtype != Q4_F32)
+        return Q4_ERR_ENUM;
+    const int sh = check_int8(M, N, K);
+    if (sh != Q4_OK)
+        return sh;
+    if (!aligned(x, 16) || !aligned(Wq, 16) || !aligned(w_scales, 4) || !aligned(y, y_dtype == Q4_F32 ? 4 : 2) ||
+        (x_dtype == Q4_I8 && !aligned(x_scales, 4)))
+        return Q4_ERR_ALIGN;
+    if (workspace_bytes > 0 && !workspace)
+        return Q4_ERR_WORKSPACE;
+    if (workspace && !aligned(workspace, 256))
+        return Q4_ERR_ALIGN;
+    if (workspace_bytes < q4::int8_workspace_bytes(x_dtype != Q4_I8, M, N, K))
+        return Q4_ERR_WORKSPACE;
+    return hip_status(q4::launch_int8_linear(x, x_dtype == Q4_I8 ? -1 : elem_kind(x_dtype), x_scales,
+                                             (const int8_t *)Wq, w_scales, y, elem_kind(y_dtype), M, N, K, workspace,
+                                             (hipStream_t)stream));
 }
 
 }  // extern "C"

@@ -1,0 +1,704 @@
+// q4_int8.hip -- the matrix product in 8-bit integers for gfx950 (MI355X):
+//
+//     y[m][n] = (sum_k qx[m][k] qw[n][k]) sx[m] sw[n]
+//
+// with one binary32 scale for each row of x (token) and each row of W
+// (channel).  The sum is a 32-bit integer and exact, so a row's bits depend
+// on the row alone: not on M, the kernel, the tile or the split of K.
+//
+// Row quantizer: a = max |x[m]|; s = a / 127 rounded once to binary32;
+// q = clamp(round_half_even(x / s), -127, 127) on the exact quotient.  A row
+// of zeros has s = 0 and codes 0; a row that holds an infinity or NaN has
+// s = NaN and codes 0, so its outputs are NaN and no other row's are.
+//
+// Packed layout of both operands (q4.h): tiles of 16 rows by 64 k in the
+// order [ceil(rows / 16)][2 ceil(K / 128)], 1024 bytes each; lane l = 16 g +
+// c of a wave owns bytes 16 l .. 16 l + 15: row 16 t + c, k = 64 q + 16 g ..
+// + 15.  That is the operand order of v_mfma_i32_16x16x64_i8, so a wave's
+// loads from memory and from LDS are contiguous and need no swizzle.
+// Padding rows and padding k are zero.
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include <algorithm>
+#include <type_traits>
+
+#include "q4_launch.hpp"
+
+namespace q4 {
+
+namespace {
+
+typedef int i32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+
+// k64 tiles of a packed row tile (K padded to 128)
+__host__ __device__ inline int int8_tiles(int K) { return 2 * ((K + 127) / 128); }
+
+// ------------------------------------------------------------- quantizer
+// Element types: 0 binary16, 1 bfloat16, 2 binary32.
+template <int KIND>
+using Elem = std::conditional_t<KIND == 2, uint32_t, uint16_t>;
+
+template <int KIND>
+__device__ __forceinline__ float elem_value(uint32_t bits)
+{
+    if constexpr (KIND == 2)
+        return __builtin_bit_cast(float, bits);
+    else if constexpr (KIND == 1)
+        return __builtin_bit_cast(float, bits << 16);
+    else
+        return (float)__builtin_bit_cast(_Float16, (uint16_t)bits);
+}
+
+// Largest |x| as ordered bits: the sign dropped, infinities and NaN above
+// every finite value.
+template <int KIND>
+constexpr uint32_t kAbsMask = KIND == 2 ? 0x7FFFFFFFu : 0x7FFFu;
+template <int KIND>
+constexpr uint32_t kInfBits = KIND == 2 ? 0x7F800000u : KIND == 1 ? 0x7F80u : 0x7C00u;
+
+// What a row's codes are made with: lift (a power of two that keeps the
+// quotient's operands normal), the lifted scale and its approximate inverse.
+struct RowScale {
+    float scale, lift, s, inv;
+};
+
+template <int KIND>
+__device__ __forceinline__ RowScale row_scale(uint32_t top)
+{
+    RowScale r;
+    if (top >= kInfBits<KIND>) {
+        r.scale = __builtin_nanf("");
+        r.lift = r.s = r.inv = 0.f;
+        return r;
+    }
+    const float a = elem_value<KIND>(top);
+    r.scale = a / 127.f;
+    r.lift = a < 0x1p-90f ? 0x1p100f : 1.f;
+    r.s = r.scale * r.lift;  // exact
+    r.inv = r.s > 0.f ? 1.f / r.s : 0.f;
+    return r;
+}
+
+// round_half_even(x / s), exactly: an estimate from the inverse (off by one
+// at most, and only next to a border), put right by the remainder x - r s,
+// which one fma gives without rounding (it is a multiple of ulp(s) / 2 and
+// at most about s).
+__device__ __forceinline__ int row_code(float x, const RowScale &r)
+{
+    if (!(r.s > 0.f))
+        return 0;
+    x *= r.lift;
+    float q = __builtin_rintf(x * r.inv);
+    const float e = __builtin_fmaf(-q, r.s, x);
+    const float e2 = 2.f * __builtin_fabsf(e);
+    const bool odd = ((int)q & 1) != 0;
+    if (e2 > r.s || (e2 == r.s && odd))
+        q += __builtin_copysignf(1.f, e);
+    return (int)__builtin_fminf(__builtin_fmaxf(q, -127.f), 127.f);
+}
+
+// One workgroup quantizes RW rows (a divisor of 16); a wave's 64 lanes are RW
+// rows by 64 / RW pieces of 16 k, so with RW = 16 both the reads (whole
+// 128-byte lines) and the packed writes (1 KB) are contiguous; fewer rows a
+// workgroup spread few rows over more compute units.  Two passes over the
+// row: the largest |x|, then the codes; the second reads the first HELD
+// pieces of each lane from registers and the rest from the L2.
+// PACKED: the packed layout (padding written), else codes [rows][K].
+// grid = row groups (PACKED: of the padded rows, so that padding rows are
+// written too).
+constexpr int kQuantThreads = 512;
+
+template <int KIND, int RW, bool PACKED>
+__global__ __launch_bounds__(kQuantThreads) void q4_int8_quantize_kernel(const void *__restrict__ x_,
+                                                                       int8_t *__restrict__ codes,
+                                                                       float *__restrict__ scales, int rows, int K)
+{
+    typedef Elem<KIND> E;
+    constexpr int PIECES = 64 / RW;                     // pieces of 16 k a wave step covers
+    constexpr int STEP = PIECES * (kQuantThreads / 64);  // and the workgroup's
+    constexpr int HELD = KIND == 2 ? 2 : 4;
+    constexpr int VECS = (int)sizeof(E);  // 16-byte vectors a piece
+    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+    const int c = lane % RW, p0 = wave * PIECES + lane / RW;
+    const int row = blockIdx.x * RW + c;
+    const bool live = row < rows;
+    const int pieces = K / 16;
+    const E *x = (const E *)x_ + (size_t)(live ? row : 0) * K;
+
+    u32x4 held[HELD][VECS];
+    uint32_t top = 0;
+    auto load = [&](int p, u32x4 (&v)[VECS]) {
+        const u32x4 *src = (const u32x4 *)(x + 16 * (size_t)p);
+#pragma unroll
+        for (int i = 0; i < VECS; ++i)
+            v[i] = src[i];
+    };
+    auto see = [&](const u32x4 (&v)[VECS]) {
+#pragma unroll
+        for (int i = 0; i < VECS; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                if constexpr (KIND == 2) {
+                    top = max(top, v[i][j] & kAbsMask<KIND>);
+                } else {
+                    top = max(top, v[i][j] & kAbsMask<KIND>);
+                    top = max(top, (v[i][j] >> 16) & kAbsMask<KIND>);
+                }
+            }
+    };
+    if (live) {
+#pragma unroll
+        for (int h = 0; h < HELD; ++h)
+            if (p0 + h * STEP < pieces)
+                load(p0 + h * STEP, held[h]);
+#pragma unroll
+        for (int h = 0; h < HELD; ++h)
+            if (p0 + h * STEP < pieces)
+                see(held[h]);
+        for (int p = p0 + HELD * STEP; p < pieces; p += STEP) {
+            u32x4 v[VECS];
+            load(p, v);
+            see(v);
+        }
+    }
+    // over the lanes and waves of the same row
+    __shared__ uint32_t tops[kQuantThreads / 64][RW];
+#pragma unroll
+    for (int d = RW; d < 64; d *= 2)
+        top = max(top, (uint32_t)__shfl_xor((int)top, d));
+    if (lane < RW)
+        tops[wave][lane] = top;
+    __syncthreads();
+    top = 0;
+#pragma unroll
+    for (int w = 0; w < kQuantThreads / 64; ++w)
+        top = max(top, tops[w][c]);
+    const RowScale rs = row_scale<KIND>(top);
+    if (live && threadIdx.x < RW)
+        scales[row] = rs.scale;
+
+    auto code = [&](const u32x4 (&v)[VECS]) {
+        u32x4 out;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            uint32_t word = 0;
+#pragma unroll
+            for (int b = 0; b < 4; ++b) {
+                const int e = 4 * j + b;
+                uint32_t bits;
+                if constexpr (KIND == 2)
+                    bits = v[e / 4][e % 4];
+                else
+                    bits = (v[e / 8][(e / 2) % 4] >> (16 * (e & 1))) & 0xFFFFu;
+                word |= ((uint32_t)row_code(elem_value<KIND>(bits), rs) & 0xFFu) << (8 * b);
+            }
+            out[j] = word;
+        }
+        return out;
+    };
+    const int tiles = int8_tiles(K);
+    const int all = PACKED ? 4 * tiles : pieces;
+    auto store = [&](int p, u32x4 v) {
+        if constexpr (PACKED) {
+            const size_t tile = (size_t)(row >> 4) * tiles + (p >> 2);
+            *(u32x4 *)(codes + tile * 1024 + (p & 3) * 256 + (row & 15) * 16) = v;
+        } else if (live) {
+            *(u32x4 *)(codes + (size_t)row * K + 16 * (size_t)p) = v;
+        }
+    };
+#pragma unroll
+    for (int h = 0; h < HELD; ++h) {
+        const int p = p0 + h * STEP;
+        if (p < all)
+            store(p, live && p < pieces ? code(held[h]) : (u32x4){0, 0, 0, 0});
+    }
+    for (int p = p0 + HELD * STEP; p < all; p += STEP) {
+        u32x4 v[VECS];
+        if (live && p < pieces) {
+            load(p, v);
+            store(p, code(v));
+        } else {
+            store(p, (u32x4){0, 0, 0, 0});
+        }
+    }
+}
+
+// Canonical codes [rows][K] -> packed, 16 bytes a thread.
+__global__ __launch_bounds__(256) void q4_int8_pack_kernel(const int8_t *__restrict__ codes,
+                                                           int8_t *__restrict__ packed, int rows, int K, size_t items)
+{
+    const int tiles = int8_tiles(K);
+    for (size_t i = (size_t)blockIdx.x * 256 + threadIdx.x; i < items; i += (size_t)gridDim.x * 256) {
+        const int lane = (int)(i & 63);
+        const size_t tile = i >> 6;
+        const size_t row = tile / tiles * 16 + (lane & 15);
+        const int k = (int)(tile % tiles) * 64 + 16 * (lane >> 4);
+        u32x4 v = {0, 0, 0, 0};
+        if (row < (size_t)rows && k < K)
+            v = *(const u32x4 *)(codes + row * K + k);
+        *(u32x4 *)(packed + i * 16) = v;
+    }
+}
+
+// --------------------------------------------------------------- outputs
+// Output types: 0 binary16, 1 bfloat16, 2 binary32.
+// A scale as mantissa in [0.5, 1) and exponent: the output's value is
+// float(sum) times both mantissas (three roundings), then one ldexp by both
+// exponents, so that no product on the way overflows or underflows where the
+// value does not (a huge activation scale against a tiny weight scale).
+struct Scale {
+    float m;
+    int e;
+};
+__device__ __forceinline__ Scale split_scale(float s)
+{
+    return Scale{__builtin_amdgcn_frexp_mantf(s), __builtin_amdgcn_frexp_expf(s)};
+}
+__device__ __forceinline__ float scaled(int sum, Scale sx, Scale sw)
+{
+    return __builtin_ldexpf((float)sum * sx.m * sw.m, sx.e + sw.e);
+}
+
+__device__ __forceinline__ uint16_t bf16_bits(float v)
+{
+    return __builtin_bit_cast(uint16_t, (__bf16)v);
+}
+__device__ __forceinline__ uint16_t f16_bits(float v)
+{
+    return __builtin_bit_cast(uint16_t, (_Float16)v);
+}
+
+// Four consecutive outputs n .. n + 3 of row m (those below N), as one store
+// where `vec` says that rows start aligned.
+template <int YK>
+__device__ __forceinline__ void store4(void *y, size_t at, int left, bool vec, f32x4 v)
+{
+    if constexpr (YK == 2) {
+        float *p = (float *)y + at;
+        if (vec && left >= 4) {
+            *(f32x4 *)p = v;
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (i < left)
+                    p[i] = v[i];
+        }
+    } else {
+        uint16_t *p = (uint16_t *)y + at;
+        uint16_t h[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            h[i] = YK == 1 ? bf16_bits(v[i]) : f16_bits(v[i]);
+        if (vec && left >= 4) {
+            *(uint2 *)p = make_uint2(h[0] | (uint32_t)h[1] << 16, h[2] | (uint32_t)h[3] << 16);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (i < left)
+                    p[i] = h[i];
+        }
+    }
+}
+
+__device__ __forceinline__ f32x4 scaled4(i32x4 a, Scale sx, const Scale (&sw)[4])
+{
+    f32x4 v;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        v[i] = scaled(a[i], sx, sw[i]);
+    return v;
+}
+
+// --------------------------------------------------------------- few rows
+// Up to 16 RT rows of x: bound by the bytes of W.  A workgroup owns one tile
+// of 16 columns; its waves take the tile's k64 steps in turn, U at a time,
+// and their integer sums meet in LDS.
+template <int RT, int YK>
+__global__ __launch_bounds__(512) void q4_int8_gemv_kernel(const int8_t *__restrict__ xq, const float *__restrict__ sx,
+                                                           const int8_t *__restrict__ wq, const float *__restrict__ sw,
+                                                           void *__restrict__ y, int M, int N, int K, int vec)
+{
+    constexpr int W = 8;
+    constexpr int U = RT >= 4 ? 2 : 4;
+    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+    const int tiles = int8_tiles(K);
+    const int8_t *w = wq + (size_t)blockIdx.x * tiles * 1024 + lane * 16;
+    const int8_t *x = xq + lane * 16;
+    const size_t xrow = (size_t)tiles * 1024;
+    const int rows = (M + 15) / 16;  // row tiles (one past the end: the last, its outputs are not stored)
+    i32x4 acc[RT];
+#pragma unroll
+    for (int r = 0; r < RT; ++r)
+        acc[r] = (i32x4){0, 0, 0, 0};
+    for (int q0 = wave; q0 < tiles; q0 += W * U) {
+        i32x4 a[U], b[U][RT];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int q = q0 + u * W;
+            if (q < tiles) {
+                a[u] = *(const i32x4 *)(w + (size_t)q * 1024);
+#pragma unroll
+                for (int r = 0; r < RT; ++r)
+                    b[u][r] = *(const i32x4 *)(x + min(r, rows - 1) * xrow + (size_t)q * 1024);
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (q0 + u * W < tiles) {
+#pragma unroll
+                for (int r = 0; r < RT; ++r)
+                    acc[r] = __builtin_amdgcn_mfma_i32_16x16x64_i8(a[u], b[u][r], acc[r], 0, 0, 0);
+            }
+    }
+    __shared__ i32x4 part[W][RT][64];
+#pragma unroll
+    for (int r = 0; r < RT; ++r)
+        part[wave][r][lane] = acc[r];
+    __syncthreads();
+    for (int r = wave; r < RT; r += W) {
+        i32x4 s = part[0][r][lane];
+#pragma unroll
+        for (int j = 1; j < W; ++j)
+            s += part[j][r][lane];
+        const int m = 16 * r + (lane & 15), n = 16 * blockIdx.x + 4 * (lane >> 4);
+        if (m < M && n < N) {
+            Scale ws[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                ws[i] = split_scale(n + i < N ? sw[n + i] : 0.f);
+            store4<YK>(y, (size_t)m * N + n, N - n, vec, scaled4(s, split_scale(sx[m]), ws));
+        }
+    }
+}
+
+// -------------------------------------------------------------- many rows
+// LDS-tiled: a workgroup of WM x WN waves owns BM rows by BN columns; steps
+// of 128 k go from memory to LDS directly, two stages deep: the loads of step
+// s + 1 are in flight while step s is multiplied.
+__device__ __forceinline__ void load_lds16(const int8_t *g, int8_t *lds)
+{
+    __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void *)g,
+                                     (__attribute__((address_space(3))) void *)lds, 16, 0, 0);
+}
+
+template <int BM, int BN, int WM, int WN, int YK>
+__global__ __launch_bounds__(64 * WM *WN) void q4_int8_gemm_kernel(
+    const int8_t *__restrict__ xq, const float *__restrict__ sx, const int8_t *__restrict__ wq,
+    const float *__restrict__ sw, void *__restrict__ y, int *__restrict__ partial, int M, int N, int K, int steps_per,
+    int vec)
+{
+    constexpr int WAVES = WM * WN;
+    constexpr int TM = BM / 16 / WM, TN = BN / 16 / WN;  // a wave's row tiles of x and of W
+    constexpr int CHUNKS = (BM + BN) / 16 * 2;           // 1 KB pieces of a stage
+    static_assert(CHUNKS % WAVES == 0, "every wave loads as many pieces");
+    constexpr int PER = CHUNKS / WAVES;
+    constexpr int STAGE = CHUNKS * 1024;
+    extern __shared__ __attribute__((aligned(16))) int8_t lds[];
+
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+    const int wm = wave % WM, wn = wave / WM;
+    const int tiles = int8_tiles(K);
+    const int tm_all = (M + 15) / 16, tn_all = (N + 15) / 16;
+    const int gm = (M + BM - 1) / BM, gn = (N + BN - 1) / BN;
+    // workgroups go to the 8 dies in turn: each die takes a run of tiles, row
+    // tiles fastest, so that its L2 holds a panel of W while it is used
+    int id = blockIdx.x;
+    {
+        const int total = gm * gn, q = total / 8, r = total % 8, die = id & 7;
+        id = die * q + min(die, r) + (id >> 3);
+    }
+    const int bm = id % gm, bn = id / gm;
+    const int s0 = blockIdx.y * steps_per, s1 = min(tiles / 2, s0 + steps_per);
+
+    // the pieces this wave loads: the first BM / 16 pairs are rows of x
+    const int8_t *src[PER];
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+        const int ch = wave * PER + i;
+        const int t = ch >> 1;
+        const int8_t *base;
+        if (t < BM / 16)  // (a row tile past the end: the last one, its outputs are not stored)
+            base = xq + (size_t)min(bm * (BM / 16) + t, tm_all - 1) * tiles * 1024;
+        else
+            base = wq + (size_t)min(bn * (BN / 16) + t - BM / 16, tn_all - 1) * tiles * 1024;
+        src[i] = base + (ch & 1) * 1024 + lane * 16 + (size_t)s0 * 2048;
+    }
+    auto fetch = [&](int stage) {
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+            load_lds16(src[i], lds + stage * STAGE + (wave * PER + i) * 1024);
+            src[i] += 2048;
+        }
+    };
+    i32x4 acc[TN][TM];
+#pragma unroll
+    for (int i = 0; i < TN; ++i)
+#pragma unroll
+        for (int j = 0; j < TM; ++j)
+            acc[i][j] = (i32x4){0, 0, 0, 0};
+    if (s0 < s1)
+        fetch(0);
+    for (int s = s0; s < s1; ++s) {
+        const int stage = (s - s0) & 1;
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // this wave's pieces of step s
+        __syncthreads();                                  // every wave's, and step s - 1 is read
+        if (s + 1 < s1)
+            fetch(stage ^ 1);
+        const int8_t *at = lds + stage * STAGE + lane * 16;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            i32x4 a[TN], b[TM];
+#pragma unroll
+            for (int j = 0; j < TM; ++j)
+                b[j] = *(const i32x4 *)(at + ((wm * TM + j) * 2 + h) * 1024);
+#pragma unroll
+            for (int i = 0; i < TN; ++i)
+                a[i] = *(const i32x4 *)(at + ((BM / 16 + wn * TN + i) * 2 + h) * 1024);
+#pragma unroll
+            for (int i = 0; i < TN; ++i)
+#pragma unroll
+                for (int j = 0; j < TM; ++j)
+                    acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(a[i], b[j], acc[i][j], 0, 0, 0);
+        }
+    }
+    // lane (g, c) holds row c of a tile of x, rows 4 g .. 4 g + 3 of one of W
+    const int m0 = bm * BM + wm * TM * 16 + (lane & 15), n0 = bn * BN + wn * TN * 16 + 4 * (lane >> 4);
+    if (partial) {
+        int *out = partial + (size_t)blockIdx.y * M * N;
+#pragma unroll
+        for (int i = 0; i < TN; ++i)
+#pragma unroll
+            for (int j = 0; j < TM; ++j) {
+                const int m = m0 + 16 * j, n = n0 + 16 * i;
+                if (m < M && n < N) {
+                    int *p = out + (size_t)m * N + n;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        if (n + e < N)
+                            p[e] = acc[i][j][e];
+                }
+            }
+        return;
+    }
+    Scale xs[TM];
+#pragma unroll
+    for (int j = 0; j < TM; ++j)
+        xs[j] = split_scale(m0 + 16 * j < M ? sx[m0 + 16 * j] : 0.f);
+#pragma unroll
+    for (int i = 0; i < TN; ++i) {
+        const int n = n0 + 16 * i;
+        Scale ws[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            ws[e] = split_scale(n + e < N ? sw[n + e] : 0.f);
+#pragma unroll
+        for (int j = 0; j < TM; ++j) {
+            const int m = m0 + 16 * j;
+            if (m < M && n < N)
+                store4<YK>(y, (size_t)m * N + n, N - n, vec, scaled4(acc[i][j], xs[j], ws));
+        }
+    }
+}
+
+// The split's integer sums, added and scaled.
+template <int YK>
+__global__ __launch_bounds__(256) void q4_int8_join_kernel(const int *__restrict__ partial, const float *__restrict__ sx,
+                                                           const float *__restrict__ sw, void *__restrict__ y, int N,
+                                                           size_t mn, int split)
+{
+    const size_t i = (size_t)blockIdx.x * 256 + threadIdx.x;
+    if (i >= mn)
+        return;
+    int s = 0;
+    for (int j = 0; j < split; ++j)
+        s += partial[j * mn + i];
+    const size_t m = i / N;
+    const float v = scaled(s, split_scale(sx[m]), split_scale(sw[i - m * N]));
+    if constexpr (YK == 2)
+        ((float *)y)[i] = v;
+    else
+        ((uint16_t *)y)[i] = YK == 1 ? bf16_bits(v) : f16_bits(v);
+}
+
+constexpr int kUnits = 256;  // compute units
+
+// The tile and the split of K for a shape.
+struct Int8Shape {
+    bool gemv;
+    int bm, bn, split;
+};
+
+Int8Shape int8_shape(int M, int N, int K)
+{
+    Int8Shape s{M <= 64, 0, 0, 1};
+    if (s.gemv)
+        return s;
+    const int big = ((M + 255) / 256) * ((N + 255) / 256);
+    s.bm = s.bn = big >= kUnits ? 256 : 128;
+    const int wgs = ((M + s.bm - 1) / s.bm) * ((N + s.bn - 1) / s.bn);
+    const int steps = int8_tiles(K) / 2;
+    while (2 * wgs * s.split <= kUnits && steps / (2 * s.split) >= 4)
+        s.split *= 2;
+    return s;
+}
+
+template <int KIND, int RW, bool PACKED>
+void launch_rows(const void *x, int8_t *codes, float *scales, int rows, int K, hipStream_t stream)
+{
+    const int groups = PACKED ? (rows + 15) / 16 * 16 / RW : (rows + RW - 1) / RW;
+    hipLaunchKernelGGL((q4_int8_quantize_kernel<KIND, RW, PACKED>), dim3((unsigned)groups), dim3(kQuantThreads), 0,
+                       stream, x, codes, scales, rows, K);
+}
+
+template <int KIND, bool PACKED>
+void launch_rows_k(const void *x, int8_t *codes, float *scales, int rows, int K, hipStream_t stream)
+{
+    if (rows >= 4096)
+        launch_rows<KIND, 16, PACKED>(x, codes, scales, rows, K, stream);
+    else if (rows >= 1024)
+        launch_rows<KIND, 4, PACKED>(x, codes, scales, rows, K, stream);
+    else
+        launch_rows<KIND, 1, PACKED>(x, codes, scales, rows, K, stream);
+}
+
+template <int RT>
+void launch_gemv_rt(int yk, const int8_t *xq, const float *sx, const int8_t *wq, const float *sw, void *y, int M, int N,
+                    int K, int vec, hipStream_t stream)
+{
+    const dim3 grid((unsigned)((N + 15) / 16)), block(512);
+    if (yk == 2)
+        hipLaunchKernelGGL((q4_int8_gemv_kernel<RT, 2>), grid, block, 0, stream, xq, sx, wq, sw, y, M, N, K, vec);
+    else if (yk == 1)
+        hipLaunchKernelGGL((q4_int8_gemv_kernel<RT, 1>), grid, block, 0, stream, xq, sx, wq, sw, y, M, N, K, vec);
+    else
+        hipLaunchKernelGGL((q4_int8_gemv_kernel<RT, 0>), grid, block, 0, stream, xq, sx, wq, sw, y, M, N, K, vec);
+}
+
+template <int BM, int BN, int WM, int WN, int YK>
+hipError_t launch_tile_y(const int8_t *xq, const float *sx, const int8_t *wq, const float *sw, void *y, int *partial,
+                         int M, int N, int K, int split, int vec, hipStream_t stream)
+{
+    constexpr int kLds = 2 * (BM + BN) / 16 * 2 * 1024;
+    if (kLds > 64 * 1024) {
+        const hipError_t e = hipFuncSetAttribute((const void *)q4_int8_gemm_kernel<BM, BN, WM, WN, YK>,
+                                                 hipFuncAttributeMaxDynamicSharedMemorySize, kLds);
+        if (e != hipSuccess)
+            return e;
+    }
+    const int steps = int8_tiles(K) / 2;
+    const dim3 grid((unsigned)((M + BM - 1) / BM * ((N + BN - 1) / BN)), (unsigned)split);
+    hipLaunchKernelGGL((q4_int8_gemm_kernel<BM, BN, WM, WN, YK>), grid, dim3(64 * WM * WN), kLds, stream, xq, sx, wq, sw,
+                       y, partial, M, N, K, (steps + split - 1) / split, vec);
+    return hipGetLastError();
+}
+
+template <int BM, int BN, int WM, int WN>
+hipError_t launch_tile(int yk, const int8_t *xq, const float *sx, const int8_t *wq, const float *sw, void *y,
+                       int *partial, int M, int N, int K, int split, int vec, hipStream_t stream)
+{
+    if (yk == 2)
+        return launch_tile_y<BM, BN, WM, WN, 2>(xq, sx, wq, sw, y, partial, M, N, K, split, vec, stream);
+    if (yk == 1)
+        return launch_tile_y<BM, BN, WM, WN, 1>(xq, sx, wq, sw, y, partial, M, N, K, split, vec, stream);
+    return launch_tile_y<BM, BN, WM, WN, 0>(xq, sx, wq, sw, y, partial, M, N, K, split, vec, stream);
+}
+
+size_t up256(size_t n) { return (n + 255) & ~(size_t)255; }
+
+}  // namespace
+
+size_t int8_packed_bytes(int rows, int K) { return (size_t)((rows + 15) / 16) * int8_tiles(K) * 1024; }
+
+hipError_t launch_int8_quantize(const void *x, int kind, int8_t *codes, bool packed, float *scales, int rows, int K,
+                                hipStream_t stream)
+{
+    if (packed) {
+        if (kind == 2)
+            launch_rows_k<2, true>(x, codes, scales, rows, K, stream);
+        else if (kind == 1)
+            launch_rows_k<1, true>(x, codes, scales, rows, K, stream);
+        else
+            launch_rows_k<0, true>(x, codes, scales, rows, K, stream);
+    } else {
+        if (kind == 2)
+            launch_rows_k<2, false>(x, codes, scales, rows, K, stream);
+        else if (kind == 1)
+            launch_rows_k<1, false>(x, codes, scales, rows, K, stream);
+        else
+            launch_rows_k<0, false>(x, codes, scales, rows, K, stream);
+    }
+    return hipGetLastError();
+}
+
+hipError_t launch_int8_pack(const int8_t *codes, int8_t *packed, int rows, int K, hipStream_t stream)
+{
+    const size_t items = int8_packed_bytes(rows, K) / 16;
+    hipLaunchKernelGGL(q4_int8_pack_kernel, dim3((unsigned)std::min<size_t>((items + 255) / 256, 1 << 16)), dim3(256), 0,
+                       stream, codes, packed, rows, K, items);
+    return hipGetLastError();
+}
+
+size_t int8_workspace_bytes(bool dense, int M, int N, int K)
+{
+    const Int8Shape sh = int8_shape(M, N, K);
+    size_t n = 0;
+    if (dense)
+        n += up256(int8_packed_bytes(M, K)) + up256((size_t)M * sizeof(float));
+    if (sh.split > 1)
+        n += (size_t)sh.split * M * N * sizeof(int);
+    return n;
+}
+
+hipError_t launch_int8_linear(const void *x, int x_kind, const float *x_scales, const int8_t *wq, const float *w_scales,
+                              void *y, int y_kind, int M, int N, int K, void *workspace, hipStream_t stream)
+{
+    const Int8Shape sh = int8_shape(M, N, K);
+    uint8_t *ws = (uint8_t *)workspace;
+    const int8_t *xq = (const int8_t *)x;
+    const float *sx = x_scales;
+    if (x_kind >= 0) {
+        int8_t *q = (int8_t *)ws;
+        ws += up256(int8_packed_bytes(M, K));
+        float *s = (float *)ws;
+        ws += up256((size_t)M * sizeof(float));
+        const hipError_t e = launch_int8_quantize(x, x_kind, q, true, s, M, K, stream);
+        if (e != hipSuccess)
+            return e;
+        xq = q;
+        sx = s;
+    }
+    const int size = y_kind == 2 ? 4 : 2;
+    const int vec = N % 4 == 0 && ((uintptr_t)y & (4 * size - 1)) == 0;
+    if (sh.gemv) {
+        const int rt = (M + 15) / 16;
+        if (rt == 1)
+            launch_gemv_rt<1>(y_kind, xq, sx, wq, w_scales, y, M, N, K, vec, stream);
+        else if (rt == 2)
+            launch_gemv_rt<2>(y_kind, xq, sx, wq, w_scales, y, M, N, K, vec, stream);
+        else
+            launch_gemv_rt<4>(y_kind, xq, sx, wq, w_scales, y, M, N, K, vec, stream);
+        return hipGetLastError();
+    }
+    int *partial = sh.split > 1 ? (int *)ws : nullptr;
+    hipError_t e;
+    if (sh.bm == 256)
+        e = launch_tile<256, 256, 2, 4>(y_kind, xq, sx, wq, w_scales, y, partial, M, N, K, sh.split, vec, stream);
+    else
+        e = launch_tile<128, 128, 2, 2>(y_kind, xq, sx, wq, w_scales, y, partial, M, N, K, sh.split, vec, stream);
+    if (e != hipSuccess || !partial)
+        return e;
+    const size_t mn = (size_t)M * N;
+    const dim3 grid((unsigned)((mn + 255) / 256));
+    if (y_kind == 2)
+        hipLaunchKernelGGL(q4_int8_join_kernel<2>, grid, dim3(256), 0, stream, partial, sx, w_scales, y, N, mn, sh.split);
+    else if (y_kind == 1)
+        hipLaunchKernelGGL(q4_int8_join_kernel<1>, grid, dim3(256), 0, stream, partial, sx, w_scales, y, N, mn, sh.split);
+    else
+        hipLaunchKernelGGL(q4_int8_join_kernel<0>, grid, dim3(256), 0, stream, partial, sx, w_scales, y, N, mn, sh.split);
+    return hipGetLastError();
+}
+
+}  // namespace q4

@@ -52,6 +52,20 @@ hipError_t launch_pack(const uint8_t *codes, bool nibbles, const uint16_t *scale
 hipError_t launch_quantize(const void *w, int kind, uint8_t *codes, uint16_t *scales, int N, int K,
                            hipStream_t stream);
 
+// The matrix product in 8-bit integers (q4_int8.hip).  Element kinds: 0
+// binary16, 1 bfloat16, 2 binary32.
+// Dense rows [rows][K] -> codes (canonical [rows][K] or packed) and scales.
+hipError_t launch_int8_quantize(const void *x, int kind, int8_t *codes, bool packed, float *scales, int rows, int K,
+                                hipStream_t stream);
+// Canonical codes [rows][K] -> packed.
+hipError_t launch_int8_pack(const int8_t *codes, int8_t *packed, int rows, int K, hipStream_t stream);
+size_t int8_packed_bytes(int rows, int K);
+// y = x . W^T; x_kind -1: x is packed codes with x_scales; 0 or 1: dense
+// rows, quantized into the workspace (which holds int8_workspace_bytes).
+hipError_t launch_int8_linear(const void *x, int x_kind, const float *x_scales, const int8_t *wq, const float *w_scales,
+                              void *y, int y_kind, int M, int N, int K, void *workspace, hipStream_t stream);
+size_t int8_workspace_bytes(bool dense, int M, int N, int K);
+
 // Sizes of the tiled layout.
 size_t packed_code_bytes(int N, int K);
 size_t packed_scale_bytes(int N, int K);

@@ -67,14 +67,16 @@ enum q4_status {
     Q4_ERR_ALIGN = -3,     /* a pointer below the alignment its call states */
     Q4_ERR_ENUM = -4,      /* unknown dtype or kernel selector */
     Q4_ERR_HIP = -5,       /* a HIP call failed (see q4_last_hip_error) */
-    Q4_ERR_WORKSPACE = -6, /* workspace_bytes non-zero with a NULL workspace */
+    Q4_ERR_WORKSPACE = -6, /* workspace_bytes non-zero with a NULL workspace, or (calls that need one) too small */
     Q4_ERR_SCRATCH = -7    /* the call needs more than Q4_SCRATCH_BYTES of scratch */
 };
 
 /* Size of the fixed per-device scratch buffer q4_linear_noalloc uses. */
 #define Q4_SCRATCH_BYTES (4u << 20)
 
-enum q4_dtype { Q4_F16 = 0, Q4_BF16 = 1, Q4_F32 = 2 /* q4_quantize input only */ };
+/* Q4_F32: quantizer inputs, 8-bit outputs and router weights only; Q4_I8:
+ * packed 8-bit rows as the x of q4_int8_linear only. */
+enum q4_dtype { Q4_F16 = 0, Q4_BF16 = 1, Q4_F32 = 2, Q4_I8 = 3 };
 
 enum q4_kernel {
     Q4_AUTO = 0, /* the crossover rule (see q4_get_crossover) picks the kernel */
@@ -222,6 +224,62 @@ int q4_linear_grouped(const void *x, int x_dtype, const q4_group_item *items, in
  * compute calls; errors as for them (Q4_ERR_ENUM for a bad w_dtype).
  */
 int q4_quantize(const void *w, int w_dtype, uint8_t *codes, void *scales, int N, int K, void *stream);
+
+/*
+ * The matrix product in 8-bit integers, with one scale for each row of x
+ * (token) and each row of W (channel), for the row counts at which the 4-bit
+ * kernels are bound by their dequantization (prompt chunks):
+ *
+ *     y[m][n] = (sum_k qx[m][k] qw[n][k]) sx[m] sw[n]
+ *
+ * The sum is a 32-bit integer and exact, so a row's bits depend on that row
+ * and W alone (not on M, the row's place, the kernel or the split of K).
+ * The value is formed in binary32 (at most three roundings, and no overflow
+ * or underflow on the way), then rounded to the output type.  K is a multiple of 32, at most Q4_INT8_MAX_K (the sum stays exact
+ * for codes down to -128); rows and N are at most 2^26, rows N at most 2^36.
+ *
+ * Canonical form: codes int8 [rows][K], scales float32 [rows], row-major.
+ * Packed form: tiles of 16 rows by 64 k (t = row / 16, q = k / 64), tile
+ * order [ceil(rows/16)][2 ceil(K/128)], 1024 bytes each: byte 16 (16 g + c)
+ * + j holds the code of row 16 t + c, k = 64 q + 16 g + j (c in 0..15, g in
+ * 0..3, j in 0..15).  Entries past the rows or past K are zero.  Scales are
+ * the same in both forms.  x and W have the same packed form.
+ *
+ * Quantizer, for each row: a = max |w|; s = a / 127 rounded once to binary32;
+ * q = clamp(round_half_even(w / s), -127, 127) on the exact quotient.  A row
+ * of zeros (or whose s rounds to zero) gets s = 0 and codes 0.  A row that
+ * holds an infinity or a NaN gets s = NaN and codes 0: every product of that
+ * row is NaN, and no other row's is.
+ *   w        [rows][K], w_dtype Q4_F32, Q4_BF16 or Q4_F16; 16-byte aligned
+ *   codes    int8 [rows][K], 16-byte aligned (q4_int8_quantize)
+ *   packed   q4_int8_packed_bytes(rows, K) bytes, 16-byte aligned
+ *            (q4_int8_quantize_pack, q4_int8_pack)
+ *   scales   float32 [rows], 4-byte aligned
+ */
+#define Q4_INT8_MAX_K 131040
+size_t q4_int8_packed_bytes(int rows, int K); /* 0 for a bad shape */
+int q4_int8_quantize(const void *w, int w_dtype, int8_t *codes, float *scales, int rows, int K, void *stream);
+int q4_int8_quantize_pack(const void *w, int w_dtype, void *packed, float *scales, int rows, int K, void *stream);
+int q4_int8_pack(const int8_t *codes, void *packed, int rows, int K, void *stream);
+
+/*
+ * The product.
+ *   x         x_dtype Q4_BF16 or Q4_F16: dense rows [M][K], quantized within
+ *             the call (the same codes and scales as q4_int8_quantize_pack);
+ *             x_scales is not read.  x_dtype Q4_I8: packed rows with their
+ *             x_scales, quantized once for several products.  16-byte aligned
+ *   Wq        packed rows of W, 16-byte aligned; w_scales float32 [N]
+ *   y         [M][N] row-major, y_dtype Q4_F32 (4-byte aligned), Q4_BF16 or
+ *             Q4_F16 (2-byte aligned; 16-byte alignment and N % 4 == 0 give
+ *             wider stores), overwritten
+ *   workspace device scratch of at least q4_int8_workspace_bytes(M, N, K,
+ *             x_dtype) bytes, 256-byte aligned (Q4_ERR_WORKSPACE otherwise;
+ *             NULL where that is 0).  Contents before and after are
+ *             unspecified; two calls that share one must not overlap in time
+ */
+size_t q4_int8_workspace_bytes(int M, int N, int K, int x_dtype); /* 0 for a bad shape */
+int q4_int8_linear(const void *x, int x_dtype, const float *x_scales, const void *Wq, const float *w_scales, void *y,
+                   int y_dtype, int M, int N, int K, void *workspace, size_t workspace_bytes, void *stream);
 
 /* Bytes of the packed codes and packed scales of an N x K matrix (0 for a
  * bad shape).  Pure host computation.  (Library layout; pages silent.) */
