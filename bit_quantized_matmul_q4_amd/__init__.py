@@ -26,7 +26,8 @@ from ._lib import KERNELS, Q4Error
 
 __all__ = ["Q4Weight", "linear", "linear_noalloc", "linear_grouped", "pack", "pack_nibbles", "quantize", "quantize_pack", "concat_n", "split_n", "packed_sizes", "workspace_bytes", "get_crossover",
            "set_crossover", "segments", "Q4Error", "library_path",
-           "Int8Matrix", "quantize_int8", "pack_int8", "quantize_pack_int8", "linear_int8"]
+           "Int8Matrix", "quantize_int8", "pack_int8", "quantize_pack_int8", "linear_int8",
+           "moe_route", "moe_experts", "moe"]
 
 
 def library_path() -> str:
@@ -348,6 +349,17 @@ def quantize_pack_int8(w: torch.Tensor) -> Int8Matrix:
     return Int8Matrix(packed, scales, R, K)
 
 
+def _workspace(workspace, need: int, dev):
+    """(tensor to keep, pointer, bytes) of a call's workspace."""
+    if isinstance(workspace, torch.Tensor):
+        _need(workspace, "workspace", (torch.uint8,), 1, dev)
+        return workspace, workspace.data_ptr(), workspace.numel()
+    if workspace and need:
+        ws = torch.empty(need, dtype=torch.uint8, device=dev)
+        return ws, ws.data_ptr(), need
+    return None, None, 0
+
+
 def linear_int8(x, w: Int8Matrix, out: torch.Tensor | None = None, out_dtype: torch.dtype = torch.float32,
                 workspace: torch.Tensor | bool | None = True) -> torch.Tensor:
     """y[m, n] = (sum_k qx[m, k] qw[n, k]) sx[m] sw[n] on the current stream of
@@ -381,21 +393,105 @@ def linear_int8(x, w: Int8Matrix, out: torch.Tensor | None = None, out_dtype: to
         if tuple(out.shape) != (M, N):
             raise ValueError("out must be [%d, %d]" % (M, N))
     kind = _DTYPES[x.dtype] if dense else _lib.Q4_I8
-    ws_ptr, ws_len = None, 0
-    if isinstance(workspace, torch.Tensor):
-        _need(workspace, "workspace", (torch.uint8,), 1, dev)
-        ws_ptr, ws_len = workspace.data_ptr(), workspace.numel()
-    elif workspace:
-        need = lib.q4_int8_workspace_bytes(M, N, K, kind)
-        if need:
-            ws = torch.empty(need, dtype=torch.uint8, device=dev)
-            ws_ptr, ws_len = ws.data_ptr(), need
+    _keep, ws_ptr, ws_len = _workspace(workspace, lib.q4_int8_workspace_bytes(M, N, K, kind), dev)
     with torch.cuda.device(dev):
         st = lib.q4_int8_linear(x.data_ptr() if dense else x.codes.data_ptr(), kind,
                                 None if dense else x.scales.data_ptr(), w.codes.data_ptr(), w.scales.data_ptr(),
                                 out.data_ptr(), _DTYPES[out.dtype], M, N, K, ws_ptr, ws_len, _stream(dev))
     _lib.check(st, "q4_int8_linear")
     return out
+
+
+def moe_route(x: torch.Tensor, router: torch.Tensor, topk: int, bias: torch.Tensor | None = None,
+              renormalize: bool = True, workspace: torch.Tensor | bool | None = True):
+    """The topk experts of each row and their weights, by the largest of
+    softmax(x . router^T + bias): (ids int32 [M, topk], weights float32
+    [M, topk]), largest first, equal ones by lower index; the weights are
+    divided by their sum where ``renormalize``.
+
+    x: bfloat16 or float16 [M, K]; router: [E, K], x's dtype or float32; bias:
+    float32 [E] (-inf disables an expert; a slot without an expert gets id -1
+    and weight 0).  The logits are 64-bit sums, so a row's choice does not
+    depend on the batch (include/q4.h).
+    """
+    lib = _lib.load()
+    _need(x, "x", (torch.bfloat16, torch.float16), 2)
+    dev = x.device
+    _need(router, "router", (x.dtype, torch.float32), 2, dev)
+    M, K = x.shape
+    E = router.shape[0]
+    if router.shape[1] != K:
+        raise ValueError("x has K=%d, router has K=%d" % (K, router.shape[1]))
+    if bias is not None:
+        _need(bias, "bias", (torch.float32,), 1, dev)
+        if bias.numel() != E:
+            raise ValueError("bias must be [%d]" % E)
+    if not 1 <= topk <= E:
+        raise ValueError("topk=%d of %d experts" % (topk, E))
+    ids = torch.empty((M, topk), dtype=torch.int32, device=dev)
+    weights = torch.empty((M, topk), dtype=torch.float32, device=dev)
+    _keep, ws_ptr, ws_len = _workspace(workspace, lib.q4_moe_route_workspace_bytes(M, E), dev)
+    with torch.cuda.device(dev):
+        st = lib.q4_moe_route(x.data_ptr(), _DTYPES[x.dtype], router.data_ptr(), _DTYPES[router.dtype],
+                              None if bias is None else bias.data_ptr(), ids.data_ptr(), weights.data_ptr(), M, E, K,
+                              topk, int(renormalize), ws_ptr, ws_len, _stream(dev))
+    _lib.check(st, "q4_moe_route")
+    return ids, weights
+
+
+def moe_experts(x: torch.Tensor, ids: torch.Tensor, weights: torch.Tensor, w13: Q4Weight, w2: Q4Weight,
+                out: torch.Tensor | None = None, workspace: torch.Tensor | bool | None = True) -> torch.Tensor:
+    """y[m] = sum_j weights[m, j] (h . dequant(w2[e])^T) with e = ids[m, j],
+    [g | u] = x[m] . dequant(w13[e])^T and h = silu(g) u: float32 [M, H].
+
+    x: bfloat16 or float16 [M, H]; ids int32, weights float32 [M, topk] (ids
+    outside the experts add nothing).  w13: the experts' gate rows and up rows
+    packed as one weight of N = E 2 I rows, K = H; w2: N = E H rows, K = I
+    (``pack`` of the stacked rows, or ``concat_n`` of the experts' weights).
+    """
+    lib = _lib.load()
+    _need(x, "x", (torch.bfloat16, torch.float16), 2)
+    dev = x.device
+    M, H = x.shape
+    _need(ids, "ids", (torch.int32,), 2, dev)
+    _need(weights, "weights", (torch.float32,), 2, dev)
+    topk = ids.shape[1]
+    if ids.shape[0] != M or weights.shape != ids.shape:
+        raise ValueError("ids and weights must be [%d, topk], got %s and %s"
+                         % (M, tuple(ids.shape), tuple(weights.shape)))
+    for name, w in (("w13", w13), ("w2", w2)):
+        if not isinstance(w, Q4Weight):
+            raise TypeError("%s must be a Q4Weight (see pack)" % name)
+        _need(w.codes, name + ".codes", (torch.uint8,), 1, dev)
+        _need(w.scales, name + ".scales", (torch.float16,), 1, dev)
+        cb, sb = packed_sizes(w.N, w.K)
+        if w.codes.numel() != cb or w.scales.numel() * 2 != sb:
+            raise ValueError("packed %s sizes do not match N=%d K=%d" % (name, w.N, w.K))
+    I = w2.K
+    E = w2.N // H if H else 0
+    if w13.K != H or E < 1 or w2.N != E * H or w13.N != E * 2 * I:
+        raise ValueError("x [%d, %d] with w13 %d x %d and w2 %d x %d: w13 is (E 2 I) x H, w2 (E H) x I"
+                         % (M, H, w13.N, w13.K, w2.N, w2.K))
+    if out is None:
+        out = torch.empty((M, H), dtype=torch.float32, device=dev)
+    else:
+        _need(out, "out", (torch.float32,), 2, dev)
+        if tuple(out.shape) != (M, H):
+            raise ValueError("out must be [%d, %d]" % (M, H))
+    _keep, ws_ptr, ws_len = _workspace(workspace, lib.q4_moe_workspace_bytes(M, I, topk), dev)
+    with torch.cuda.device(dev):
+        st = lib.q4_moe_experts(x.data_ptr(), _DTYPES[x.dtype], ids.data_ptr(), weights.data_ptr(),
+                                w13.codes.data_ptr(), w13.scales.data_ptr(), w2.codes.data_ptr(),
+                                w2.scales.data_ptr(), out.data_ptr(), M, E, H, I, topk, ws_ptr, ws_len, _stream(dev))
+    _lib.check(st, "q4_moe_experts")
+    return out
+
+
+def moe(x: torch.Tensor, router: torch.Tensor, w13: Q4Weight, w2: Q4Weight, topk: int,
+        bias: torch.Tensor | None = None, renormalize: bool = True, out: torch.Tensor | None = None) -> torch.Tensor:
+    """The whole expert layer: ``moe_route`` and ``moe_experts``."""
+    ids, weights = moe_route(x, router, topk, bias, renormalize)
+    return moe_experts(x, ids, weights, w13, w2, out)
 
 
 def get_crossover() -> int:

@@ -59,7 +59,7 @@ def _compile(sources, out, extra=()):
 
 
 def build_library() -> str:
-    return _compile([os.path.join(CSRC, f) for f in ("q4_kernels.hip", "q4_int8.hip", "q4_api.cpp")], LIB)
+    return _compile([os.path.join(CSRC, f) for f in ("q4_kernels.hip", "q4_int8.hip", "q4_moe.hip", "q4_api.cpp")], LIB)
 
 
 def build_probe() -> str:

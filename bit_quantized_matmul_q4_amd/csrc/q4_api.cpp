@@ -100,6 +100,16 @@ int check_int8(long long rows, long long N, long long K)
     return Q4_OK;
 }
 
+// Shapes of the expert layer: what its grids and 32-bit offsets hold.
+int check_moe(long long M, long long E, long long K, long long topk)
+{
+    if (M < 1 || E < 1 || topk < 1 || topk > E || K < 32 || K % 32 != 0)
+        return Q4_ERR_SHAPE;
+    if (M > Q4_MOE_MAX_ROWS || E > Q4_MOE_MAX_EXPERTS || K > (1LL << 17))
+        return Q4_ERR_SHAPE;
+    return Q4_OK;
+}
+
 // The launchers' element kinds.
 int elem_kind(int dtype) { return dtype == Q4_F32 ? 2 : dtype == Q4_BF16 ? 1 : 0; }
 
@@ -427,6 +437,67 @@ int q4_int8_linear(const void *x, int x_dtype, const float *x_scales, const void
     return hip_status(q4::launch_int8_linear(x, x_dtype == Q4_I8 ? -1 : elem_kind(x_dtype), x_scales,
                                              (const int8_t *)Wq, w_scales, y, elem_kind(y_dtype), M, N, K, workspace,
                                              (hipStream_t)stream));
+}
+
+size_t q4_moe_route_workspace_bytes(int M, int E)
+{
+    return check_moe(M, E, 32, 1) == Q4_OK ? q4::moe_route_workspace_bytes(M, E) : 0;
+}
+
+int q4_moe_route(const void *x, int x_dtype, const void *router, int router_dtype, const float *bias, int *ids,
+                 float *weights, int M, int E, int K, int topk, int renormalize, void *workspace,
+                 size_t workspace_bytes, void *stream)
+{
+    if (!x || !router || !ids || !weights)
+        return Q4_ERR_NULL;
+    if ((x_dtype != Q4_F16 && x_dtype != Q4_BF16) || (router_dtype != x_dtype && router_dtype != Q4_F32))
+        return Q4_ERR_ENUM;
+    const int sh = check_moe(M, E, K, topk);
+    if (sh != Q4_OK)
+        return sh;
+    if (!aligned(x, 16) || !aligned(router, 16) || !aligned(bias, 4) || !aligned(ids, 4) || !aligned(weights, 4))
+        return Q4_ERR_ALIGN;
+    if (workspace_bytes > 0 && !workspace)
+        return Q4_ERR_WORKSPACE;
+    if (workspace && !aligned(workspace, 256))
+        return Q4_ERR_ALIGN;
+    if (workspace_bytes < q4::moe_route_workspace_bytes(M, E))
+        return Q4_ERR_WORKSPACE;
+    return hip_status(q4::launch_moe_route(x, elem_kind(x_dtype), router, elem_kind(router_dtype), bias, ids, weights, M,
+                                           E, K, topk, renormalize != 0, workspace, (hipStream_t)stream));
+}
+
+size_t q4_moe_workspace_bytes(int M, int I, int topk)
+{
+    return check_moe(M, Q4_MOE_MAX_EXPERTS, I, topk) == Q4_OK ? q4::moe_workspace_bytes(M, I, topk) : 0;
+}
+
+int q4_moe_experts(const void *x, int x_dtype, const int *ids, const float *weights, const void *W13, const void *s13,
+                   const void *W2, const void *s2, float *y, int M, int E, int H, int I, int topk, void *workspace,
+                   size_t workspace_bytes, void *stream)
+{
+    if (!x || !ids || !weights || !W13 || !s13 || !W2 || !s2 || !y)
+        return Q4_ERR_NULL;
+    if (x_dtype != Q4_F16 && x_dtype != Q4_BF16)
+        return Q4_ERR_ENUM;
+    // (a row may name more experts than there are: ids repeat, or lie outside)
+    int sh = check_moe(M, E, H, 1);
+    if (sh == Q4_OK)
+        sh = check_moe(M, Q4_MOE_MAX_EXPERTS, I, topk);
+    if (sh != Q4_OK)
+        return sh;
+    if (!aligned(x, 16) || !aligned(ids, 4) || !aligned(weights, 4) || !aligned(W13, 16) || !aligned(s13, 8) ||
+        !aligned(W2, 16) || !aligned(s2, 8) || !aligned(y, 4))
+        return Q4_ERR_ALIGN;
+    if (workspace_bytes > 0 && !workspace)
+        return Q4_ERR_WORKSPACE;
+    if (workspace && !aligned(workspace, 256))
+        return Q4_ERR_ALIGN;
+    if (workspace_bytes < q4::moe_workspace_bytes(M, I, topk))
+        return Q4_ERR_WORKSPACE;
+    return hip_status(q4::launch_moe_experts(x, x_dtype == Q4_BF16, ids, weights, (const uint8_t *)W13,
+                                             (const uint16_t *)s13, (const uint8_t *)W2, (const uint16_t *)s2, y, M,
+                                             topk, E, H, I, workspace, (hipStream_t)stream));
 }
 
 }  // extern "C"

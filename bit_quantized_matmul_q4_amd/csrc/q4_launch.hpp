@@ -66,6 +66,16 @@ hipError_t launch_int8_linear(const void *x, int x_kind, const float *x_scales, 
                               void *y, int y_kind, int M, int N, int K, void *workspace, hipStream_t stream);
 size_t int8_workspace_bytes(bool dense, int M, int N, int K);
 
+// The expert layer (q4_moe.hip).
+hipError_t launch_moe_route(const void *x, int x_kind, const void *router, int r_kind, const float *bias, int *ids,
+                            float *weights, int M, int E, int K, int topk, int renormalize, void *workspace,
+                            hipStream_t stream);
+size_t moe_route_workspace_bytes(int M, int E);
+hipError_t launch_moe_experts(const void *x, bool bf16, const int *ids, const float *weights, const uint8_t *w13,
+                              const uint16_t *s13, const uint8_t *w2, const uint16_t *s2, float *y, int M, int topk,
+                              int E, int H, int I, void *workspace, hipStream_t stream);
+size_t moe_workspace_bytes(int M, int I, int topk);
+
 // Sizes of the tiled layout.
 size_t packed_code_bytes(int N, int K);
 size_t packed_scale_bytes(int N, int K);

@@ -281,6 +281,62 @@ size_t q4_int8_workspace_bytes(int M, int N, int K, int x_dtype); /* 0 for a bad
 int q4_int8_linear(const void *x, int x_dtype, const float *x_scales, const void *Wq, const float *w_scales, void *y,
                    int y_dtype, int M, int N, int K, void *workspace, size_t workspace_bytes, void *stream);
 
+/*
+ * A mixture-of-experts layer with 4-bit experts, at the row counts of decode:
+ * the router, then the products of each row's experts.  A row's results
+ * depend on that row and the weights alone (not on M, the row's place or the
+ * other rows' experts), as everywhere in this library.
+ *
+ * The router:
+ *     l[m][e] = sum_k x[m][k] router[e][k] (+ bias[e])
+ *     ids[m], weights[m]: the topk largest of softmax(l[m]), largest first,
+ *     equal ones by lower index; with renormalize != 0 the topk weights are
+ *     divided by their sum
+ * The logits are binary64 sums (the choice compares neighbours, so it must
+ * not depend on an order of rounding); the weights are binary32.  An expert
+ * whose logit is -infinity (a bias of -infinity) is never chosen: a slot that
+ * finds no other gets id -1 and weight 0.  A NaN logit counts as the largest
+ * and makes the row's weights NaN.
+ *   x        x_dtype Q4_BF16 or Q4_F16, [M][K], 16-byte aligned
+ *   router   [E][K], router_dtype x_dtype or Q4_F32, 16-byte aligned
+ *   bias     float32 [E], 4-byte aligned, or NULL
+ *   ids      int32 [M][topk];  weights  float32 [M][topk]
+ *   workspace at least q4_moe_route_workspace_bytes(M, E) bytes, as for
+ *            q4_int8_linear
+ * 1 <= topk <= E <= Q4_MOE_MAX_EXPERTS, M <= Q4_MOE_MAX_ROWS, K a multiple of
+ * 32, at most 2^17.
+ */
+#define Q4_MOE_MAX_EXPERTS 1024
+#define Q4_MOE_MAX_ROWS (1 << 20)
+size_t q4_moe_route_workspace_bytes(int M, int E); /* 0 for a bad shape */
+int q4_moe_route(const void *x, int x_dtype, const void *router, int router_dtype, const float *bias, int *ids,
+                 float *weights, int M, int E, int K, int topk, int renormalize, void *workspace,
+                 size_t workspace_bytes, void *stream);
+
+/*
+ * The experts:
+ *     [g | u] = x[m] . dequant(W13[e])^T     for e = ids[m][j]
+ *     h       = g / (1 + exp(-g)) u
+ *     y[m]    = sum_j weights[m][j] (h . dequant(W2[e])^T), in the order of j
+ * with binary32 sums throughout; h keeps 22 bits or more of the largest of
+ * each 32 values.  An id outside 0 .. E - 1 (-1, or an expert that another
+ * device holds) adds nothing; a row without experts gets zeros; an expert may
+ * appear twice in a row.
+ *   x        x_dtype Q4_BF16 or Q4_F16, [M][H], 16-byte aligned
+ *   ids      int32 [M][topk];  weights  float32 [M][topk]
+ *   W13, s13 packed form (q4_pack) of the experts' rows stacked, (2 E I) x H:
+ *            each expert's I gate rows, then its I up rows
+ *   W2, s2   packed form of (E H) x I
+ *   y        float32 [M][H], 4-byte aligned, overwritten
+ *   workspace at least q4_moe_workspace_bytes(M, I, topk) bytes, as above
+ * H and I are multiples of 32, at most 2^17; topk <= Q4_MOE_MAX_EXPERTS.  Made
+ * for few rows: past Q4_MOE_MAX_EXPERTS / topk rows the call runs in pieces.
+ */
+size_t q4_moe_workspace_bytes(int M, int I, int topk); /* 0 for a bad shape */
+int q4_moe_experts(const void *x, int x_dtype, const int *ids, const float *weights, const void *W13, const void *s13,
+                   const void *W2, const void *s2, float *y, int M, int E, int H, int I, int topk, void *workspace,
+                   size_t workspace_bytes, void *stream);
+
 /* Bytes of the packed codes and packed scales of an N x K matrix (0 for a
  * bad shape).  Pure host computation.  (Library layout; pages silent.) */
 size_t q4_packed_code_bytes(int N, int K);
