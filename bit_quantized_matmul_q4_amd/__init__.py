@@ -402,19 +402,7 @@ def linear_int8(x, w: Int8Matrix, out: torch.Tensor | None = None, out_dtype: to
     return out
 
 
-def moe_route(x: torch.Tensor, router: torch.Tensor, topk: int, bias: torch.Tensor | None = None,
-              renormalize: bool = True, workspace: torch.Tensor | bool | None = True):
-    """The topk experts of each row and their weights, by the largest of
-    softmax(x . router^T + bias): (ids int32 [M, topk], weights float32
-    [M, topk]), largest first, equal ones by lower index; the weights are
-    divided by their sum where ``renormalize``.
-
-    x: bfloat16 or float16 [M, K]; router: [E, K], x's dtype or float32; bias:
-    float32 [E] (-inf disables an expert; a slot without an expert gets id -1
-    and weight 0).  The logits are 64-bit sums, so a row's choice does not
-    depend on the batch (include/q4.h).
-    """
-    lib = _lib.load()
+def _need_route(x, router, topk, bias):
     _need(x, "x", (torch.bfloat16, torch.float16), 2)
     dev = x.device
     _need(router, "router", (x.dtype, torch.float32), 2, dev)
@@ -428,9 +416,56 @@ def moe_route(x: torch.Tensor, router: torch.Tensor, topk: int, bias: torch.Tens
             raise ValueError("bias must be [%d]" % E)
     if not 1 <= topk <= E:
         raise ValueError("topk=%d of %d experts" % (topk, E))
+    return M, K, E
+
+
+def _need_experts(x, w13, w2):
+    """(experts, I) of an expert layer's weights for x [M, H]."""
+    M, H = x.shape
+    for name, w in (("w13", w13), ("w2", w2)):
+        _need_q4(w, name, x.device)
+    I = w2.K
+    E = w2.N // H if H else 0
+    if w13.K != H or E < 1 or w2.N != E * H or w13.N != E * 2 * I:
+        raise ValueError("x [%d, %d] with w13 %d x %d and w2 %d x %d: w13 is (E 2 I) x H, w2 (E H) x I"
+                         % (M, H, w13.N, w13.K, w2.N, w2.K))
+    return E, I
+
+
+def _need_out(out, shape, dtypes, dev):
+    _need(out, "out", dtypes, 2, dev)
+    if tuple(out.shape) != shape:
+        raise ValueError("out must be [%d, %d]" % shape)
+
+
+def _need_q4(w, name: str, dev):
+    if not isinstance(w, Q4Weight):
+        raise TypeError("%s must be a Q4Weight (see pack)" % name)
+    _need(w.codes, name + ".codes", (torch.uint8,), 1, dev)
+    _need(w.scales, name + ".scales", (torch.float16,), 1, dev)
+    cb, sb = packed_sizes(w.N, w.K)
+    if w.codes.numel() != cb or w.scales.numel() * 2 != sb:
+        raise ValueError("packed %s sizes do not match N=%d K=%d" % (name, w.N, w.K))
+
+
+def moe_route(x: torch.Tensor, router: torch.Tensor, topk: int, bias: torch.Tensor | None = None,
+              renormalize: bool = True, workspace: torch.Tensor | bool | None = True):
+    """The topk experts of each row and their weights, by the largest of
+    softmax(x . router^T + bias): (ids int32 [M, topk], weights float32
+    [M, topk]), largest first, equal ones by lower index; the weights are
+    divided by their sum where ``renormalize``.
+
+    x: bfloat16 or float16 [M, K]; router: [E, K], x's dtype or float32; bias:
+    float32 [E] (-inf disables an expert; a slot without an expert gets id -1
+    and weight 0).  The logits are 64-bit sums, so a row's choice does not
+    depend on the batch (include/q4.h).
+    """
+    lib = _lib.load()
+    M, K, E = _need_route(x, router, topk, bias)
+    dev = x.device
     ids = torch.empty((M, topk), dtype=torch.int32, device=dev)
     weights = torch.empty((M, topk), dtype=torch.float32, device=dev)
-    _keep, ws_ptr, ws_len = _workspace(workspace, lib.q4_moe_route_workspace_bytes(M, E), dev)
+    _keep, ws_ptr, ws_len = _workspace(workspace, lib.q4_moe_route_workspace_bytes(M, E, K), dev)
     with torch.cuda.device(dev):
         st = lib.q4_moe_route(x.data_ptr(), _DTYPES[x.dtype], router.data_ptr(), _DTYPES[router.dtype],
                               None if bias is None else bias.data_ptr(), ids.data_ptr(), weights.data_ptr(), M, E, K,
@@ -459,26 +494,12 @@ def moe_experts(x: torch.Tensor, ids: torch.Tensor, weights: torch.Tensor, w13: 
     if ids.shape[0] != M or weights.shape != ids.shape:
         raise ValueError("ids and weights must be [%d, topk], got %s and %s"
                          % (M, tuple(ids.shape), tuple(weights.shape)))
-    for name, w in (("w13", w13), ("w2", w2)):
-        if not isinstance(w, Q4Weight):
-            raise TypeError("%s must be a Q4Weight (see pack)" % name)
-        _need(w.codes, name + ".codes", (torch.uint8,), 1, dev)
-        _need(w.scales, name + ".scales", (torch.float16,), 1, dev)
-        cb, sb = packed_sizes(w.N, w.K)
-        if w.codes.numel() != cb or w.scales.numel() * 2 != sb:
-            raise ValueError("packed %s sizes do not match N=%d K=%d" % (name, w.N, w.K))
-    I = w2.K
-    E = w2.N // H if H else 0
-    if w13.K != H or E < 1 or w2.N != E * H or w13.N != E * 2 * I:
-        raise ValueError("x [%d, %d] with w13 %d x %d and w2 %d x %d: w13 is (E 2 I) x H, w2 (E H) x I"
-                         % (M, H, w13.N, w13.K, w2.N, w2.K))
+    E, I = _need_experts(x, w13, w2)
     if out is None:
         out = torch.empty((M, H), dtype=torch.float32, device=dev)
     else:
-        _need(out, "out", (torch.float32,), 2, dev)
-        if tuple(out.shape) != (M, H):
-            raise ValueError("out must be [%d, %d]" % (M, H))
-    _keep, ws_ptr, ws_len = _workspace(workspace, lib.q4_moe_workspace_bytes(M, I, topk), dev)
+        _need_out(out, (M, H), (torch.float32,), dev)
+    _keep, ws_ptr, ws_len = _workspace(workspace, lib.q4_moe_experts_workspace_bytes(M, H, I, topk), dev)
     with torch.cuda.device(dev):
         st = lib.q4_moe_experts(x.data_ptr(), _DTYPES[x.dtype], ids.data_ptr(), weights.data_ptr(),
                                 w13.codes.data_ptr(), w13.scales.data_ptr(), w2.codes.data_ptr(),
@@ -488,10 +509,28 @@ def moe_experts(x: torch.Tensor, ids: torch.Tensor, weights: torch.Tensor, w13: 
 
 
 def moe(x: torch.Tensor, router: torch.Tensor, w13: Q4Weight, w2: Q4Weight, topk: int,
-        bias: torch.Tensor | None = None, renormalize: bool = True, out: torch.Tensor | None = None) -> torch.Tensor:
-    """The whole expert layer: ``moe_route`` and ``moe_experts``."""
-    ids, weights = moe_route(x, router, topk, bias, renormalize)
-    return moe_experts(x, ids, weights, w13, w2, out)
+        bias: torch.Tensor | None = None, renormalize: bool = True, out: torch.Tensor | None = None,
+        workspace: torch.Tensor | bool | None = True) -> torch.Tensor:
+    """The whole expert layer, ``moe_route`` and ``moe_experts`` in one call
+    (fewer launches, the same bits): float32 [M, H]."""
+    lib = _lib.load()
+    M, H, E = _need_route(x, router, topk, bias)
+    dev = x.device
+    experts, I = _need_experts(x, w13, w2)
+    if experts != E:
+        raise ValueError("the router has %d experts, the weights %d" % (E, experts))
+    if out is None:
+        out = torch.empty((M, H), dtype=torch.float32, device=dev)
+    else:
+        _need_out(out, (M, H), (torch.float32,), dev)
+    _keep, ws_ptr, ws_len = _workspace(workspace, lib.q4_moe_layer_workspace_bytes(M, E, H, I, topk), dev)
+    with torch.cuda.device(dev):
+        st = lib.q4_moe_layer(x.data_ptr(), _DTYPES[x.dtype], router.data_ptr(), _DTYPES[router.dtype],
+                              None if bias is None else bias.data_ptr(), w13.codes.data_ptr(), w13.scales.data_ptr(),
+                              w2.codes.data_ptr(), w2.scales.data_ptr(), out.data_ptr(), M, E, H, I, topk,
+                              int(renormalize), ws_ptr, ws_len, _stream(dev))
+    _lib.check(st, "q4_moe_layer")
+    return out
 
 
 def get_crossover() -> int:

@@ -37,7 +37,8 @@ EXPORTS = (
     "q4_linear", "q4_linear_f16", "q4_linear_ex", "q4_linear_noalloc", "q4_linear_grouped", "q4_workspace_bytes",
     "q4_pack", "q4_pack_nibbles", "q4_quantize",
     "q4_int8_packed_bytes", "q4_int8_quantize", "q4_int8_quantize_pack", "q4_int8_pack", "q4_int8_workspace_bytes",
-    "q4_int8_linear", "q4_moe_route", "q4_moe_route_workspace_bytes", "q4_moe_experts", "q4_moe_workspace_bytes",
+    "q4_int8_linear", "q4_moe_route", "q4_moe_route_workspace_bytes", "q4_moe_experts",
+    "q4_moe_experts_workspace_bytes", "q4_moe_layer", "q4_moe_layer_workspace_bytes",
     "q4_packed_code_bytes", "q4_packed_scale_bytes",
     "q4_get_crossover", "q4_set_crossover", "q4_segments", "q4_strerror",
     "q4_last_hip_error", "q4_abi_version",
@@ -104,12 +105,16 @@ def _declare(lib):
     lib.q4_int8_linear.restype = i
     lib.q4_moe_route.argtypes = [vp, i, vp, i, vp, vp, vp, i, i, i, i, i, vp, sz, vp]
     lib.q4_moe_route.restype = i
-    lib.q4_moe_route_workspace_bytes.argtypes = [i, i]
+    lib.q4_moe_route_workspace_bytes.argtypes = [i, i, i]
     lib.q4_moe_route_workspace_bytes.restype = sz
     lib.q4_moe_experts.argtypes = [vp, i, vp, vp, vp, vp, vp, vp, vp, i, i, i, i, i, vp, sz, vp]
     lib.q4_moe_experts.restype = i
-    lib.q4_moe_workspace_bytes.argtypes = [i, i, i]
-    lib.q4_moe_workspace_bytes.restype = sz
+    lib.q4_moe_experts_workspace_bytes.argtypes = [i, i, i, i]
+    lib.q4_moe_experts_workspace_bytes.restype = sz
+    lib.q4_moe_layer.argtypes = [vp, i, vp, i, vp, vp, vp, vp, vp, vp, i, i, i, i, i, i, vp, sz, vp]
+    lib.q4_moe_layer.restype = i
+    lib.q4_moe_layer_workspace_bytes.argtypes = [i, i, i, i, i]
+    lib.q4_moe_layer_workspace_bytes.restype = sz
     lib.q4_get_crossover.argtypes = []
     lib.q4_get_crossover.restype = i
     lib.q4_set_crossover.argtypes = [i]

@@ -439,9 +439,9 @@ int q4_int8_linear(const void *x, int x_dtype, const float *x_scales, const void
                                              (hipStream_t)stream));
 }
 
-size_t q4_moe_route_workspace_bytes(int M, int E)
+size_t q4_moe_route_workspace_bytes(int M, int E, int K)
 {
-    return check_moe(M, E, 32, 1) == Q4_OK ? q4::moe_route_workspace_bytes(M, E) : 0;
+    return check_moe(M, E, K, 1) == Q4_OK ? q4::moe_route_workspace_bytes(M, E, K) : 0;
 }
 
 int q4_moe_route(const void *x, int x_dtype, const void *router, int router_dtype, const float *bias, int *ids,
@@ -461,15 +461,22 @@ int q4_moe_route(const void *x, int x_dtype, const void *router, int router_dtyp
         return Q4_ERR_WORKSPACE;
     if (workspace && !aligned(workspace, 256))
         return Q4_ERR_ALIGN;
-    if (workspace_bytes < q4::moe_route_workspace_bytes(M, E))
+    if (workspace_bytes < q4::moe_route_workspace_bytes(M, E, K))
         return Q4_ERR_WORKSPACE;
     return hip_status(q4::launch_moe_route(x, elem_kind(x_dtype), router, elem_kind(router_dtype), bias, ids, weights, M,
                                            E, K, topk, renormalize != 0, workspace, (hipStream_t)stream));
 }
 
-size_t q4_moe_workspace_bytes(int M, int I, int topk)
+// (a row may name more experts than there are: ids repeat, or lie outside)
+static int check_experts(int M, int E, int H, int I, int topk)
 {
-    return check_moe(M, Q4_MOE_MAX_EXPERTS, I, topk) == Q4_OK ? q4::moe_workspace_bytes(M, I, topk) : 0;
+    const int sh = check_moe(M, E, H, 1);
+    return sh != Q4_OK ? sh : check_moe(M, Q4_MOE_MAX_EXPERTS, I, topk);
+}
+
+size_t q4_moe_experts_workspace_bytes(int M, int H, int I, int topk)
+{
+    return check_experts(M, 1, H, I, topk) == Q4_OK ? q4::moe_workspace_bytes(M, H, I, topk) : 0;
 }
 
 int q4_moe_experts(const void *x, int x_dtype, const int *ids, const float *weights, const void *W13, const void *s13,
@@ -480,10 +487,7 @@ int q4_moe_experts(const void *x, int x_dtype, const int *ids, const float *weig
         return Q4_ERR_NULL;
     if (x_dtype != Q4_F16 && x_dtype != Q4_BF16)
         return Q4_ERR_ENUM;
-    // (a row may name more experts than there are: ids repeat, or lie outside)
-    int sh = check_moe(M, E, H, 1);
-    if (sh == Q4_OK)
-        sh = check_moe(M, Q4_MOE_MAX_EXPERTS, I, topk);
+    const int sh = check_experts(M, E, H, I, topk);
     if (sh != Q4_OK)
         return sh;
     if (!aligned(x, 16) || !aligned(ids, 4) || !aligned(weights, 4) || !aligned(W13, 16) || !aligned(s13, 8) ||
@@ -493,11 +497,46 @@ int q4_moe_experts(const void *x, int x_dtype, const int *ids, const float *weig
         return Q4_ERR_WORKSPACE;
     if (workspace && !aligned(workspace, 256))
         return Q4_ERR_ALIGN;
-    if (workspace_bytes < q4::moe_workspace_bytes(M, I, topk))
+    if (workspace_bytes < q4::moe_workspace_bytes(M, H, I, topk))
         return Q4_ERR_WORKSPACE;
     return hip_status(q4::launch_moe_experts(x, x_dtype == Q4_BF16, ids, weights, (const uint8_t *)W13,
                                              (const uint16_t *)s13, (const uint8_t *)W2, (const uint16_t *)s2, y, M,
                                              topk, E, H, I, workspace, (hipStream_t)stream));
+}
+
+size_t q4_moe_layer_workspace_bytes(int M, int E, int H, int I, int topk)
+{
+    if (check_moe(M, E, H, topk) != Q4_OK || check_experts(M, E, H, I, topk) != Q4_OK)
+        return 0;
+    return q4::moe_layer_workspace_bytes(M, E, H, I, topk);
+}
+
+int q4_moe_layer(const void *x, int x_dtype, const void *router, int router_dtype, const float *bias, const void *W13,
+                 const void *s13, const void *W2, const void *s2, float *y, int M, int E, int H, int I, int topk,
+                 int renormalize, void *workspace, size_t workspace_bytes, void *stream)
+{
+    if (!x || !router || !W13 || !s13 || !W2 || !s2 || !y)
+        return Q4_ERR_NULL;
+    if ((x_dtype != Q4_F16 && x_dtype != Q4_BF16) || (router_dtype != x_dtype && router_dtype != Q4_F32))
+        return Q4_ERR_ENUM;
+    int sh = check_moe(M, E, H, topk);
+    if (sh == Q4_OK)
+        sh = check_experts(M, E, H, I, topk);
+    if (sh != Q4_OK)
+        return sh;
+    if (!aligned(x, 16) || !aligned(router, 16) || !aligned(bias, 4) || !aligned(W13, 16) || !aligned(s13, 8) ||
+        !aligned(W2, 16) || !aligned(s2, 8) || !aligned(y, 4))
+        return Q4_ERR_ALIGN;
+    if (workspace_bytes > 0 && !workspace)
+        return Q4_ERR_WORKSPACE;
+    if (workspace && !aligned(workspace, 256))
+        return Q4_ERR_ALIGN;
+    if (workspace_bytes < q4::moe_layer_workspace_bytes(M, E, H, I, topk))
+        return Q4_ERR_WORKSPACE;
+    return hip_status(q4::launch_moe_layer(x, elem_kind(x_dtype), router, elem_kind(router_dtype), bias,
+                                           (const uint8_t *)W13, (const uint16_t *)s13, (const uint8_t *)W2,
+                                           (const uint16_t *)s2, y, M, E, H, I, topk, renormalize != 0, workspace,
+                                           (hipStream_t)stream));
 }
 
 }  // extern "C"

@@ -70,11 +70,15 @@ size_t int8_workspace_bytes(bool dense, int M, int N, int K);
 hipError_t launch_moe_route(const void *x, int x_kind, const void *router, int r_kind, const float *bias, int *ids,
                             float *weights, int M, int E, int K, int topk, int renormalize, void *workspace,
                             hipStream_t stream);
-size_t moe_route_workspace_bytes(int M, int E);
+size_t moe_route_workspace_bytes(int M, int E, int K);
 hipError_t launch_moe_experts(const void *x, bool bf16, const int *ids, const float *weights, const uint8_t *w13,
                               const uint16_t *s13, const uint8_t *w2, const uint16_t *s2, float *y, int M, int topk,
                               int E, int H, int I, void *workspace, hipStream_t stream);
-size_t moe_workspace_bytes(int M, int I, int topk);
+size_t moe_workspace_bytes(int M, int H, int I, int topk);
+hipError_t launch_moe_layer(const void *x, int x_kind, const void *router, int r_kind, const float *bias,
+                            const uint8_t *w13, const uint16_t *s13, const uint8_t *w2, const uint16_t *s2, float *y,
+                            int M, int E, int H, int I, int topk, int renormalize, void *workspace, hipStream_t stream);
+size_t moe_layer_workspace_bytes(int M, int E, int H, int I, int topk);
 
 // Sizes of the tiled layout.
 size_t packed_code_bytes(int N, int K);

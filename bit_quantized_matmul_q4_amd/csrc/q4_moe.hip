@@ -13,9 +13,9 @@
 //
 // Operands.  The matrix cores take the codes as exact binary16 q - 8
 // (Dequant<false>).  bfloat16 x becomes binary16 after a power of two for
-// each row and segment that puts its largest value in [2^14, 2^15): exact for
-// every value down to 2^-31 of the largest, and off by at most 2^-40 of the
-// largest below that, which a 32-bit sum cannot hold either.  h is kept as
+// each row that puts its largest value in [2^14, 2^15): exact for every value
+// down to 2^-31 of the largest, and off by at most 2^-40 of the largest below
+// that, which a 32-bit sum beside the largest cannot hold either.  h is kept as
 // two binary16 numbers (the value and what its rounding left) after a power
 // of two for each 32 values, 22 bits or more of each block's largest.  All
 // sums are binary32.
@@ -38,7 +38,9 @@ constexpr int kExperts = 1024;  // most experts
 
 // ---------------------------------------------------------------- router
 // Sums in binary64 (v_mfma_f64_16x16x4): the choice compares neighbouring
-// logits, and 32-bit sums would let their order decide it.
+// logits, and 32-bit sums would let their order decide it.  The order is a
+// function of K alone: chains of 64 k, four of them added in order to a part
+// of 256 k, the parts added in order.
 // Element kinds: 0 binary16, 1 bfloat16, 2 binary32.  Eight values of a row.
 template <int KIND>
 struct Eight {
@@ -65,136 +67,33 @@ struct Eight {
     }
 };
 
-// grid = (16-expert tiles, 16-row tiles); the 16 waves take the chunks of 32 k
-// in turn, and their sums are added in wave order.  Lane (g, c) holds expert
-// c's (A) and row c's (B) values k = 32 s + 8 g + i of step i.
+constexpr int kPart = 256;  // k of a part
+
+// The chain of the 64 k from k0 on (short at the end of the row): lane (g, c)
+// holds expert c's (A) and row c's (B) values k = 32 s + 8 g + i of step i.
 template <int XK, int RK>
-__global__ __launch_bounds__(1024) void q4_moe_logits_kernel(const uint16_t *__restrict__ x,
-                                                             const void *__restrict__ router,
-                                                             const float *__restrict__ bias,
-                                                             double *__restrict__ logits, int M, int E, int K)
+__device__ __forceinline__ f64x4 logit_chain(const uint16_t *xr, const uint8_t *rr, int k0, int K, int g)
 {
-    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, c = lane & 15, g = lane >> 4;
-    const int e = min((int)blockIdx.x * 16 + c, E - 1), m = min((int)blockIdx.y * 16 + c, M - 1);
-    const uint16_t *xr = x + (size_t)m * K;
-    const uint8_t *rr = (const uint8_t *)router + (size_t)e * K * (RK == 2 ? 4 : 2);
     f64x4 acc = {0, 0, 0, 0};
-    for (int s = wave; s < K / 32; s += 16) {
-        Eight<XK> a;
-        Eight<RK> b;
-        a.load(xr, 32 * (size_t)s + 8 * g);
-        b.load(rr, 32 * (size_t)s + 8 * g);
+    Eight<XK> a[2];
+    Eight<RK> b[2];
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-            acc = __builtin_amdgcn_mfma_f64_16x16x4f64(b.at(i), a.at(i), acc, 0, 0, 0);
-    }
-    __shared__ double part[16][4][64];
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-        part[wave][i][lane] = acc[i];
-    __syncthreads();
-    if (wave >= 4)
-        return;
-    double s = part[0][wave][lane];
-#pragma unroll
-    for (int w = 1; w < 16; ++w)
-        s += part[w][wave][lane];
-    // component i of lane (g, c): expert 4 i + g of the tile, row c
-    const int oe = blockIdx.x * 16 + 4 * wave + g, om = blockIdx.y * 16 + c;
-    if (oe < E && om < M)
-        logits[(size_t)om * E + oe] = s + (bias ? (double)bias[oe] : 0.0);
-}
-
-// One wave a row: every expert's rank is the number of experts before it (a
-// larger logit, or the same at a lower index; NaN counts as the largest), and
-// the first topk ranks are the choice.
-__global__ __launch_bounds__(256) void q4_moe_select_kernel(const double *__restrict__ logits, int *__restrict__ ids,
-                                                            float *__restrict__ weights, int E, int topk,
-                                                            int renormalize)
-{
-    extern __shared__ double row[];  // E keys, then topk chosen logits
-    double *chosen = row + E;
-    const int m = blockIdx.x;
-    const double *l = logits + (size_t)m * E;
-    for (int e = threadIdx.x; e < E; e += 256)
-        row[e] = l[e];
-    __syncthreads();
-    for (int e = threadIdx.x; e < E; e += 256) {
-        const double v = row[e], key = v != v ? __builtin_inf() : v;
-        int rank = 0;
-        for (int f = 0; f < E; ++f) {
-            const double u = row[f], k = u != u ? __builtin_inf() : u;
-            rank += (k > key || (k == key && f < e)) ? 1 : 0;
+    for (int s = 0; s < 2; ++s)
+        if (k0 + 32 * s < K) {
+            a[s].load(xr, k0 + 32 * s + 8 * g);
+            b[s].load(rr, k0 + 32 * s + 8 * g);
         }
-        if (rank < topk) {
-            chosen[rank] = v;
-            ids[(size_t)m * topk + rank] = v == -__builtin_inf() ? -1 : e;
-        }
-    }
-    __syncthreads();
-    if (threadIdx.x >= 64)
-        return;
-    const double top = chosen[0];
-    // softmax over all experts, or over the chosen ones
-    float sum = 0.f;
-    const int n = renormalize ? topk : E;
-    for (int i = threadIdx.x; i < n; i += 64) {
-        const double v = renormalize ? chosen[i] : row[i];
-        sum += v == -__builtin_inf() ? 0.f : __builtin_expf((float)(v - top));
-    }
 #pragma unroll
-    for (int d = 1; d < 64; d *= 2)
-        sum += __shfl_xor(sum, d);
-    for (int i = threadIdx.x; i < topk; i += 64) {
-        const double v = chosen[i];
-        weights[(size_t)m * topk + i] = v == -__builtin_inf() ? 0.f : __builtin_expf((float)(v - top)) / sum;
-    }
+    for (int s = 0; s < 2; ++s)
+        if (k0 + 32 * s < K) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                acc = __builtin_amdgcn_mfma_f64_16x16x4f64(b[s].at(i), a[s].at(i), acc, 0, 0, 0);
+        }
+    return acc;
 }
 
-// -------------------------------------------------------- expert products
-// Row slots: batch row i of a group of 4 R rows sits, for block j of a quad,
-// in the operand and A row slot that `Slots<R>` gives; its value of block j
-// then lands in component comp(j, r) of lane group i % 4 with r = i / 4 (the
-// layout of gemv_quad_slots and gemv_quad_slots2).
-template <int R>
-struct Slots;
-template <>
-struct Slots<1> {
-    static __device__ __forceinline__ int row(int c) { return c >> 2; }
-    static __device__ __forceinline__ int block(int, int c) { return c & 3; }
-    static __device__ __forceinline__ constexpr int operand(int) { return 0; }
-    static __device__ __forceinline__ constexpr int comp(int j, int) { return j; }
-};
-template <>
-struct Slots<2> {
-    static __device__ __forceinline__ int row(int c) { return (c >> 2) + 4 * (c & 1); }
-    static __device__ __forceinline__ int block(int o, int c) { return 2 * o + ((c & 3) >> 1); }
-    static __device__ __forceinline__ constexpr int operand(int j) { return j >> 1; }
-    static __device__ __forceinline__ constexpr int comp(int j, int r) { return 2 * (j & 1) + r; }
-};
-template <>
-struct Slots<4> {
-    static __device__ __forceinline__ int row(int c) { return (c >> 2) + 4 * (c & 3); }
-    static __device__ __forceinline__ int block(int o, int) { return o; }
-    static __device__ __forceinline__ constexpr int operand(int j) { return j; }
-    static __device__ __forceinline__ constexpr int comp(int, int r) { return r; }
-};
-
-__device__ __forceinline__ u32x4 load_codes(const uint8_t *p)
-{
-    return __builtin_nontemporal_load((const u32x4 *)p);
-}
-__device__ __forceinline__ u32x2 load_scales(const uint16_t *p)
-{
-    return __builtin_nontemporal_load((const u32x2 *)p);
-}
-__device__ __forceinline__ float quad_scale(u32x2 s, int j)
-{
-    return half_bits_to_float((j < 2 ? s.x : s.y) >> (16 * (j & 1)) & 0xFFFFu);
-}
-
-__device__ __forceinline__ f32x4 dot16(u32x4 a, u32x4 b, f32x4 c) { return blockdot_acc<false>(a, b, c); }
-
+// ------------------------------------------------------ x as binary16
 // Exponent shift that puts a largest magnitude `top` in [2^14, 2^15), or 0 for
 // zeros.
 __device__ __forceinline__ int lift_of(float top)
@@ -229,222 +128,739 @@ __device__ __forceinline__ float largest(u32x4 v, float top)
     return top;
 }
 
-// The rows (slots) that chose expert e, in order, by one wave: -> count.
-__device__ __forceinline__ int rows_of(const int *ids, int n, int e, uint16_t *list)
+// One row of bfloat16 x by one wave: x16 and its lift.
+__device__ __forceinline__ void lift_row(const uint16_t *x, uint16_t *x16, int *lift, int K)
 {
     const int lane = threadIdx.x & 63;
-    int count = 0;
-    for (int s0 = 0; s0 < n; s0 += 64) {
-        const bool hit = s0 + lane < n && ids[s0 + lane] == e;
-        const uint64_t mask = __ballot(hit);
-        if (hit)
-            list[count + __popcll(mask & ((1ull << lane) - 1))] = (uint16_t)(s0 + lane);
-        count += __popcll(mask);
-    }
-    return count;
+    constexpr int HELD = 4;  // rows up to 2048 long are read once
+    u32x4 v[HELD];
+    float top = 0.f;
+#pragma unroll
+    for (int i = 0; i < HELD; ++i)
+        if (8 * (lane + 64 * i) < K)
+            v[i] = *(const u32x4 *)(x + 8 * (lane + 64 * i));
+#pragma unroll
+    for (int i = 0; i < HELD; ++i)
+        if (8 * (lane + 64 * i) < K)
+            top = largest(v[i], top);
+    for (int k = 8 * (lane + 64 * HELD); k < K; k += 512)
+        top = largest(*(const u32x4 *)(x + k), top);
+#pragma unroll
+    for (int d = 1; d < 64; d *= 2)
+        top = __builtin_fmaxf(top, __shfl_xor(top, d));
+    const int up = lift_of(top);
+#pragma unroll
+    for (int i = 0; i < HELD; ++i)
+        if (8 * (lane + 64 * i) < K)
+            *(u32x4 *)(x16 + 8 * (lane + 64 * i)) = lifted(v[i], up);
+    for (int k = 8 * (lane + 64 * HELD); k < K; k += 512)
+        *(u32x4 *)(x16 + k) = lifted(*(const u32x4 *)(x + k), up);
+    if (lane == 0)
+        *lift = up;
 }
 
-// gate and up.  grid = (I / 32, experts that can be chosen); wave j of a
-// workgroup takes segment j of H for two tiles of gate and two of up, so the
-// workgroup ends with 32 values of h, one block of the down product.
-template <bool BF16, int R>
-__global__ __launch_bounds__(1024) void q4_moe_up_kernel(const uint16_t *__restrict__ x, const int *__restrict__ ids,
-                                                         const uint8_t *__restrict__ wq,
-                                                         const uint16_t *__restrict__ scales, uint16_t *__restrict__ hi,
-                                                         uint16_t *__restrict__ lo, int *__restrict__ shift, int n,
-                                                         int topk, int E, int H, int I, Plan plan)
+__global__ __launch_bounds__(256) void q4_moe_lift_kernel(const uint16_t *__restrict__ x, uint16_t *__restrict__ x16,
+                                                          int *__restrict__ lift, int M, int K)
 {
-    extern __shared__ __attribute__((aligned(16))) float part[];  // [segment][tile][r][lane]
-    __shared__ uint32_t seen[kExperts / 32];
-    __shared__ uint16_t list[kSlots];
-    __shared__ int found[2];  // the expert, its rows
+    const int m = blockIdx.x * 4 + (threadIdx.x >> 6);
+    if (m < M)
+        lift_row(x + (size_t)m * K, x16 + (size_t)m * K, lift + m, K);
+}
+
+// Few rows: grid = (16-expert tiles, 16-row tiles, parts), a wave a chain; the
+// reader adds the parts.  One more z takes the rows to binary16 (x16 given).
+template <int XK, int RK>
+__global__ __launch_bounds__(256) void q4_moe_logits_kernel(const uint16_t *__restrict__ x,
+                                                            const void *__restrict__ router,
+                                                            double *__restrict__ parts, uint16_t *__restrict__ x16,
+                                                            int *__restrict__ lift, int M, int E, int K)
+{
     const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, c = lane & 15, g = lane >> 4;
-    if (wave == 0) {
-        // the blockIdx.y-th of the chosen experts
-        if (lane < kExperts / 32)
-            seen[lane] = 0;
-        __builtin_amdgcn_wave_barrier();
-        for (int s = lane; s < n; s += 64) {
-            const int e = ids[s];
-            if (e >= 0 && e < E)
-                atomicOr(&seen[e >> 5], 1u << (e & 31));
-        }
-        __builtin_amdgcn_wave_barrier();
-        __threadfence_block();
-        uint32_t bits = lane < kExperts / 32 ? ((volatile uint32_t *)seen)[lane] : 0;
-        const int mine = __popc(bits);
-        int before = mine;
+    const int part = blockIdx.z;
+    if (part * kPart >= K) {
+        const int all = gridDim.x * gridDim.y * 4;
+        for (int m = (blockIdx.y * gridDim.x + blockIdx.x) * 4 + wave; m < M; m += all)
+            lift_row(x + (size_t)m * K, x16 + (size_t)m * K, lift + m, K);
+        return;
+    }
+    const int e = min((int)blockIdx.x * 16 + c, E - 1), m = min((int)blockIdx.y * 16 + c, M - 1);
+    const f64x4 acc = logit_chain<XK, RK>(x + (size_t)m * K,
+                                          (const uint8_t *)router + (size_t)e * K * (RK == 2 ? 4 : 2),
+                                          part * kPart + 64 * wave, K, g);
+    __shared__ double chain[4][4][64];
 #pragma unroll
-        for (int d = 1; d < 32; d *= 2) {
-            const int v = __shfl_up(before, d);
-            if (lane >= d)
-                before += v;
+    for (int i = 0; i < 4; ++i)
+        chain[wave][i][lane] = acc[i];
+    __syncthreads();
+    const double s = ((chain[0][wave][lane] + chain[1][wave][lane]) + chain[2][wave][lane]) + chain[3][wave][lane];
+    // component i of lane (g, c): expert 4 i + g of the tile, row c
+    const int oe = blockIdx.x * 16 + 4 * wave + g, om = blockIdx.y * 16 + c;
+    if (oe < E && om < M)
+        parts[((size_t)part * M + om) * E + oe] = s;
+}
+
+// Many rows: a wave owns 16 experts by 16 rows over all of K, the same sums.
+template <int XK, int RK>
+__global__ __launch_bounds__(256) void q4_moe_logits_rows_kernel(const uint16_t *__restrict__ x,
+                                                                 const void *__restrict__ router,
+                                                                 double *__restrict__ logits, int M, int E, int K)
+{
+    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, c = lane & 15, g = lane >> 4;
+    const int et = blockIdx.x, mt = blockIdx.y * 4 + wave;
+    if (mt * 16 >= M)
+        return;
+    const int e = min(et * 16 + c, E - 1), m = min(mt * 16 + c, M - 1);
+    const uint16_t *xr = x + (size_t)m * K;
+    const uint8_t *rr = (const uint8_t *)router + (size_t)e * K * (RK == 2 ? 4 : 2);
+    f64x4 sum = {0, 0, 0, 0};
+    for (int k = 0; k < K; k += kPart) {
+        f64x4 p = logit_chain<XK, RK>(xr, rr, k, K, g);
+#pragma unroll
+        for (int w = 1; w < 4; ++w)
+            p += logit_chain<XK, RK>(xr, rr, k + 64 * w, K, g);
+        sum = k ? sum + p : p;
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int oe = et * 16 + 4 * i + g, om = mt * 16 + c;
+        if (oe < E && om < M)
+            logits[(size_t)om * E + oe] = sum[i];
+    }
+}
+
+// A logit as an integer of the same order, NaN above everything.
+__device__ __forceinline__ uint64_t order_key(double v)
+{
+    const uint64_t b = __builtin_bit_cast(uint64_t, v);
+    if (v != v)
+        return ~0ull;
+    return b >> 63 ? ~b : b | 1ull << 63;
+}
+__device__ __forceinline__ double key_value(uint64_t k)
+{
+    if (k == ~0ull)
+        return __builtin_nan("");
+    return __builtin_bit_cast(double, k >> 63 ? k ^ (1ull << 63) : ~k);
+}
+
+// What a workgroup needs to choose its rows' experts from the logits' parts.
+struct Choice {
+    const double *parts;  // [count][M][E]
+    const float *bias;    // or null
+    int count, M, E, topk, renormalize;
+};
+
+// Rows m0 .. m0 + rows - 1 by a workgroup: every expert's rank in its row is the
+// number of experts before it (a larger logit, or an equal one at a lower
+// index), spread over as many threads as there are; the first topk ranks are
+// the choice.  keys: rows E numbers of LDS; chosen: rows topk.  ids goes to
+// LDS (ids_out + row topk) and, as the weights, to memory where asked.
+template <typename ID>
+__device__ __forceinline__ void choose_rows(const Choice &ch, int m0, int rows, uint64_t *keys, double *chosen,
+                                            ID *ids_lds, int *ids, float *weights, bool out)
+{
+    const int tid = threadIdx.x, T = blockDim.x, E = ch.E, topk = ch.topk;
+    const int pairs = rows * E;
+    for (int p = tid; p < pairs; p += T) {
+        const double *at = ch.parts + (size_t)m0 * E + p;
+        const size_t step = (size_t)ch.M * E;
+        double l = 0.0;  // (0 + the first part: that part, but for the sign of a zero)
+        for (int i0 = 0; i0 < ch.count; i0 += 8) {
+            double v[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                v[i] = i0 + i < ch.count ? at[(i0 + i) * step] : 0.0;
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                l += v[i];
         }
-        before -= mine;
-        int left = (int)blockIdx.y - before;
-        if (lane == 0)
-            found[0] = -1;
-        __builtin_amdgcn_wave_barrier();
-        if (lane < kExperts / 32 && left >= 0 && left < mine) {
-            for (; left > 0; --left)
-                bits &= bits - 1;
-            found[0] = 32 * lane + __ffs(bits) - 1;
-        }
-        __builtin_amdgcn_wave_barrier();
-        __threadfence_block();
-        const int e = ((volatile int *)found)[0];
-        const int count = e < 0 ? 0 : rows_of(ids, n, e, list);
-        if (lane == 0)
-            found[1] = count;
+        if (ch.bias)
+            l += (double)ch.bias[p % E];
+        keys[p] = order_key(l);
     }
     __syncthreads();
-    const int e = found[0], count = found[1];
-    if (e < 0)
-        return;
-    const int S = plan.S;
-    const int qa = seg_first_block(plan, wave) / 4, qb = (seg_end_block(plan, wave) + 3) / 4;
-    const Dequant<false> dq;
-    // tiles: gate 2 t, gate 2 t + 1, up 2 t, up 2 t + 1 of the expert
-    const size_t tile0 = (size_t)e * (2 * I / 16) + 2 * blockIdx.x;
-    const uint8_t *w[4];
-    const uint16_t *ws[4];
-#pragma unroll
-    for (int t = 0; t < 4; ++t) {
-        const size_t tile = tile0 + (t & 1) + (t >> 1) * (I / 16);
-        w[t] = wq + tile * plan.G * 1024 + lane * 16;
-        ws[t] = scales + tile * plan.G * 64 + c * 4;
-    }
-    for (int r0 = 0; r0 < count; r0 += 4 * R) {
-        const int row = r0 + Slots<R>::row(c);
-        const bool live = row < count;
-        const uint16_t *xr = x + (size_t)(live ? list[row] / topk : 0) * H + 8 * g;
-        auto load_x = [&](int o, int q) -> u32x4 {
-            const int b = 4 * q + Slots<R>::block(o, c);
-            if (live && b < plan.nb)
-                return *(const u32x4 *)(xr + 32 * b);
-            return (u32x4){0, 0, 0, 0};
-        };
-        int lift = 0;
-        int back[R];
-        if constexpr (BF16) {
-            float top = 0.f;
-            for (int q = qa; q < qb; ++q)
-#pragma unroll
-                for (int o = 0; o < R; ++o)
-                    top = largest(load_x(o, q), top);
-            // over the lanes that hold the same row: all four g, and the
-            // slots of the row
-            top = __builtin_fmaxf(top, __shfl_xor(top, 16));
-            top = __builtin_fmaxf(top, __shfl_xor(top, 32));
-            if constexpr (R == 1)
-                top = __builtin_fmaxf(top, __shfl_xor(top, 1));
-            if constexpr (R <= 2)
-                top = __builtin_fmaxf(top, __shfl_xor(top, 2));
-            lift = lift_of(top);
-            // lane group g's rows are 4 r + g: slot 4 g + r holds row 4 r + g
-#pragma unroll
-            for (int r = 0; r < R; ++r)
-                back[r] = __shfl(lift, 4 * g + r);
+    int share = 1;  // threads a pair
+    while (2 * share * pairs <= T && share < 64)
+        share *= 2;
+    const int at = tid % share;
+    for (int p = tid / share; p < pairs; p += T / share) {
+        const int row = p / E, e = p - row * E;
+        const uint64_t key = keys[p], *k = keys + row * E;
+        int rank = 0;
+        for (int f = at; f < E; f += share) {
+            const uint64_t o = k[f];
+            rank += (o > key) | ((o == key) & (f < e));
         }
-        float p[4][R];
+        for (int d = 1; d < share; d *= 2)
+            rank += __shfl_xor(rank, d);
+        if (at == 0 && rank < topk) {
+            const double v = key_value(key);
+            chosen[row * topk + rank] = v;
+            const int id = v == -__builtin_inf() ? -1 : e;
+            if (ids_lds)
+                ids_lds[row * topk + rank] = (ID)id;
+            if (out)
+                ids[(size_t)(m0 + row) * topk + rank] = id;
+        }
+    }
+    __syncthreads();
+    if (!out)
+        return;
+    // softmax over all experts, or over the chosen ones: a wave a row
+    const int lane = tid & 63;
+    for (int row = tid >> 6; row < rows; row += T >> 6) {
+        const double *c = chosen + row * topk;
+        const double top = c[0];
+        float sum = 0.f;
+        const int n = ch.renormalize ? topk : E;
+        for (int i = lane; i < n; i += 64) {
+            const double v = ch.renormalize ? c[i] : key_value(keys[row * E + i]);
+            sum += v == -__builtin_inf() ? 0.f : __builtin_expf((float)(v - top));
+        }
 #pragma unroll
-        for (int t = 0; t < 4; ++t)
-#pragma unroll
-            for (int r = 0; r < R; ++r)
-                p[t][r] = 0.f;
-        for (int q = qa; q < qb; ++q) {
-            u32x4 a[R], codes[4];
-            u32x2 sc[4];
-#pragma unroll
-            for (int t = 0; t < 4; ++t) {
-                codes[t] = load_codes(w[t] + (size_t)q * 1024);
-                sc[t] = load_scales(ws[t] + (size_t)q * 64);
+        for (int d = 1; d < 64; d *= 2)
+            sum += __shfl_xor(sum, d);
+        for (int i = lane; i < topk; i += 64) {
+            const double v = c[i];
+            weights[(size_t)(m0 + row) * topk + i] =
+                v == -__builtin_inf() ? 0.f : __builtin_expf((float)(v - top)) / sum;
+        }
+    }
+}
+
+// A workgroup a row; with x16, the last wave takes the row to binary16 first.
+__global__ __launch_bounds__(256) void q4_moe_select_kernel(Choice ch, int *__restrict__ ids,
+                                                            float *__restrict__ weights,
+                                                            const uint16_t *__restrict__ x,
+                                                            uint16_t *__restrict__ x16, int *__restrict__ lift, int K)
+{
+    extern __shared__ double row[];  // E keys, then topk chosen logits
+    const size_t m = blockIdx.x;
+    if (x16 && threadIdx.x >= 192)
+        lift_row(x + m * K, x16 + m * K, lift + m, K);
+    choose_rows<int>(ch, (int)m, 1, (uint64_t *)row, row + ch.E, nullptr, ids, weights, true);
+}
+
+// -------------------------------------------------------- expert products
+// Row slots: batch row i of a group of 4 R rows sits, for block j of a quad,
+// in the operand and A row slot that `Slots<R>` gives; its value of block j
+// then lands in component comp(j, r) of lane group i % 4 with r = i / 4 (the
+// layout of gemv_quad_slots and gemv_quad_slots2).
+template <int R>
+struct Slots;
+template <>
+struct Slots<1> {
+    static __device__ __forceinline__ int row(int c) { return c >> 2; }
+    static __device__ __forceinline__ int block(int, int c) { return c & 3; }
+    static __device__ __forceinline__ constexpr int operand(int) { return 0; }
+    static __device__ __forceinline__ constexpr int comp(int j, int) { return j; }
+};
+template <>
+struct Slots<2> {
+    static __device__ __forceinline__ int row(int c) { return (c >> 2) + 4 * (c & 1); }
+    static __device__ __forceinline__ int block(int o, int c) { return 2 * o + ((c & 3) >> 1); }
+    static __device__ __forceinline__ constexpr int operand(int j) { return j >> 1; }
+    static __device__ __forceinline__ constexpr int comp(int j, int r) { return 2 * (j & 1) + r; }
+};
+template <>
+struct Slots<4> {
+    static __device__ __forceinline__ int row(int c) { return (c >> 2) + 4 * (c & 3); }
+    static __device__ __forceinline__ int block(int o, int) { return o; }
+    static __device__ __forceinline__ constexpr int operand(int j) { return j; }
+    static __device__ __forceinline__ constexpr int comp(int, int r) { return r; }
+};
+
+// Buffer loads: a wave-uniform base with the range of what may be read, a
+// lane's own 32-bit offset and a uniform one, so that a stream costs one
+// register a lane.  An offset of kNowhere is past every range (they stay
+// below 2^29 bytes, the uniform offsets too): it reads zero.
+constexpr uint32_t kNowhere = 1u << 31;
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_of(const void *base, size_t bytes)
+{
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(base), (short)0, (int)bytes, 0x00020000);
+}
+__device__ __forceinline__ u32x4 load16(__amdgpu_buffer_rsrc_t b, uint32_t at, uint32_t uniform)
+{
+    return __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(b, at, uniform, 0));
+}
+// Codes and scales are read once a call: the non-temporal hint, as in the
+// 4-bit product's kernels.
+__device__ __forceinline__ u32x4 load_codes(__amdgpu_buffer_rsrc_t b, uint32_t at, int q)
+{
+    return __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(b, at, 1024 * q, 2));
+}
+__device__ __forceinline__ u32x2 load_scales(__amdgpu_buffer_rsrc_t b, uint32_t at, int q)
+{
+    return __builtin_bit_cast(u32x2, __builtin_amdgcn_raw_buffer_load_b64(b, at, 128 * q, 2));
+}
+// A tile of 16 columns: its codes and scales over all of K.
+struct Tile {
+    __amdgpu_buffer_rsrc_t w, s;
+    Tile() = default;
+    __device__ __forceinline__ Tile(const uint8_t *wq, const uint16_t *scales, size_t tile, int G)
+        : w(buffer_of(wq + tile * G * 1024, (size_t)G * 1024)), s(buffer_of(scales + tile * G * 64, (size_t)G * 128))
+    {
+    }
+};
+__device__ __forceinline__ float quad_scale(u32x2 s, int j)
+{
+    return half_bits_to_float((j < 2 ? s.x : s.y) >> (16 * (j & 1)) & 0xFFFFu);
+}
+
+__device__ __forceinline__ f32x4 dot16(u32x4 a, u32x4 b, f32x4 c) { return blockdot_acc<false>(a, b, c); }
+
+// Up to kFused compares of two logits the gate/up kernel chooses the experts
+// itself, so that the layer is three launches: every workgroup ranks all rows,
+// and the first writes the choice for the down kernel.
+constexpr int kFused = 16384;
+
+// The blockIdx.y-th of the chosen experts, and its slots in `list` -> their
+// count, or -1 if fewer experts are chosen.  By the whole workgroup.  Up to 64
+// slots every wave finds them alone (experts in the order of their first
+// slot, all waves writing the same list), so that its loads start at once;
+// more go through a bitmap in LDS (in the order of their numbers).
+struct Found {
+    uint32_t seen[kExperts / 32];
+    uint16_t list[kSlots];
+    int16_t who[kSlots];  // the slots' experts, -1 for none
+    int count;
+};
+
+__device__ __forceinline__ int slot_expert(int id, int E) { return id >= 0 && id < E ? id : -1; }
+
+template <typename START>
+__device__ __forceinline__ int find_expert(Found &f, int n, const int *ids, bool known, int E, int nth, START start)
+{
+    const int tid = threadIdx.x, lane = tid & 63;
+    if (n <= 64) {
+        const int id = lane < n ? (known ? (int)f.who[lane] : slot_expert(ids[lane], E)) : -1;
+        uint64_t left = __ballot(id >= 0), mine = 0;
+        int e = -1;
+        for (int i = 0; left; ++i) {
+            const int v = __builtin_amdgcn_readlane(id, __builtin_ctzll(left));
+            const uint64_t same = __ballot(id == v);
+            if (i == nth) {
+                e = v;
+                mine = same;
+                break;
             }
+            left &= ~same;
+        }
+        if (e < 0)
+            return -1;
+        start(e);
+        if (mine >> lane & 1)
+            f.list[__popcll(mine & ((1ull << lane) - 1))] = (uint16_t)lane;
+        __threadfence_block();
+        return __popcll(mine);
+    }
+    if (tid < kExperts / 32)
+        f.seen[tid] = 0;
+    if (!known)
+        for (int s = tid; s < n; s += blockDim.x)
+            f.who[s] = (int16_t)slot_expert(ids[s], E);
+    __syncthreads();
+    for (int s = tid; s < n; s += blockDim.x)
+        if (f.who[s] >= 0)
+            atomicOr(&f.seen[f.who[s] >> 5], 1u << (f.who[s] & 31));
+    __syncthreads();
+    uint32_t bits = lane < kExperts / 32 ? f.seen[lane] : 0;
+    const int mine = __popc(bits);
+    int before = mine;
 #pragma unroll
-            for (int o = 0; o < R; ++o) {
-                a[o] = load_x(o, q);
-                if constexpr (BF16)
-                    a[o] = lifted(a[o], lift);
+    for (int d = 1; d < 32; d *= 2) {
+        const int v = __shfl_up(before, d);
+        if (lane >= d)
+            before += v;
+    }
+    int left = nth - (before - mine);
+    const bool here = lane < kExperts / 32 && left >= 0 && left < mine;
+    const uint64_t owner = __ballot(here);
+    if (!owner)
+        return -1;
+    if (here)
+        for (; left > 0; --left)
+            bits &= bits - 1;
+    const int e = __builtin_amdgcn_readlane(32 * lane + __ffs(bits) - 1, __builtin_ctzll(owner));
+    start(e);
+    if (tid < 64) {
+        int count = 0;
+        for (int s0 = 0; s0 < n; s0 += 64) {
+            const bool hit = s0 + lane < n && f.who[s0 + lane] == e;
+            const uint64_t mask = __ballot(hit);
+            if (hit)
+                f.list[count + __popcll(mask & ((1ull << lane) - 1))] = (uint16_t)(s0 + lane);
+            count += __popcll(mask);
+        }
+        if (lane == 0)
+            f.count = count;
+    }
+    __syncthreads();
+    return __builtin_amdgcn_readfirstlane(f.count);
+}
+
+// What a workgroup multiplies: four tiles of 16 columns of one expert's weight
+// (the quads of K are the waves' runs of L segments).
+struct FourTiles {
+    Tile t0, t1, t2, t3;
+};
+struct Weights {
+    u32x4 codes[4];
+    u32x2 scales[4];
+    __device__ __forceinline__ void load(const FourTiles &f, int q)
+    {
+        const uint32_t lane = threadIdx.x & 63, w_at = 16 * lane, s_at = 8 * (lane & 15);
+        codes[0] = load_codes(f.t0.w, w_at, q);
+        codes[1] = load_codes(f.t1.w, w_at, q);
+        codes[2] = load_codes(f.t2.w, w_at, q);
+        codes[3] = load_codes(f.t3.w, w_at, q);
+        scales[0] = load_scales(f.t0.s, s_at, q);
+        scales[1] = load_scales(f.t1.s, s_at, q);
+        scales[2] = load_scales(f.t2.s, s_at, q);
+        scales[3] = load_scales(f.t3.s, s_at, q);
+    }
+};
+
+// The rows' operands of one quad: x as it is.
+template <int R>
+struct RowsX {
+    u32x4 x[R];
+    struct In {
+        __amdgpu_buffer_rsrc_t x;
+        uint32_t at;
+        int nb;
+    };
+    static __device__ __forceinline__ In in(const uint16_t *x, int rows_all, int K, int nb, int row, bool live)
+    {
+        const uint32_t g = (threadIdx.x & 63) >> 4;
+        return In{buffer_of(x, (size_t)rows_all * K * 2), live ? (uint32_t)row * 2u * K + 16 * g : kNowhere, nb};
+    }
+    __device__ __forceinline__ void load(const In &in, int q)
+    {
+        const int c = threadIdx.x & 15;
+#pragma unroll
+        for (int o = 0; o < R; ++o) {  // (blocks past the end of a short last quad: zero)
+            const int b = Slots<R>::block(o, c);
+            x[o] = load16(in.x, 4 * q + b < in.nb ? in.at + 64 * b : kNowhere, 256 * q);
+        }
+    }
+    __device__ __forceinline__ f32x4 dot(int j, u32x4 b) const { return blockdot<false>(x[Slots<R>::operand(j)], b); }
+    __device__ __forceinline__ float scale(float d, int, int) const { return d; }
+};
+
+// The products of up to 4 R rows (operands `rows`) with the wave's run of L <= 4
+// segments of four tiles, a quad of both loaded ahead (the first quad's
+// weights by the caller); the run's roots go to root [tile][r][lane].
+template <int R, typename ROWS>
+__device__ __forceinline__ void multiply_run(const FourTiles &tiles, Weights &first, const typename ROWS::In &in, int sa,
+                                             int L, const Plan &plan, float *root)
+{
+    const int lane = threadIdx.x & 63;
+    const Dequant<false> dq;
+    const int qa = (sa * plan.G) >> plan.log2S, qb = ((sa + L) * plan.G) >> plan.log2S;
+    float p[4][R], s0[4][R], s1[4][R];
+#pragma unroll
+    for (int t = 0; t < 4; ++t)
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+            p[t][r] = s0[t][r] = s1[t][r] = 0.f;
+    int seg = 0, end = ((sa + 1) * plan.G) >> plan.log2S;
+    auto multiply = [&](const Weights &w, const ROWS &x, int q) {
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+            f32x4 D[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                D[j] = x.dot(j, dq(w.codes[t][j]));
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float d = quad_scale(w.scales[t], j);
+#pragma unroll
+                for (int r = 0; r < R; ++r)
+                    p[t][r] = __builtin_fmaf(x.scale(d, r, j), D[j][Slots<R>::comp(j, r)], p[t][r]);
             }
+        }
+        if (q + 1 == end) {  // a segment ends: the tree's lower two levels
 #pragma unroll
-            for (int t = 0; t < 4; ++t) {
-                f32x4 D[4];
+            for (int t = 0; t < 4; ++t)
 #pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    D[j] = blockdot<false>(a[Slots<R>::operand(j)], dq(codes[t][j]));
+                for (int r = 0; r < R; ++r) {
+                    float v = p[t][r];
+                    if (seg & 1)
+                        v = s0[t][r] + v;
+                    if (seg == 3)
+                        v = s1[t][r] + v;
+                    if (seg & 1)
+                        s1[t][r] = v;
+                    else
+                        s0[t][r] = v;
+                    p[t][r] = seg == L - 1 ? v : 0.f;
+                }
+            ++seg;
+            end = ((sa + seg + 1) * plan.G) >> plan.log2S;
+        }
+    };
+    Weights second;
+    ROWS xa, xb;
+    xa.load(in, qa);
+    for (int q = qa; q < qb; q += 2) {
+        if (q + 1 < qb) {
+            second.load(tiles, q + 1);
+            xb.load(in, q + 1);
+        }
+        multiply(first, xa, q);
+        if (q + 1 < qb) {
+            if (q + 2 < qb) {
+                first.load(tiles, q + 2);
+                xa.load(in, q + 2);
+            }
+            multiply(second, xb, q + 1);
+        }
+    }
+#pragma unroll
+    for (int t = 0; t < 4; ++t)
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+            root[(t * R + r) * 64 + lane] = p[t][r];
+}
+
+// The runs' roots of output (tile, row i) of a group, column c: the tree's top.
+template <int R>
+__device__ __forceinline__ float join_runs(const float *part, int waves, int tile, int i, int c)
+{
+    float v[8];
+#pragma unroll
+    for (int w = 0; w < 8; ++w)
+        v[w] = w < waves ? part[((w * 4 + tile) * R + (i >> 2)) * 64 + (i & 3) * 16 + c] : 0.f;
+    return tree_sum<8>(v, waves);
+}
+
+// What the gate/up kernel reads and writes.
+struct UpArgs {
+    const uint16_t *x;
+    const int *lift;  // or null: x as given
+    uint16_t *hi, *lo;
+    int *shift;
+    int H, I, shifts;
+};
+
+// A group of up to 4 R of the expert's rows: products, activation, h.
+template <int R>
+__device__ __forceinline__ void up_rows(const UpArgs &u, const FourTiles &tiles, Weights &first, const uint16_t *list,
+                                        int rows, int M, int topk, int L, const Plan &plan, float *part, int *back)
+{
+    const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), c = tid & 15;
+    const int waves = blockDim.x >> 6;
+    const int row = Slots<R>::row(c);
+    const bool live = row < rows;
+    if (tid < rows)
+        back[tid] = u.lift ? -u.lift[list[tid] / topk] : 0;
+    const auto in = RowsX<R>::in(u.x, M, u.H, plan.nb, live ? list[row] / topk : 0, live);
+    multiply_run<R, RowsX<R>>(tiles, first, in, wave * L, L, plan, part + wave * 4 * R * 64);
+    __syncthreads();
+    // 32 lanes a row: the trees, the activation, the block's power of two
+    for (int o = tid; o < rows * 32; o += blockDim.x) {
+        const int i = o >> 5, col = o & 31;
+        const float gate = __builtin_ldexpf(join_runs<R>(part, waves, col >> 4, i, col & 15), back[i]);
+        const float up = __builtin_ldexpf(join_runs<R>(part, waves, 2 + (col >> 4), i, col & 15), back[i]);
+        const float h = gate / (1.f + __builtin_expf(-gate)) * up;
+        float top = __builtin_fabsf(h) < __builtin_inff() ? __builtin_fabsf(h) : 0.f;
+#pragma unroll
+        for (int d = 1; d < 32; d *= 2)
+            top = __builtin_fmaxf(top, __shfl_xor(top, d));
+        const int raise = lift_of(top);
+        const float v = __builtin_ldexpf(h, raise);
+        const _Float16 vh = (_Float16)v;
+        const float rest = v - (float)vh;
+        const _Float16 vl = __builtin_fabsf(v) < __builtin_inff() ? (_Float16)rest : (_Float16)0.f;
+        const size_t slot = list[i];
+        const size_t k = slot * u.I + 32 * blockIdx.x + col;
+        u.hi[k] = __builtin_bit_cast(uint16_t, vh);
+        u.lo[k] = __builtin_bit_cast(uint16_t, vl);
+        if (col == 0)
+            u.shift[slot * u.shifts + blockIdx.x] = -raise;
+    }
+}
+
+// gate and up.  grid = (I / 32, experts that can be chosen).  A workgroup owns
+// two tiles of gate and two of up of one expert, so that it ends with 32
+// values of h: one block of the down product.  An expert's rows go 4, 8 or 16
+// (at most 4 RM) at a time, by how many are left.
+template <int RM>
+__global__ __launch_bounds__(512) void q4_moe_up_kernel(Choice ch, UpArgs u, int *__restrict__ ids,
+                                                        float *__restrict__ weights,
+                                                        const uint8_t *__restrict__ wq,
+                                                        const uint16_t *__restrict__ scales, int L, Plan plan)
+{
+    extern __shared__ __attribute__((aligned(16))) float part[];  // [wave][tile][r][lane]
+    __shared__ Found found;
+    __shared__ int back[16];
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int n = ch.M * ch.topk;
+    if (ch.parts) {
+        uint64_t *keys = (uint64_t *)part;
+        choose_rows<int16_t>(ch, 0, ch.M, keys, (double *)(keys + ch.M * ch.E), found.who, ids, weights,
+                             blockIdx.x == 0 && blockIdx.y == 0);
+        __syncthreads();  // (the keys' room is the products' next)
+    }
+    FourTiles tiles;
+    Weights first;
+    const int qa = (wave * L * plan.G) >> plan.log2S;
+    const int count = find_expert(found, n, ids, ch.parts != nullptr, ch.E, blockIdx.y, [&](int e) {
+        const size_t gate = (size_t)e * (2 * u.I / 16) + 2 * blockIdx.x, up = gate + u.I / 16;
+        tiles = FourTiles{Tile(wq, scales, gate, plan.G), Tile(wq, scales, gate + 1, plan.G),
+                          Tile(wq, scales, up, plan.G), Tile(wq, scales, up + 1, plan.G)};
+        first.load(tiles, qa);
+    });
+    for (int r0 = 0; r0 < count;) {
+        const int left = count - r0;
+        if (r0) {
+            __syncthreads();  // the last group's sums are read
+            first.load(tiles, qa);
+        }
+        if (RM == 1 || left <= 4) {
+            up_rows<1>(u, tiles, first, found.list + r0, min(left, 4), ch.M, ch.topk, L, plan, part, back);
+            r0 += 4;
+        } else if (RM == 2 || left <= 8) {
+            up_rows<RM == 1 ? 1 : 2>(u, tiles, first, found.list + r0, min(left, 8), ch.M, ch.topk, L, plan, part, back);
+            r0 += 8;
+        } else {
+            up_rows<RM>(u, tiles, first, found.list + r0, min(left, 16), ch.M, ch.topk, L, plan, part, back);
+            r0 += 16;
+        }
+    }
+}
+
+// h as the gate/up kernel leaves it.
+struct DownIn {
+    const uint16_t *hi, *lo;
+    const int *shift;
+    int n, I, shifts;  // slots, values and powers of two of a slot
+};
+
+template <int R>
+struct DownRows {
+    u32x4 hi[R], lo[R];
+    u32x4 shift[R];  // of the quad's blocks
+};
+
+// `rows` rows of `list` (up to 4 R) by the run of L segments from segment sa
+// of one tile of one expert: codes D quads ahead, h one.
+template <int R>
+__device__ __forceinline__ void down_rows(const DownIn &in, const uint16_t *list, int rows, const Tile &tile, int sa,
+                                          int L, const Plan &plan, float *root, int runs, int run)
+{
+    constexpr int D = R == 1 ? 4 : 2;
+    const int lane = threadIdx.x & 63, c = lane & 15, g = lane >> 4;
+    const Dequant<false> dq;
+    const int qa = (sa * plan.G) >> plan.log2S, qb = ((sa + L) * plan.G) >> plan.log2S;
+    const uint32_t w_at = 16 * lane, s_at = 8 * c;
+    u32x4 codes[D];
+    u32x2 sc[D];
+#pragma unroll
+    for (int i = 0; i < D; ++i)
+        if (qa + i < qb) {
+            codes[i] = load_codes(tile.w, w_at, qa + i);
+            sc[i] = load_scales(tile.s, s_at, qa + i);
+        }
+    const __amdgpu_buffer_rsrc_t hb = buffer_of(in.hi, (size_t)in.n * in.I * 2),
+                                 lb = buffer_of(in.lo, (size_t)in.n * in.I * 2),
+                                 sb = buffer_of(in.shift, (size_t)in.n * in.shifts * 4);
+    const int row = Slots<R>::row(c);
+    const uint32_t h_at = row < rows ? (uint32_t)list[row] * 2u * in.I + 16 * g : kNowhere;
+    // the rows whose values this lane group accumulates
+    int mine[R];
+    uint32_t shift_at[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        mine[r] = 4 * r + g < rows ? list[4 * r + g] : -1;
+        shift_at[r] = mine[r] >= 0 ? (uint32_t)mine[r] * 4u * in.shifts : kNowhere;
+    }
+    auto load_h = [&](DownRows<R> &h, int q) {
+#pragma unroll
+        for (int o = 0; o < R; ++o) {  // (blocks past the end of a short last quad: zero)
+            const int b = Slots<R>::block(o, c);
+            const uint32_t at = 4 * q + b < plan.nb ? h_at + 64 * b : kNowhere;
+            h.hi[o] = load16(hb, at, 256 * q);
+            h.lo[o] = load16(lb, at, 256 * q);
+        }
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+            h.shift[r] = load16(sb, shift_at[r], 16 * q);
+    };
+    TreeStack<R, float> tree;
+    float p[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+        p[r] = 0.f;
+    int seg = sa, end = ((sa + 1) * plan.G) >> plan.log2S;
+    DownRows<R> next;
+    load_h(next, qa);
+    for (int q0 = qa; q0 < qb; q0 += D) {
+#pragma unroll
+        for (int i = 0; i < D; ++i) {
+            const int q = q0 + i;
+            if (q < qb) {
+                const DownRows<R> h = next;
+                const u32x4 cw = codes[i];
+                const u32x2 sw = sc[i];
+                if (q + 1 < qb)
+                    load_h(next, q + 1);
+                if (q + D < qb) {
+                    codes[i] = load_codes(tile.w, w_at, q + D);
+                    sc[i] = load_scales(tile.s, s_at, q + D);
+                }
+                f32x4 v[4];
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    const float d = quad_scale(sc[t], j);
+                    const u32x4 b = dq(cw[j]);
+                    v[j] = dot16(h.hi[Slots<R>::operand(j)], b, blockdot<false>(h.lo[Slots<R>::operand(j)], b));
+                }
 #pragma unroll
-                    for (int r = 0; r < R; ++r)
-                        p[t][r] = __builtin_fmaf(d, D[j][Slots<R>::comp(j, r)], p[t][r]);
+                for (int j = 0; j < 4; ++j) {
+                    const float d = quad_scale(sw, j);
+#pragma unroll
+                    for (int r = 0; r < R; ++r) {
+                        const int by = (int)h.shift[r][j];
+                        p[r] = __builtin_fmaf(__builtin_ldexpf(d, by), v[j][Slots<R>::comp(j, r)], p[r]);
+                    }
+                }
+                if (q + 1 == end) {
+                    if (!tree.push(p, seg - sa, L)) {
+#pragma unroll
+                        for (int r = 0; r < R; ++r)
+                            p[r] = 0.f;
+                    }
+                    ++seg;
+                    end = ((seg + 1) * plan.G) >> plan.log2S;
                 }
             }
         }
-        if (r0)
-            __syncthreads();  // the last group's sums are read
-#pragma unroll
-        for (int t = 0; t < 4; ++t)
-#pragma unroll
-            for (int r = 0; r < R; ++r) {
-                float v = p[t][r];
-                if constexpr (BF16)
-                    v = __builtin_ldexpf(v, -back[r]);
-                part[((wave * 4 + t) * R + r) * 64 + lane] = v;
-            }
-        __syncthreads();
-        // 32 lanes a row: the trees, the activation, the block's power of two
-        const int rows = min(count - r0, 4 * R);
-        for (int o = threadIdx.x; o < rows * 32; o += blockDim.x) {
-            const int i = o >> 5, col = o & 31;
-            const int at = ((col >> 4) * R + (i >> 2)) * 64 + (i & 3) * 16 + (col & 15);
-            float gv[16], uv[16];
-#pragma unroll
-            for (int s = 0; s < 16; ++s) {
-                gv[s] = s < S ? part[s * 4 * R * 64 + at] : 0.f;
-                uv[s] = s < S ? part[s * 4 * R * 64 + 2 * R * 64 + at] : 0.f;
-            }
-            const float gate = tree_sum<16>(gv, S), up = tree_sum<16>(uv, S);
-            const float h = gate / (1.f + __builtin_expf(-gate)) * up;
-            float top = __builtin_fabsf(h) < __builtin_inff() ? __builtin_fabsf(h) : 0.f;
-#pragma unroll
-            for (int d = 1; d < 32; d *= 2)
-                top = __builtin_fmaxf(top, __shfl_xor(top, d));
-            const int up2 = lift_of(top);
-            const float v = __builtin_ldexpf(h, up2);
-            const _Float16 vh = (_Float16)v;
-            const float rest = v - (float)vh;
-            const _Float16 vl = __builtin_fabsf(v) < __builtin_inff() ? (_Float16)rest : (_Float16)0.f;
-            const size_t slot = list[r0 + i];
-            const size_t k = slot * I + 32 * blockIdx.x + col;
-            hi[k] = __builtin_bit_cast(uint16_t, vh);
-            lo[k] = __builtin_bit_cast(uint16_t, vl);
-            if (col == 0)
-                shift[slot * (I / 32) + blockIdx.x] = -up2;
-        }
     }
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+        if (mine[r] >= 0)
+            root[(mine[r] * runs + run) * 16 + c] = p[r];
 }
 
 // down and the sum over the chosen experts.  grid = tiles of 16 columns of y;
 // a workgroup's waves take (expert, run of segments) pairs in turn, the runs'
 // roots meet in LDS, and each output adds its experts in the order of j.
-template <int R>
+// FEW: no expert has more than 4 rows unless a row names it twice.
+template <bool FEW>
 __global__ __launch_bounds__(1024) void q4_moe_down_kernel(const int *__restrict__ ids,
-                                                           const float *__restrict__ weights,
-                                                           const uint16_t *__restrict__ hi,
-                                                           const uint16_t *__restrict__ lo,
-                                                           const int *__restrict__ shift,
+                                                           const float *__restrict__ weights, DownIn in,
                                                            const uint8_t *__restrict__ wq,
                                                            const uint16_t *__restrict__ scales, float *__restrict__ y,
-                                                           int M, int topk, int E, int H, int I, Plan plan)
+                                                           int M, int topk, int E, int H, Plan plan)
 {
     extern __shared__ __attribute__((aligned(16))) float root[];  // [slot][run][16 columns]
-    __shared__ int first[kExperts];      // an expert's rows before the scatter, their end after it
-    __shared__ uint16_t list[kSlots];    // slots in the order of their experts
+    __shared__ int first[kExperts];        // an expert's rows before the scatter, their end after it
+    __shared__ uint16_t list[kSlots];      // slots in the order of their experts
     __shared__ uint16_t active[kExperts];  // chosen experts
     __shared__ int sums[2][16];
     __shared__ int total;
-    const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63, c = lane & 15, g = lane >> 4;
+    const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
     const int n = M * topk;
     // counting sort of the slots by expert
     first[tid] = 0;
@@ -483,76 +899,26 @@ __global__ __launch_bounds__(1024) void q4_moe_down_kernel(const int *__restrict
     if (valid)
         list[atomicAdd(&first[id], 1)] = (uint16_t)tid;
     __syncthreads();
-    const int A = total, S = plan.S;
+    const int A = __builtin_amdgcn_readfirstlane(total), S = plan.S;
     int runs = 1;
     while (A * runs < 16 && 2 * runs <= S && 2 * runs * n <= kSlots)
         runs *= 2;
     const int L = S / runs;
-    const Dequant<false> dq;
     for (int u = wave; u < A * runs; u += 16) {
-        const int e = active[u / runs], run = u % runs;
-        const int end = first[e], begin = u / runs ? first[active[u / runs - 1]] : 0;
-        const size_t tile = (size_t)e * (H / 16) + blockIdx.x;
-        const uint8_t *w = wq + tile * plan.G * 1024 + lane * 16;
-        const uint16_t *ws = scales + tile * plan.G * 64 + c * 4;
-        for (int r0 = begin; r0 < end; r0 += 4 * R) {
-            const int row = r0 + Slots<R>::row(c);
-            const bool live = row < end;
-            const size_t slot = live ? list[row] : 0;
-            const uint16_t *ph = hi + slot * I + 8 * g, *pl = lo + slot * I + 8 * g;
-            // the rows whose values this lane group accumulates
-            const int *sh[R];
-            int mine[R];
-#pragma unroll
-            for (int r = 0; r < R; ++r) {
-                const int i = r0 + 4 * r + g;
-                mine[r] = i < end ? list[i] : -1;
-                sh[r] = shift + (size_t)max(mine[r], 0) * (I / 32);
+        const int a = u / runs, run = u % runs;
+        const int e = __builtin_amdgcn_readfirstlane(active[a]);
+        const int end = __builtin_amdgcn_readfirstlane(first[e]);
+        const int begin = __builtin_amdgcn_readfirstlane(a ? first[active[a - 1]] : 0);
+        const Tile tile(wq, scales, (size_t)e * (H / 16) + blockIdx.x, plan.G);
+        for (int r0 = begin; r0 < end;) {
+            const int left = end - r0;
+            if (FEW || left <= 4) {
+                down_rows<1>(in, list + r0, min(left, 4), tile, run * L, L, plan, root, runs, run);
+                r0 += 4;
+            } else {
+                down_rows<2>(in, list + r0, min(left, 8), tile, run * L, L, plan, root, runs, run);
+                r0 += 8;
             }
-            TreeStack<R, float> tree;
-            float p[R];
-            for (int li = 0; li < L; ++li) {
-                const int s = run * L + li;
-                const int qa = seg_first_block(plan, s) / 4, qb = (seg_end_block(plan, s) + 3) / 4;
-#pragma unroll
-                for (int r = 0; r < R; ++r)
-                    p[r] = 0.f;
-                for (int q = qa; q < qb; ++q) {
-                    const u32x4 codes = load_codes(w + (size_t)q * 1024);
-                    const u32x2 sc = load_scales(ws + (size_t)q * 64);
-                    u32x4 ah[R], al[R];
-#pragma unroll
-                    for (int o = 0; o < R; ++o) {
-                        const int b = 4 * q + Slots<R>::block(o, c);
-                        ah[o] = al[o] = (u32x4){0, 0, 0, 0};
-                        if (live && b < plan.nb) {
-                            ah[o] = *(const u32x4 *)(ph + 32 * b);
-                            al[o] = *(const u32x4 *)(pl + 32 * b);
-                        }
-                    }
-                    f32x4 D[4];
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const u32x4 b = dq(codes[j]);
-                        D[j] = dot16(ah[Slots<R>::operand(j)], b, blockdot<false>(al[Slots<R>::operand(j)], b));
-                    }
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        if (4 * q + j < plan.nb) {
-                            const float d = quad_scale(sc, j);
-#pragma unroll
-                            for (int r = 0; r < R; ++r)
-                                p[r] = __builtin_fmaf(__builtin_ldexpf(d, sh[r][4 * q + j]),
-                                                      D[j][Slots<R>::comp(j, r)], p[r]);
-                        }
-                    }
-                }
-                tree.push(p, li, L);
-            }
-#pragma unroll
-            for (int r = 0; r < R; ++r)
-                if (mine[r] >= 0)
-                    root[(mine[r] * runs + run) * 16 + c] = p[r];
         }
     }
     __syncthreads();
@@ -578,73 +944,157 @@ size_t up256(size_t n) { return (n + 255) & ~(size_t)255; }
 // Rows one launch handles.
 int chunk_rows(int M, int topk) { return std::min(M, kSlots / topk); }
 
-template <int XK>
-void launch_logits(int rk, dim3 grid, const uint16_t *x, const void *router, const float *bias, double *logits, int M,
-                   int E, int K, hipStream_t stream)
+// Parts of the logits in memory: all of K's for few rows, else one (the sum).
+// The part form fills the card from one row on; from about a tile a compute
+// unit on, the row form needs no room for parts.
+int logit_parts(int M, int E, int K)
 {
-    if (rk == 2)
-        hipLaunchKernelGGL((q4_moe_logits_kernel<XK, 2>), grid, dim3(1024), 0, stream, x, router, bias, logits, M, E, K);
-    else
-        hipLaunchKernelGGL((q4_moe_logits_kernel<XK, XK>), grid, dim3(1024), 0, stream, x, router, bias, logits, M, E,
-                           K);
+    const long long tiles = (long long)((M + 15) / 16) * ((E + 15) / 16);
+    return tiles >= 1024 ? 1 : (K + kPart - 1) / kPart;
 }
 
-template <bool BF16, int R>
-hipError_t launch_experts(const uint16_t *x, const int *ids, const float *weights, const uint8_t *w13,
-                          const uint16_t *s13, const uint8_t *w2, const uint16_t *s2, float *y, int M, int topk, int E,
-                          int H, int I, uint16_t *hi, uint16_t *lo, int *shift, hipStream_t stream)
+template <int XK, int RK>
+void launch_logits_k(const uint16_t *x, const void *router, double *parts, uint16_t *x16, int *lift, int M, int E,
+                     int K, hipStream_t stream)
+{
+    const int count = logit_parts(M, E, K);
+    const unsigned et = (unsigned)((E + 15) / 16), mt = (unsigned)((M + 15) / 16);
+    if (count == 1 && K > kPart)
+        hipLaunchKernelGGL((q4_moe_logits_rows_kernel<XK, RK>), dim3(et, (mt + 3) / 4), dim3(256), 0, stream, x, router,
+                           parts, M, E, K);
+    else
+        hipLaunchKernelGGL((q4_moe_logits_kernel<XK, RK>), dim3(et, mt, (unsigned)(count + (x16 ? 1 : 0))), dim3(256), 0,
+                           stream, x, router, parts, x16, lift, M, E, K);
+}
+
+hipError_t launch_logits(const void *x, int xk, const void *router, int rk, double *parts, uint16_t *x16, int *lift,
+                         int M, int E, int K, hipStream_t stream)
+{
+    const uint16_t *xp = (const uint16_t *)x;
+    if (xk == 1 && rk == 2)
+        launch_logits_k<1, 2>(xp, router, parts, x16, lift, M, E, K, stream);
+    else if (xk == 1)
+        launch_logits_k<1, 1>(xp, router, parts, x16, lift, M, E, K, stream);
+    else if (rk == 2)
+        launch_logits_k<0, 2>(xp, router, parts, x16, lift, M, E, K, stream);
+    else
+        launch_logits_k<0, 0>(xp, router, parts, x16, lift, M, E, K, stream);
+    return hipGetLastError();
+}
+
+hipError_t launch_select(const Choice &ch, int *ids, float *weights, const void *x, uint16_t *x16, int *lift, int K,
+                         hipStream_t stream)
+{
+    hipLaunchKernelGGL(q4_moe_select_kernel, dim3((unsigned)ch.M), dim3(256),
+                       (size_t)(ch.E + ch.topk) * sizeof(double), stream, ch, ids, weights, (const uint16_t *)x, x16,
+                       lift, K);
+    return hipGetLastError();
+}
+
+// Where the parts of a workspace lie; sizes of a piece of rows.
+struct MoeRoom {
+    uint16_t *hi, *lo, *x16;
+    int *shift, *lift;
+    size_t bytes;
+    MoeRoom(void *base, int rows, int topk, int H, int I)
+    {
+        const size_t n = (size_t)rows * topk;
+        uint8_t *p = (uint8_t *)base;
+        size_t at = 0;
+        auto take = [&](size_t b) {
+            uint8_t *r = p + at;
+            at += up256(b);
+            return r;
+        };
+        hi = (uint16_t *)take(n * I * 2);
+        lo = (uint16_t *)take(n * I * 2);
+        shift = (int *)take(n * shifts_of(I) * 4);
+        x16 = (uint16_t *)take((size_t)rows * H * 2);
+        lift = (int *)take((size_t)rows * 4);
+        bytes = at;
+    }
+    // an expert row's powers of two, padded to whole quads
+    static int shifts_of(int I) { return (I / 32 + 3) / 4 * 4; }
+};
+
+// The largest group of rows the gate/up kernel is built for: by the rows an
+// expert gets on average.
+int up_group(int n, int E)
+{
+    const int rows = n / std::min(n, E);
+    return rows <= 1 ? 1 : rows <= 7 ? 2 : 4;
+}
+
+// gate/up and down of a piece of rows; ch.parts: the gate/up kernel chooses.
+hipError_t products(const Choice &ch, const uint16_t *x, const int *lift, int *ids, float *weights, const uint8_t *w13,
+                    const uint16_t *s13, const uint8_t *w2, const uint16_t *s2, float *y, int H, int I,
+                    const MoeRoom &room, hipStream_t stream)
 {
     const Plan up = make_plan(H), down = make_plan(I);
-    const int n = M * topk;
-    const size_t lds_up = (size_t)up.S * 4 * R * 64 * sizeof(float);
-    // (the largest with the kernels' fixed parts passes the default limit)
-    hipError_t e = hipSuccess;
-    if (R == 4)
-        e = hipFuncSetAttribute((const void *)q4_moe_up_kernel<BF16, R>, hipFuncAttributeMaxDynamicSharedMemorySize,
-                                (int)lds_up);
+    const int n = ch.M * ch.topk, shifts = MoeRoom::shifts_of(I);
+    const dim3 grid((unsigned)(I / 32), (unsigned)std::min(n, ch.E));
+    // eight waves a workgroup while the card is not full, else four
+    const int waves = std::min(up.S, (size_t)grid.x * grid.y >= 1024 ? 4 : 8);
+    const int RM = up_group(n, ch.E);
+    size_t lds_up = (size_t)waves * 4 * RM * 64 * sizeof(float);
+    if (ch.parts)
+        lds_up = std::max(lds_up, (size_t)(ch.M * ch.E + n) * sizeof(double));
     // roots: [slot][run][16], where the kernel keeps slots x runs within kSlots
     const size_t lds_down = (size_t)std::min(kSlots, 16 * n) * 16 * sizeof(float);
-    if (e == hipSuccess && lds_down > 32 * 1024)
-        e = hipFuncSetAttribute((const void *)q4_moe_down_kernel<R>, hipFuncAttributeMaxDynamicSharedMemorySize,
-                                (int)lds_down);
+    const bool few = ch.M <= 4;
+    const void *down_fn = few ? (const void *)q4_moe_down_kernel<true> : (const void *)q4_moe_down_kernel<false>;
+    // (with the kernel's fixed parts, the largest pass the default limit)
+    hipError_t e = hipSuccess;
+    if (lds_down > 32 * 1024)
+        e = hipFuncSetAttribute(down_fn, hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds_down);
     if (e != hipSuccess)
         return e;
-    hipLaunchKernelGGL((q4_moe_up_kernel<BF16, R>), dim3((unsigned)(I / 32), (unsigned)std::min(n, E)),
-                       dim3(64 * up.S), lds_up, stream, x, ids, w13, s13, hi, lo, shift, n, topk, E, H, I, up);
+    const UpArgs u{x, lift, room.hi, room.lo, room.shift, H, I, shifts};
+    const int L = up.S / waves;
+    if (RM == 1)
+        hipLaunchKernelGGL(q4_moe_up_kernel<1>, grid, dim3(64 * waves), lds_up, stream, ch, u, ids, weights, w13, s13, L,
+                           up);
+    else if (RM == 2)
+        hipLaunchKernelGGL(q4_moe_up_kernel<2>, grid, dim3(64 * waves), lds_up, stream, ch, u, ids, weights, w13, s13, L,
+                           up);
+    else
+        hipLaunchKernelGGL(q4_moe_up_kernel<4>, grid, dim3(64 * waves), lds_up, stream, ch, u, ids, weights, w13, s13, L,
+                           up);
     e = hipGetLastError();
     if (e != hipSuccess)
         return e;
-    hipLaunchKernelGGL((q4_moe_down_kernel<R>), dim3((unsigned)(H / 16)), dim3(1024), lds_down, stream, ids, weights,
-                       hi, lo, shift, w2, s2, y, M, topk, E, H, I, down);
+    const DownIn in{room.hi, room.lo, room.shift, n, I, shifts};
+    if (few)
+        hipLaunchKernelGGL(q4_moe_down_kernel<true>, dim3((unsigned)(H / 16)), dim3(1024), lds_down, stream, ids, weights,
+                           in, w2, s2, y, ch.M, ch.topk, ch.E, H, down);
+    else
+        hipLaunchKernelGGL(q4_moe_down_kernel<false>, dim3((unsigned)(H / 16)), dim3(1024), lds_down, stream, ids,
+                           weights, in, w2, s2, y, ch.M, ch.topk, ch.E, H, down);
     return hipGetLastError();
 }
 
 }  // namespace
 
-size_t moe_route_workspace_bytes(int M, int E) { return up256((size_t)M * E * sizeof(double)); }
+size_t moe_route_workspace_bytes(int M, int E, int K)
+{
+    return up256((size_t)logit_parts(M, E, K) * M * E * sizeof(double));
+}
 
 hipError_t launch_moe_route(const void *x, int x_kind, const void *router, int r_kind, const float *bias, int *ids,
                             float *weights, int M, int E, int K, int topk, int renormalize, void *workspace,
                             hipStream_t stream)
 {
-    double *logits = (double *)workspace;
-    const dim3 grid((unsigned)((E + 15) / 16), (unsigned)((M + 15) / 16));
-    if (x_kind == 1)
-        launch_logits<1>(r_kind, grid, (const uint16_t *)x, router, bias, logits, M, E, K, stream);
-    else
-        launch_logits<0>(r_kind, grid, (const uint16_t *)x, router, bias, logits, M, E, K, stream);
-    const hipError_t e = hipGetLastError();
+    double *parts = (double *)workspace;
+    const hipError_t e = launch_logits(x, x_kind, router, r_kind, parts, nullptr, nullptr, M, E, K, stream);
     if (e != hipSuccess)
         return e;
-    hipLaunchKernelGGL(q4_moe_select_kernel, dim3((unsigned)M), dim3(256), (size_t)(E + topk) * sizeof(double), stream,
-                       logits, ids, weights, E, topk, renormalize);
-    return hipGetLastError();
+    const Choice ch{parts, bias, logit_parts(M, E, K), M, E, topk, renormalize};
+    return launch_select(ch, ids, weights, nullptr, nullptr, nullptr, K, stream);
 }
 
-size_t moe_workspace_bytes(int M, int I, int topk)
+size_t moe_workspace_bytes(int M, int H, int I, int topk)
 {
-    const size_t n = (size_t)chunk_rows(M, topk) * topk;
-    return 2 * up256(n * I * sizeof(uint16_t)) + up256(n * (I / 32) * sizeof(int));
+    return MoeRoom(nullptr, chunk_rows(M, topk), topk, H, I).bytes;
 }
 
 hipError_t launch_moe_experts(const void *x, bool bf16, const int *ids, const float *weights, const uint8_t *w13,
@@ -652,29 +1102,75 @@ hipError_t launch_moe_experts(const void *x, bool bf16, const int *ids, const fl
                               int E, int H, int I, void *workspace, hipStream_t stream)
 {
     const int rows = chunk_rows(M, topk);
-    const size_t part = up256((size_t)rows * topk * I * sizeof(uint16_t));
-    uint16_t *hi = (uint16_t *)workspace;
-    uint16_t *lo = (uint16_t *)((uint8_t *)workspace + part);
-    int *shift = (int *)((uint8_t *)workspace + 2 * part);
+    const MoeRoom room(workspace, rows, topk, H, I);
     for (int m = 0; m < M; m += rows) {
         const int now = std::min(rows, M - m);
         const uint16_t *xm = (const uint16_t *)x + (size_t)m * H;
-        const int *im = ids + (size_t)m * topk;
-        const float *wm = weights + (size_t)m * topk;
-        float *ym = y + (size_t)m * H;
-        hipError_t e;
-#define Q4_MOE(B, R) launch_experts<B, R>(xm, im, wm, w13, s13, w2, s2, ym, now, topk, E, H, I, hi, lo, shift, stream)
-        if (now <= 4)
-            e = bf16 ? Q4_MOE(true, 1) : Q4_MOE(false, 1);
-        else if (now <= 8)
-            e = bf16 ? Q4_MOE(true, 2) : Q4_MOE(false, 2);
-        else
-            e = bf16 ? Q4_MOE(true, 4) : Q4_MOE(false, 4);
-#undef Q4_MOE
+        if (bf16) {
+            hipLaunchKernelGGL(q4_moe_lift_kernel, dim3((unsigned)((now + 3) / 4)), dim3(256), 0, stream, xm, room.x16,
+                               room.lift, now, H);
+            const hipError_t e = hipGetLastError();
+            if (e != hipSuccess)
+                return e;
+        }
+        const Choice ch{nullptr, nullptr, 0, now, E, topk, 0};
+        const hipError_t e = products(ch, bf16 ? room.x16 : xm, bf16 ? room.lift : nullptr,
+                                      const_cast<int *>(ids) + (size_t)m * topk,
+                                      const_cast<float *>(weights) + (size_t)m * topk, w13, s13, w2, s2,
+                                      y + (size_t)m * H, H, I, room, stream);
         if (e != hipSuccess)
             return e;
     }
     return hipSuccess;
+}
+
+// The whole layer's room: ids and weights, the logits' parts, the products'.
+static size_t layer_room(int M, int E, int H, int topk)
+{
+    return 2 * up256((size_t)M * topk * 4) + moe_route_workspace_bytes(M, E, H);
+}
+
+size_t moe_layer_workspace_bytes(int M, int E, int H, int I, int topk)
+{
+    return layer_room(M, E, H, topk) + moe_workspace_bytes(M, H, I, topk);
+}
+
+hipError_t launch_moe_layer(const void *x, int x_kind, const void *router, int r_kind, const float *bias,
+                            const uint8_t *w13, const uint16_t *s13, const uint8_t *w2, const uint16_t *s2, float *y,
+                            int M, int E, int H, int I, int topk, int renormalize, void *workspace, hipStream_t stream)
+{
+    uint8_t *p = (uint8_t *)workspace;
+    int *ids = (int *)p;
+    float *weights = (float *)(p + up256((size_t)M * topk * 4));
+    double *parts = (double *)(p + 2 * up256((size_t)M * topk * 4));
+    void *rest = p + layer_room(M, E, H, topk);
+    const bool bf16 = x_kind == 1;
+    const int count = logit_parts(M, E, H);
+    const Choice ch{parts, bias, count, M, E, topk, renormalize};
+    if (chunk_rows(M, topk) < M) {  // too many rows for one piece
+        const hipError_t e =
+            launch_moe_route(x, x_kind, router, r_kind, bias, ids, weights, M, E, H, topk, renormalize, parts, stream);
+        if (e != hipSuccess)
+            return e;
+        return launch_moe_experts(x, bf16, ids, weights, w13, s13, w2, s2, y, M, topk, E, H, I, rest, stream);
+    }
+    const MoeRoom room(rest, M, topk, H, I);
+    const uint16_t *xp = bf16 ? room.x16 : (const uint16_t *)x;
+    const int *lift = bf16 ? room.lift : nullptr;
+    // (the part form of the logits, which is all that few rows use, takes x to
+    // binary16 on the side; otherwise the select kernel does)
+    const bool fused = (long long)M * E * E <= kFused && !(count == 1 && H > kPart);
+    hipError_t e = launch_logits(x, x_kind, router, r_kind, parts, bf16 && fused ? room.x16 : nullptr, room.lift, M, E,
+                                 H, stream);
+    if (e != hipSuccess)
+        return e;
+    if (fused)
+        return products(ch, xp, lift, ids, weights, w13, s13, w2, s2, y, H, I, room, stream);
+    e = launch_select(ch, ids, weights, x, bf16 ? room.x16 : nullptr, room.lift, H, stream);
+    if (e != hipSuccess)
+        return e;
+    const Choice given{nullptr, nullptr, 0, M, E, topk, 0};
+    return products(given, xp, lift, ids, weights, w13, s13, w2, s2, y, H, I, room, stream);
 }
 
 }  // namespace q4

@@ -301,14 +301,14 @@ int q4_int8_linear(const void *x, int x_dtype, const float *x_scales, const void
  *   router   [E][K], router_dtype x_dtype or Q4_F32, 16-byte aligned
  *   bias     float32 [E], 4-byte aligned, or NULL
  *   ids      int32 [M][topk];  weights  float32 [M][topk]
- *   workspace at least q4_moe_route_workspace_bytes(M, E) bytes, as for
+ *   workspace at least q4_moe_route_workspace_bytes(M, E, K) bytes, as for
  *            q4_int8_linear
  * 1 <= topk <= E <= Q4_MOE_MAX_EXPERTS, M <= Q4_MOE_MAX_ROWS, K a multiple of
  * 32, at most 2^17.
  */
 #define Q4_MOE_MAX_EXPERTS 1024
 #define Q4_MOE_MAX_ROWS (1 << 20)
-size_t q4_moe_route_workspace_bytes(int M, int E); /* 0 for a bad shape */
+size_t q4_moe_route_workspace_bytes(int M, int E, int K); /* 0 for a bad shape */
 int q4_moe_route(const void *x, int x_dtype, const void *router, int router_dtype, const float *bias, int *ids,
                  float *weights, int M, int E, int K, int topk, int renormalize, void *workspace,
                  size_t workspace_bytes, void *stream);
@@ -328,14 +328,26 @@ int q4_moe_route(const void *x, int x_dtype, const void *router, int router_dtyp
  *            each expert's I gate rows, then its I up rows
  *   W2, s2   packed form of (E H) x I
  *   y        float32 [M][H], 4-byte aligned, overwritten
- *   workspace at least q4_moe_workspace_bytes(M, I, topk) bytes, as above
+ *   workspace at least q4_moe_experts_workspace_bytes(M, H, I, topk) bytes, as
+ *            above
  * H and I are multiples of 32, at most 2^17; topk <= Q4_MOE_MAX_EXPERTS.  Made
  * for few rows: past Q4_MOE_MAX_EXPERTS / topk rows the call runs in pieces.
  */
-size_t q4_moe_workspace_bytes(int M, int I, int topk); /* 0 for a bad shape */
+size_t q4_moe_experts_workspace_bytes(int M, int H, int I, int topk); /* 0 for a bad shape */
 int q4_moe_experts(const void *x, int x_dtype, const int *ids, const float *weights, const void *W13, const void *s13,
                    const void *W2, const void *s2, float *y, int M, int E, int H, int I, int topk, void *workspace,
                    size_t workspace_bytes, void *stream);
+
+/*
+ * The whole layer: q4_moe_route and q4_moe_experts (the same bits as the two
+ * calls) in three launches for a few rows (M E <= 1024), four above.
+ * Arguments as theirs, with K = H; workspace of at least
+ * q4_moe_layer_workspace_bytes(M, E, H, I, topk) bytes.
+ */
+size_t q4_moe_layer_workspace_bytes(int M, int E, int H, int I, int topk); /* 0 for a bad shape */
+int q4_moe_layer(const void *x, int x_dtype, const void *router, int router_dtype, const float *bias, const void *W13,
+                 const void *s13, const void *W2, const void *s2, float *y, int M, int E, int H, int I, int topk,
+                 int renormalize, void *workspace, size_t workspace_bytes, void *stream);
 
 /* Bytes of the packed codes and packed scales of an N x K matrix (0 for a
  * bad shape).  Pure host computation.  (Library layout; pages silent.) */

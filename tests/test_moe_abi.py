@@ -40,7 +40,7 @@ def test_route_argument_checks(lib):
     for kw in ({"x": FAKE + 8}, {"r": FAKE + 8}, {"bias": FAKE + 2}, {"ids": FAKE + 2}, {"w": FAKE + 1},
                {"ws": FAKE + 16}):
         assert route(lib, **kw) == _lib.Q4_ERR_ALIGN, kw
-    need = lib.q4_moe_route_workspace_bytes(4, 8)
+    need = lib.q4_moe_route_workspace_bytes(4, 8, 64)
     assert need > 0
     assert route(lib, wb=need - 1) == _lib.Q4_ERR_WORKSPACE
     assert route(lib, ws=None) == _lib.Q4_ERR_WORKSPACE
@@ -59,7 +59,7 @@ def test_experts_argument_checks(lib):
     for kw in ({"x": FAKE + 8}, {"ids": FAKE + 2}, {"w": FAKE + 2}, {"w13": FAKE + 8}, {"s13": FAKE + 4},
                {"w2": FAKE + 8}, {"s2": FAKE + 4}, {"y": FAKE + 2}, {"ws": FAKE + 16}):
         assert experts(lib, **kw) == _lib.Q4_ERR_ALIGN, kw
-    need = lib.q4_moe_workspace_bytes(4, 32, 2)
+    need = lib.q4_moe_experts_workspace_bytes(4, 64, 32, 2)
     assert need > 0
     assert experts(lib, wb=need - 1) == _lib.Q4_ERR_WORKSPACE
     assert experts(lib, ws=None) == _lib.Q4_ERR_WORKSPACE
@@ -67,9 +67,30 @@ def test_experts_argument_checks(lib):
 
 
 def test_sizes(lib):
-    assert lib.q4_moe_route_workspace_bytes(0, 8) == 0
-    assert lib.q4_moe_route_workspace_bytes(3, 1025) == 0
-    assert lib.q4_moe_workspace_bytes(3, 48, 2) == 0
-    assert lib.q4_moe_workspace_bytes(3, 64, 0) == 0
-    # past 1024 (row, expert) pairs the call runs in pieces: no more room
-    assert lib.q4_moe_workspace_bytes(128, 64, 8) == lib.q4_moe_workspace_bytes(5000, 64, 8)
+    route, room, layer = (lib.q4_moe_route_workspace_bytes, lib.q4_moe_experts_workspace_bytes,
+                          lib.q4_moe_layer_workspace_bytes)
+    assert route(0, 8, 64) == 0 and route(3, 1025, 64) == 0 and route(3, 8, 40) == 0
+    assert room(3, 64, 48, 2) == 0 and room(3, 48, 64, 2) == 0 and room(3, 64, 64, 0) == 0
+    assert layer(3, 4, 64, 64, 5) == 0 and layer(3, 4, 64, 48, 2) == 0
+    # past 1024 (row, expert) pairs the products run in pieces: no more room
+    assert room(128, 96, 64, 8) == room(5000, 96, 64, 8)
+    assert layer(3, 4, 64, 64, 2) >= route(3, 4, 64) + room(3, 64, 64, 2)
+
+
+def test_layer_argument_checks(lib):
+    def layer(x=FAKE, xd=BF16, r=FAKE, rd=BF16, bias=None, w13=FAKE, s13=FAKE, w2=FAKE, s2=FAKE, y=FAKE, M=4, E=8, H=64,
+              I=32, k=2, ws=FAKE, wb=1 << 30):
+        return lib.q4_moe_layer(x, xd, r, rd, bias, w13, s13, w2, s2, y, M, E, H, I, k, 1, ws, wb, None)
+
+    for bad in ("x", "r", "w13", "s13", "w2", "s2", "y"):
+        assert layer(**{bad: None}) == _lib.Q4_ERR_NULL
+    assert layer(xd=F32) == _lib.Q4_ERR_ENUM
+    assert layer(rd=F16) == _lib.Q4_ERR_ENUM
+    for kw in ({"M": 0}, {"E": 0}, {"E": 1025}, {"k": 0}, {"k": 9}, {"H": 48}, {"I": 16}, {"I": (1 << 17) + 32}):
+        assert layer(**kw) == _lib.Q4_ERR_SHAPE, kw
+    for kw in ({"x": FAKE + 8}, {"r": FAKE + 8}, {"bias": FAKE + 2}, {"w13": FAKE + 8}, {"s13": FAKE + 4},
+               {"w2": FAKE + 8}, {"s2": FAKE + 4}, {"y": FAKE + 2}, {"ws": FAKE + 16}):
+        assert layer(**kw) == _lib.Q4_ERR_ALIGN, kw
+    assert layer(wb=lib.q4_moe_layer_workspace_bytes(4, 8, 64, 32, 2) - 1) == _lib.Q4_ERR_WORKSPACE
+    assert layer(ws=None) == _lib.Q4_ERR_WORKSPACE
+    assert lib.q4_last_hip_error() == 0

@@ -69,7 +69,7 @@ def check_route(x, router, bias, topk, renormalize, what):
 
 @pytest.mark.parametrize("M,E,K,topk", [(1, 1, 32, 1), (1, 8, 64, 2), (2, 17, 96, 17), (3, 60, 896, 4),
                                         (16, 64, 2048, 8), (17, 127, 416, 6), (33, 128, 3584, 8), (5, 1024, 160, 32),
-                                        (300, 40, 224, 3)])
+                                        (300, 40, 224, 3), (530, 512, 320, 4)])
 @pytest.mark.parametrize("xt,rt", [("bf16", "bf16"), ("f16", "f32"), ("f16", "f16"), ("bf16", "f32")])
 def test_route(M, E, K, topk, xt, rt):
     gu.note("moe_route M=%d E=%d K=%d topk=%d %s %s" % (M, E, K, topk, xt, rt))
@@ -315,6 +315,30 @@ def test_rows_do_not_depend_on_the_batch(H, I):
         assert torch.equal(part.view(torch.int32), whole[70 - M:].view(torch.int32)), M
 
 
+@pytest.mark.parametrize("M,E,H,I,topk,xt", [(1, 8, 96, 64, 2, "bf16"), (4, 128, 288, 32, 8, "f16"),
+                                              (16, 64, 512, 96, 5, "bf16"), (17, 64, 512, 96, 5, "bf16"),
+                                              (9, 120, 160, 32, 3, "bf16"), (3, 5, 4256, 32, 2, "bf16"),
+                                              (300, 12, 64, 32, 6, "bf16"), (300, 12, 64, 32, 6, "f16")])
+@pytest.mark.parametrize("renormalize", [True, False])
+def test_layer_is_route_and_experts(M, E, H, I, topk, xt, renormalize):
+    """The whole layer in one call, in each of its forms: the bits of its two parts."""
+    gu.note("moe M=%d E=%d H=%d I=%d topk=%d %s" % (M, E, H, I, topk, xt))
+    layer = Layer(E, H, I, M + E)
+    g = gen(M + E)
+    x = torch.randn(M, H, generator=g).to(DTYPES[xt]).cuda()
+    r = (torch.randn(E, H, generator=g) / H**0.5).cuda()
+    bias = torch.randn(E, generator=g).cuda()
+    bias[E // 2] = -float("inf")
+    ids, w = q4.moe_route(x, r, topk, bias, renormalize)
+    ref = q4.moe_experts(x, ids, w, layer.w13, layer.w2)
+    y = q4.moe(x, r, layer.w13, layer.w2, topk, bias, renormalize)
+    torch.cuda.synchronize()
+    assert torch.equal(y.view(torch.int32), ref.view(torch.int32))
+    none = q4.moe(x, r, layer.w13, layer.w2, topk, torch.full_like(bias, -float("inf")), renormalize)
+    torch.cuda.synchronize()
+    assert (none == 0).all()
+
+
 def test_weights_from_concat():
     """The stacked weights by concat_n of separately packed experts: the same bits."""
     gu.note("moe concat_n")
@@ -396,7 +420,7 @@ def test_workspace_and_output_guards():
     x = torch.randn(M, 96, generator=g).bfloat16().cuda()
     ids, w = choose(g, M, 4, topk).cuda(), torch.rand(M, topk, generator=g).cuda()
     ref = q4.moe_experts(x, ids, w, layer.w13, layer.w2)
-    need = int(_lib.load().q4_moe_workspace_bytes(M, 64, topk))
+    need = int(_lib.load().q4_moe_experts_workspace_bytes(M, 96, 64, topk))
     ws = torch.full((need + 256,), 255, dtype=torch.uint8, device="cuda")  # NaN in every unwritten place
     room = torch.full((M * 96 + 50,), 7.0, device="cuda")
     out = room[25:25 + M * 96].view(M, 96)
@@ -441,6 +465,10 @@ def test_refusals():
         q4.moe_experts(x, ids, w, layer.w2, layer.w13)
     with pytest.raises(TypeError):
         q4.moe_experts(x, ids, w, layer.d13, layer.w2)
+    with pytest.raises(ValueError):
+        q4.moe(x, r[:3], layer.w13, layer.w2, 2)
+    with pytest.raises(ValueError):
+        q4.moe(x, r, layer.w13, layer.w2, 5)
     with pytest.raises(ValueError):
         q4.moe_experts(x[:, :64].contiguous(), ids, w, layer.w13, layer.w2)
     with pytest.raises(q4.Q4Error):
