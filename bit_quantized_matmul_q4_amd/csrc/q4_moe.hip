@@ -23,6 +23,7 @@
 #include <stdint.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "q4_device.hpp"
 #include "q4_launch.hpp"
@@ -287,6 +288,7 @@ __device__ __forceinline__ void choose_rows(const Choice &ch, int m0, int rows, 
         const int row = p / E, e = p - row * E;
         const uint64_t key = keys[p], *k = keys + row * E;
         int rank = 0;
+#pragma unroll 8
         for (int f = at; f < E; f += share) {
             const uint64_t o = k[f];
             rank += (o > key) | ((o == key) & (f < e));
@@ -329,14 +331,14 @@ __device__ __forceinline__ void choose_rows(const Choice &ch, int m0, int rows, 
 }
 
 // A workgroup a row; with x16, the last wave takes the row to binary16 first.
-__global__ __launch_bounds__(256) void q4_moe_select_kernel(Choice ch, int *__restrict__ ids,
+__global__ __launch_bounds__(512) void q4_moe_select_kernel(Choice ch, int *__restrict__ ids,
                                                             float *__restrict__ weights,
                                                             const uint16_t *__restrict__ x,
                                                             uint16_t *__restrict__ x16, int *__restrict__ lift, int K)
 {
     extern __shared__ double row[];  // E keys, then topk chosen logits
     const size_t m = blockIdx.x;
-    if (x16 && threadIdx.x >= 192)
+    if (x16 && threadIdx.x >= 448)
         lift_row(x + m * K, x16 + m * K, lift + m, K);
     choose_rows<int>(ch, (int)m, 1, (uint64_t *)row, row + ch.E, nullptr, ids, weights, true);
 }
@@ -410,93 +412,61 @@ __device__ __forceinline__ float quad_scale(u32x2 s, int j)
 __device__ __forceinline__ f32x4 dot16(u32x4 a, u32x4 b, f32x4 c) { return blockdot_acc<false>(a, b, c); }
 
 // Up to kFused compares of two logits the gate/up kernel chooses the experts
-// itself, so that the layer is three launches: every workgroup ranks all rows,
-// and the first writes the choice for the down kernel.
+// itself, so that the layer is four launches instead of five: every workgroup
+// ranks all rows, and the first writes the choice for the down kernel.
 constexpr int kFused = 16384;
-
-// The blockIdx.y-th of the chosen experts, and its slots in `list` -> their
-// count, or -1 if fewer experts are chosen.  By the whole workgroup.  Up to 64
-// slots every wave finds them alone (experts in the order of their first
-// slot, all waves writing the same list), so that its loads start at once;
-// more go through a bitmap in LDS (in the order of their numbers).
-struct Found {
-    uint32_t seen[kExperts / 32];
-    uint16_t list[kSlots];
-    int16_t who[kSlots];  // the slots' experts, -1 for none
-    int count;
-};
 
 __device__ __forceinline__ int slot_expert(int id, int E) { return id >= 0 && id < E ? id : -1; }
 
+// The expert of a workgroup and its slots.
+struct Found {
+    uint16_t list[kSlots];
+    int16_t who[kSlots];  // the slots' experts where this kernel chose them
+};
+
+// Workgroup `nth` of a grid of min(n, E): with as many slots as experts or
+// more, it is expert nth's; else it is slot nth's expert's, if that is the
+// expert's first slot.  Every wave finds its slots alone (a compare and a
+// ballot for 64 slots), without a barrier, all writing the same list, and
+// `start` sends for its weights as soon as the expert is known.  -> how many
+// slots, 0 for a workgroup without work.
 template <typename START>
 __device__ __forceinline__ int find_expert(Found &f, int n, const int *ids, bool known, int E, int nth, START start)
 {
-    const int tid = threadIdx.x, lane = tid & 63;
-    if (n <= 64) {
-        const int id = lane < n ? (known ? (int)f.who[lane] : slot_expert(ids[lane], E)) : -1;
-        uint64_t left = __ballot(id >= 0), mine = 0;
-        int e = -1;
-        for (int i = 0; left; ++i) {
-            const int v = __builtin_amdgcn_readlane(id, __builtin_ctzll(left));
-            const uint64_t same = __ballot(id == v);
-            if (i == nth) {
-                e = v;
-                mine = same;
-                break;
-            }
-            left &= ~same;
-        }
+    const int lane = threadIdx.x & 63;
+    auto who = [&](int s) { return known ? (int)f.who[s] : slot_expert(ids[s], E); };
+    const bool by_slot = n < E;
+    int e = nth;
+    if (by_slot) {
+        e = __builtin_amdgcn_readfirstlane(who(nth));
         if (e < 0)
-            return -1;
-        start(e);
-        if (mine >> lane & 1)
-            f.list[__popcll(mine & ((1ull << lane) - 1))] = (uint16_t)lane;
-        __threadfence_block();
-        return __popcll(mine);
+            return 0;
     }
-    if (tid < kExperts / 32)
-        f.seen[tid] = 0;
-    if (!known)
-        for (int s = tid; s < n; s += blockDim.x)
-            f.who[s] = (int16_t)slot_expert(ids[s], E);
-    __syncthreads();
-    for (int s = tid; s < n; s += blockDim.x)
-        if (f.who[s] >= 0)
-            atomicOr(&f.seen[f.who[s] >> 5], 1u << (f.who[s] & 31));
-    __syncthreads();
-    uint32_t bits = lane < kExperts / 32 ? f.seen[lane] : 0;
-    const int mine = __popc(bits);
-    int before = mine;
+    int count = 0;
+    bool started = false;
+    for (int s0 = 0; s0 < n; s0 += 256) {
+        int id[4];
 #pragma unroll
-    for (int d = 1; d < 32; d *= 2) {
-        const int v = __shfl_up(before, d);
-        if (lane >= d)
-            before += v;
-    }
-    int left = nth - (before - mine);
-    const bool here = lane < kExperts / 32 && left >= 0 && left < mine;
-    const uint64_t owner = __ballot(here);
-    if (!owner)
-        return -1;
-    if (here)
-        for (; left > 0; --left)
-            bits &= bits - 1;
-    const int e = __builtin_amdgcn_readlane(32 * lane + __ffs(bits) - 1, __builtin_ctzll(owner));
-    start(e);
-    if (tid < 64) {
-        int count = 0;
-        for (int s0 = 0; s0 < n; s0 += 64) {
-            const bool hit = s0 + lane < n && f.who[s0 + lane] == e;
-            const uint64_t mask = __ballot(hit);
-            if (hit)
-                f.list[count + __popcll(mask & ((1ull << lane) - 1))] = (uint16_t)(s0 + lane);
+        for (int i = 0; i < 4; ++i)
+            id[i] = s0 + 64 * i + lane < n ? who(s0 + 64 * i + lane) : -1;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint64_t mask = __ballot(id[i] == e);
+            if (!mask)
+                continue;
+            if (!started) {
+                if (by_slot && s0 + 64 * i + __builtin_ctzll(mask) != nth)
+                    return 0;
+                start(e);
+                started = true;
+            }
+            if (mask >> lane & 1)
+                f.list[count + __popcll(mask & ((1ull << lane) - 1))] = (uint16_t)(s0 + 64 * i + lane);
             count += __popcll(mask);
         }
-        if (lane == 0)
-            f.count = count;
     }
-    __syncthreads();
-    return __builtin_amdgcn_readfirstlane(f.count);
+    __threadfence_block();
+    return count;
 }
 
 // What a workgroup multiplies: four tiles of 16 columns of one expert's weight
@@ -546,6 +516,61 @@ struct RowsX {
     }
     __device__ __forceinline__ f32x4 dot(int j, u32x4 b) const { return blockdot<false>(x[Slots<R>::operand(j)], b); }
     __device__ __forceinline__ float scale(float d, int, int) const { return d; }
+};
+
+// h as the gate/up kernel leaves it.
+struct DownIn {
+    const uint16_t *hi, *lo;
+    const int *shift;
+    int n, I, shifts;  // slots, values and powers of two of a slot
+};
+
+// A row's operands of h for one quad: both halves, and the powers of two of the
+// rows whose values the lane group accumulates.
+template <int R>
+struct RowsH {
+    u32x4 hi[R], lo[R], shift[R];
+    struct In {
+        __amdgpu_buffer_rsrc_t hi, lo, shift;
+        uint32_t at, shift_at[R];
+        int nb;
+    };
+    static __device__ __forceinline__ In in(const DownIn &h, const uint16_t *list, int rows, int nb)
+    {
+        const int lane = threadIdx.x & 63, g = lane >> 4, row = Slots<R>::row(lane & 15);
+        In i;
+        i.hi = buffer_of(h.hi, (size_t)h.n * h.I * 2);
+        i.lo = buffer_of(h.lo, (size_t)h.n * h.I * 2);
+        i.shift = buffer_of(h.shift, (size_t)h.n * h.shifts * 4);
+        i.at = row < rows ? (uint32_t)list[row] * 2u * h.I + 16 * g : kNowhere;
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+            i.shift_at[r] = 4 * r + g < rows ? (uint32_t)list[4 * r + g] * 4u * h.shifts : kNowhere;
+        i.nb = nb;
+        return i;
+    }
+    __device__ __forceinline__ void load(const In &in, int q)
+    {
+        const int c = threadIdx.x & 15;
+#pragma unroll
+        for (int o = 0; o < R; ++o) {  // (blocks past the end of a short last quad: zero)
+            const int b = Slots<R>::block(o, c);
+            const uint32_t at = 4 * q + b < in.nb ? in.at + 64 * b : kNowhere;
+            hi[o] = load16(in.hi, at, 256 * q);
+            lo[o] = load16(in.lo, at, 256 * q);
+        }
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+            shift[r] = load16(in.shift, in.shift_at[r], 16 * q);
+    }
+    __device__ __forceinline__ f32x4 dot(int j, u32x4 b) const
+    {
+        return dot16(hi[Slots<R>::operand(j)], b, blockdot<false>(lo[Slots<R>::operand(j)], b));
+    }
+    __device__ __forceinline__ float scale(float d, int r, int j) const
+    {
+        return __builtin_ldexpf(d, (int)shift[r][j]);
+    }
 };
 
 // The products of up to 4 R rows (operands `rows`) with the wave's run of L <= 4
@@ -635,308 +660,193 @@ __device__ __forceinline__ float join_runs(const float *part, int waves, int til
     return tree_sum<8>(v, waves);
 }
 
-// What the gate/up kernel reads and writes.
-struct UpArgs {
+// gate and up: a unit is two tiles of gate and two of up, so that it ends with
+// 32 values of h, one block of the down product.
+struct Up {
     const uint16_t *x;
     const int *lift;  // or null: x as given
     uint16_t *hi, *lo;
     int *shift;
-    int H, I, shifts;
+    int M, topk, H, I, shifts;
+
+    template <int R>
+    using Rows = RowsX<R>;
+    __host__ __device__ int units() const { return I / 32; }
+    __device__ __forceinline__ FourTiles tiles(const uint8_t *wq, const uint16_t *scales, int e, int unit, int G) const
+    {
+        const size_t gate = (size_t)e * (2 * I / 16) + 2 * unit, up = gate + I / 16;
+        return FourTiles{Tile(wq, scales, gate, G), Tile(wq, scales, gate + 1, G), Tile(wq, scales, up, G),
+                         Tile(wq, scales, up + 1, G)};
+    }
+    template <int R>
+    __device__ __forceinline__ typename RowsX<R>::In in(const uint16_t *list, int rows, int nb) const
+    {
+        const int row = Slots<R>::row(threadIdx.x & 15);
+        const bool live = row < rows;
+        return RowsX<R>::in(x, M, H, nb, live ? list[row] / topk : 0, live);
+    }
+    // (loaded before the products, used after them)
+    __device__ __forceinline__ int before(const uint16_t *list, int rows) const
+    {
+        return lift && (int)threadIdx.x < rows ? -lift[list[threadIdx.x] / topk] : 0;
+    }
+    // 32 lanes a row: the trees, the activation, the block's power of two
+    template <int R>
+    __device__ __forceinline__ void after(const float *part, int waves, const int *back, const uint16_t *list, int rows,
+                                          int unit) const
+    {
+        for (int o = threadIdx.x; o < rows * 32; o += blockDim.x) {
+            const int i = o >> 5, col = o & 31;
+            const float gate = __builtin_ldexpf(join_runs<R>(part, waves, col >> 4, i, col & 15), back[i]);
+            const float up = __builtin_ldexpf(join_runs<R>(part, waves, 2 + (col >> 4), i, col & 15), back[i]);
+            const float h = gate / (1.f + __builtin_expf(-gate)) * up;
+            float top = __builtin_fabsf(h) < __builtin_inff() ? __builtin_fabsf(h) : 0.f;
+#pragma unroll
+            for (int d = 1; d < 32; d *= 2)
+                top = __builtin_fmaxf(top, __shfl_xor(top, d));
+            const int raise = lift_of(top);
+            const float v = __builtin_ldexpf(h, raise);
+            const _Float16 vh = (_Float16)v;
+            const float rest = v - (float)vh;
+            const _Float16 vl = __builtin_fabsf(v) < __builtin_inff() ? (_Float16)rest : (_Float16)0.f;
+            const size_t slot = list[i];
+            const size_t k = slot * I + 32 * unit + col;
+            hi[k] = __builtin_bit_cast(uint16_t, vh);
+            lo[k] = __builtin_bit_cast(uint16_t, vl);
+            if (col == 0)
+                shift[slot * shifts + unit] = -raise;
+        }
+    }
 };
 
-// A group of up to 4 R of the expert's rows: products, activation, h.
-template <int R>
-__device__ __forceinline__ void up_rows(const UpArgs &u, const FourTiles &tiles, Weights &first, const uint16_t *list,
-                                        int rows, int M, int topk, int L, const Plan &plan, float *part, int *back)
-{
-    const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), c = tid & 15;
-    const int waves = blockDim.x >> 6;
-    const int row = Slots<R>::row(c);
-    const bool live = row < rows;
-    if (tid < rows)
-        back[tid] = u.lift ? -u.lift[list[tid] / topk] : 0;
-    const auto in = RowsX<R>::in(u.x, M, u.H, plan.nb, live ? list[row] / topk : 0, live);
-    multiply_run<R, RowsX<R>>(tiles, first, in, wave * L, L, plan, part + wave * 4 * R * 64);
-    __syncthreads();
-    // 32 lanes a row: the trees, the activation, the block's power of two
-    for (int o = tid; o < rows * 32; o += blockDim.x) {
-        const int i = o >> 5, col = o & 31;
-        const float gate = __builtin_ldexpf(join_runs<R>(part, waves, col >> 4, i, col & 15), back[i]);
-        const float up = __builtin_ldexpf(join_runs<R>(part, waves, 2 + (col >> 4), i, col & 15), back[i]);
-        const float h = gate / (1.f + __builtin_expf(-gate)) * up;
-        float top = __builtin_fabsf(h) < __builtin_inff() ? __builtin_fabsf(h) : 0.f;
-#pragma unroll
-        for (int d = 1; d < 32; d *= 2)
-            top = __builtin_fmaxf(top, __shfl_xor(top, d));
-        const int raise = lift_of(top);
-        const float v = __builtin_ldexpf(h, raise);
-        const _Float16 vh = (_Float16)v;
-        const float rest = v - (float)vh;
-        const _Float16 vl = __builtin_fabsf(v) < __builtin_inff() ? (_Float16)rest : (_Float16)0.f;
-        const size_t slot = list[i];
-        const size_t k = slot * u.I + 32 * blockIdx.x + col;
-        u.hi[k] = __builtin_bit_cast(uint16_t, vh);
-        u.lo[k] = __builtin_bit_cast(uint16_t, vl);
-        if (col == 0)
-            u.shift[slot * u.shifts + blockIdx.x] = -raise;
-    }
-}
+// down: a unit is 64 columns, so that h is read once for four tiles; each (row,
+// expert) pair's product goes to memory (t [slot][H]).
+struct Down {
+    DownIn h;
+    float *t;
+    int H;
 
-// gate and up.  grid = (I / 32, experts that can be chosen).  A workgroup owns
-// two tiles of gate and two of up of one expert, so that it ends with 32
-// values of h: one block of the down product.  An expert's rows go 4, 8 or 16
-// (at most 4 RM) at a time, by how many are left.
-template <int RM>
-__global__ __launch_bounds__(512) void q4_moe_up_kernel(Choice ch, UpArgs u, int *__restrict__ ids,
-                                                        float *__restrict__ weights,
-                                                        const uint8_t *__restrict__ wq,
-                                                        const uint16_t *__restrict__ scales, int L, Plan plan)
+    template <int R>
+    using Rows = RowsH<R>;
+    __host__ __device__ int units() const { return (H + 63) / 64; }
+    // (past the last column: the last tile, its values are not stored)
+    __device__ __forceinline__ FourTiles tiles(const uint8_t *wq, const uint16_t *scales, int e, int unit, int G) const
+    {
+        const size_t base = (size_t)e * (H / 16);
+        const int at = 4 * unit, last = H / 16 - 1;
+        return FourTiles{Tile(wq, scales, base + at, G), Tile(wq, scales, base + min(at + 1, last), G),
+                         Tile(wq, scales, base + min(at + 2, last), G), Tile(wq, scales, base + min(at + 3, last), G)};
+    }
+    template <int R>
+    __device__ __forceinline__ typename RowsH<R>::In in(const uint16_t *list, int rows, int nb) const
+    {
+        return RowsH<R>::in(h, list, rows, nb);
+    }
+    __device__ __forceinline__ int before(const uint16_t *, int) const { return 0; }
+    template <int R>
+    __device__ __forceinline__ void after(const float *part, int waves, const int *, const uint16_t *list, int rows,
+                                          int unit) const
+    {
+        for (int o = threadIdx.x; o < rows * 64; o += blockDim.x) {
+            const int i = o >> 6, col = 64 * unit + (o & 63);
+            if (col < H)
+                t[(size_t)list[i] * H + col] = join_runs<R>(part, waves, (o & 63) >> 4, i, o & 15);
+        }
+    }
+};
+
+// One product of the layer.  grid = (units, min(slots, E)): a unit of four tiles
+// of one expert a workgroup, its waves on runs of L segments of K.  An expert's
+// rows go 4, 8 or 16 (at most 4 RM) at a time, by how many are left; the
+// weights of the next group's first quad are on their way while this one's
+// sums are joined, and the sums' room in LDS alternates, so that one barrier
+// a group is enough.
+template <typename OP, int RM>
+__global__ __launch_bounds__(512) void q4_moe_product_kernel(Choice ch, OP op, int *__restrict__ ids,
+                                                             float *__restrict__ weights,
+                                                             const uint8_t *__restrict__ wq,
+                                                             const uint16_t *__restrict__ scales, int L, Plan plan)
 {
-    extern __shared__ __attribute__((aligned(16))) float part[];  // [wave][tile][r][lane]
+    extern __shared__ __attribute__((aligned(16))) float room[];  // 2 x [wave][tile][r][lane]
     __shared__ Found found;
-    __shared__ int back[16];
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int n = ch.M * ch.topk;
+    __shared__ int back[2][16];
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), waves = blockDim.x >> 6;
     if (ch.parts) {
-        uint64_t *keys = (uint64_t *)part;
+        uint64_t *keys = (uint64_t *)room;
         choose_rows<int16_t>(ch, 0, ch.M, keys, (double *)(keys + ch.M * ch.E), found.who, ids, weights,
                              blockIdx.x == 0 && blockIdx.y == 0);
         __syncthreads();  // (the keys' room is the products' next)
     }
+    const int qa = (wave * L * plan.G) >> plan.log2S;
     FourTiles tiles;
     Weights first;
-    const int qa = (wave * L * plan.G) >> plan.log2S;
-    const int count = find_expert(found, n, ids, ch.parts != nullptr, ch.E, blockIdx.y, [&](int e) {
-        const size_t gate = (size_t)e * (2 * u.I / 16) + 2 * blockIdx.x, up = gate + u.I / 16;
-        tiles = FourTiles{Tile(wq, scales, gate, plan.G), Tile(wq, scales, gate + 1, plan.G),
-                          Tile(wq, scales, up, plan.G), Tile(wq, scales, up + 1, plan.G)};
+    const int count = find_expert(found, ch.M * ch.topk, ids, ch.parts != nullptr, ch.E, blockIdx.y, [&](int e) {
+        tiles = op.tiles(wq, scales, e, blockIdx.x, plan.G);
         first.load(tiles, qa);
     });
+    int turn = 0;
     for (int r0 = 0; r0 < count;) {
         const int left = count - r0;
-        if (r0) {
-            __syncthreads();  // the last group's sums are read
-            first.load(tiles, qa);
-        }
-        if (RM == 1 || left <= 4) {
-            up_rows<1>(u, tiles, first, found.list + r0, min(left, 4), ch.M, ch.topk, L, plan, part, back);
-            r0 += 4;
-        } else if (RM == 2 || left <= 8) {
-            up_rows<RM == 1 ? 1 : 2>(u, tiles, first, found.list + r0, min(left, 8), ch.M, ch.topk, L, plan, part, back);
-            r0 += 8;
-        } else {
-            up_rows<RM>(u, tiles, first, found.list + r0, min(left, 16), ch.M, ch.topk, L, plan, part, back);
-            r0 += 16;
-        }
+        const uint16_t *list = found.list + r0;
+        float *part = room + turn * waves * 4 * RM * 64;
+        auto group = [&](auto r) {
+            constexpr int R = decltype(r)::value;
+            const int rows = min(left, 4 * R);
+            const int b = op.before(list, rows);
+            multiply_run<R, typename OP::template Rows<R>>(tiles, first, op.template in<R>(list, rows, plan.nb),
+                                                           wave * L, L, plan, part + wave * 4 * R * 64);
+            if ((int)threadIdx.x < 16)
+                back[turn][threadIdx.x] = b;
+            r0 += 4 * R;
+            if (r0 < count)
+                first.load(tiles, qa);
+            __syncthreads();
+            op.template after<R>(part, waves, back[turn], list, rows, blockIdx.x);
+        };
+        if (RM == 1 || left <= 4)
+            group(std::integral_constant<int, 1>());
+        else if (RM == 2 || left <= 8)
+            group(std::integral_constant<int, RM == 1 ? 1 : 2>());
+        else
+            group(std::integral_constant<int, RM>());
+        turn ^= 1;
     }
 }
 
-// h as the gate/up kernel leaves it.
-struct DownIn {
-    const uint16_t *hi, *lo;
-    const int *shift;
-    int n, I, shifts;  // slots, values and powers of two of a slot
-};
-
-template <int R>
-struct DownRows {
-    u32x4 hi[R], lo[R];
-    u32x4 shift[R];  // of the quad's blocks
-};
-
-// `rows` rows of `list` (up to 4 R) by the run of L segments from segment sa
-// of one tile of one expert: codes D quads ahead, h one.
-template <int R>
-__device__ __forceinline__ void down_rows(const DownIn &in, const uint16_t *list, int rows, const Tile &tile, int sa,
-                                          int L, const Plan &plan, float *root, int runs, int run)
+// y[m] = sum_j weights[m][j] t[m, j], in the order of j.  grid = (1024 columns,
+// rows).
+__global__ __launch_bounds__(256) void q4_moe_join_kernel(const int *__restrict__ ids, const float *__restrict__ weights,
+                                                          const float *__restrict__ t, float *__restrict__ y, int topk,
+                                                          int E, int H)
 {
-    constexpr int D = R == 1 ? 4 : 2;
-    const int lane = threadIdx.x & 63, c = lane & 15, g = lane >> 4;
-    const Dequant<false> dq;
-    const int qa = (sa * plan.G) >> plan.log2S, qb = ((sa + L) * plan.G) >> plan.log2S;
-    const uint32_t w_at = 16 * lane, s_at = 8 * c;
-    u32x4 codes[D];
-    u32x2 sc[D];
+    const int col = (blockIdx.x * 256 + threadIdx.x) * 4;
+    const size_t m = blockIdx.y;
+    if (col >= H)
+        return;
+    f32x4 sum = {0.f, 0.f, 0.f, 0.f};
+    for (int j0 = 0; j0 < topk; j0 += 8) {
+        f32x4 v[8];
+        bool has[8];
 #pragma unroll
-    for (int i = 0; i < D; ++i)
-        if (qa + i < qb) {
-            codes[i] = load_codes(tile.w, w_at, qa + i);
-            sc[i] = load_scales(tile.s, s_at, qa + i);
-        }
-    const __amdgpu_buffer_rsrc_t hb = buffer_of(in.hi, (size_t)in.n * in.I * 2),
-                                 lb = buffer_of(in.lo, (size_t)in.n * in.I * 2),
-                                 sb = buffer_of(in.shift, (size_t)in.n * in.shifts * 4);
-    const int row = Slots<R>::row(c);
-    const uint32_t h_at = row < rows ? (uint32_t)list[row] * 2u * in.I + 16 * g : kNowhere;
-    // the rows whose values this lane group accumulates
-    int mine[R];
-    uint32_t shift_at[R];
-#pragma unroll
-    for (int r = 0; r < R; ++r) {
-        mine[r] = 4 * r + g < rows ? list[4 * r + g] : -1;
-        shift_at[r] = mine[r] >= 0 ? (uint32_t)mine[r] * 4u * in.shifts : kNowhere;
-    }
-    auto load_h = [&](DownRows<R> &h, int q) {
-#pragma unroll
-        for (int o = 0; o < R; ++o) {  // (blocks past the end of a short last quad: zero)
-            const int b = Slots<R>::block(o, c);
-            const uint32_t at = 4 * q + b < plan.nb ? h_at + 64 * b : kNowhere;
-            h.hi[o] = load16(hb, at, 256 * q);
-            h.lo[o] = load16(lb, at, 256 * q);
+        for (int j = 0; j < 8; ++j) {
+            const size_t slot = m * topk + j0 + j;
+            has[j] = j0 + j < topk && slot_expert(ids[slot], E) >= 0;
+            if (has[j])
+                v[j] = *(const f32x4 *)(t + slot * H + col);
         }
 #pragma unroll
-        for (int r = 0; r < R; ++r)
-            h.shift[r] = load16(sb, shift_at[r], 16 * q);
-    };
-    TreeStack<R, float> tree;
-    float p[R];
+        for (int j = 0; j < 8; ++j)
+            if (has[j]) {
+                const float w = weights[m * topk + j0 + j];
 #pragma unroll
-    for (int r = 0; r < R; ++r)
-        p[r] = 0.f;
-    int seg = sa, end = ((sa + 1) * plan.G) >> plan.log2S;
-    DownRows<R> next;
-    load_h(next, qa);
-    for (int q0 = qa; q0 < qb; q0 += D) {
-#pragma unroll
-        for (int i = 0; i < D; ++i) {
-            const int q = q0 + i;
-            if (q < qb) {
-                const DownRows<R> h = next;
-                const u32x4 cw = codes[i];
-                const u32x2 sw = sc[i];
-                if (q + 1 < qb)
-                    load_h(next, q + 1);
-                if (q + D < qb) {
-                    codes[i] = load_codes(tile.w, w_at, q + D);
-                    sc[i] = load_scales(tile.s, s_at, q + D);
-                }
-                f32x4 v[4];
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const u32x4 b = dq(cw[j]);
-                    v[j] = dot16(h.hi[Slots<R>::operand(j)], b, blockdot<false>(h.lo[Slots<R>::operand(j)], b));
-                }
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const float d = quad_scale(sw, j);
-#pragma unroll
-                    for (int r = 0; r < R; ++r) {
-                        const int by = (int)h.shift[r][j];
-                        p[r] = __builtin_fmaf(__builtin_ldexpf(d, by), v[j][Slots<R>::comp(j, r)], p[r]);
-                    }
-                }
-                if (q + 1 == end) {
-                    if (!tree.push(p, seg - sa, L)) {
-#pragma unroll
-                        for (int r = 0; r < R; ++r)
-                            p[r] = 0.f;
-                    }
-                    ++seg;
-                    end = ((seg + 1) * plan.G) >> plan.log2S;
-                }
+                for (int i = 0; i < 4; ++i)
+                    sum[i] = __builtin_fmaf(w, v[j][i], sum[i]);
             }
-        }
     }
+    float *out = y + m * H + col;
 #pragma unroll
-    for (int r = 0; r < R; ++r)
-        if (mine[r] >= 0)
-            root[(mine[r] * runs + run) * 16 + c] = p[r];
-}
-
-// down and the sum over the chosen experts.  grid = tiles of 16 columns of y;
-// a workgroup's waves take (expert, run of segments) pairs in turn, the runs'
-// roots meet in LDS, and each output adds its experts in the order of j.
-// FEW: no expert has more than 4 rows unless a row names it twice.
-template <bool FEW>
-__global__ __launch_bounds__(1024) void q4_moe_down_kernel(const int *__restrict__ ids,
-                                                           const float *__restrict__ weights, DownIn in,
-                                                           const uint8_t *__restrict__ wq,
-                                                           const uint16_t *__restrict__ scales, float *__restrict__ y,
-                                                           int M, int topk, int E, int H, Plan plan)
-{
-    extern __shared__ __attribute__((aligned(16))) float root[];  // [slot][run][16 columns]
-    __shared__ int first[kExperts];        // an expert's rows before the scatter, their end after it
-    __shared__ uint16_t list[kSlots];      // slots in the order of their experts
-    __shared__ uint16_t active[kExperts];  // chosen experts
-    __shared__ int sums[2][16];
-    __shared__ int total;
-    const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
-    const int n = M * topk;
-    // counting sort of the slots by expert
-    first[tid] = 0;
-    __syncthreads();
-    const int id = tid < n ? ids[tid] : -1;
-    const bool valid = id >= 0 && id < E;
-    if (valid)
-        atomicAdd(&first[id], 1);
-    __syncthreads();
-    const int count = first[tid];
-    int before = count, rank = count > 0;
-    for (int d = 1; d < 64; d *= 2) {
-        const int a = __shfl_up(before, d), b = __shfl_up(rank, d);
-        if (lane >= d) {
-            before += a;
-            rank += b;
-        }
-    }
-    if (lane == 63) {
-        sums[0][wave] = before;
-        sums[1][wave] = rank;
-    }
-    __syncthreads();
-    for (int w = 0; w < wave; ++w) {
-        before += sums[0][w];
-        rank += sums[1][w];
-    }
-    if (count)
-        active[rank - 1] = (uint16_t)tid;
-    first[tid] = before - count;
-    if (tid == 1023)
-        total = rank;
-    __syncthreads();
-    // (the order of an expert's rows in the list does not matter: a row's bits
-    // do not depend on its place)
-    if (valid)
-        list[atomicAdd(&first[id], 1)] = (uint16_t)tid;
-    __syncthreads();
-    const int A = __builtin_amdgcn_readfirstlane(total), S = plan.S;
-    int runs = 1;
-    while (A * runs < 16 && 2 * runs <= S && 2 * runs * n <= kSlots)
-        runs *= 2;
-    const int L = S / runs;
-    for (int u = wave; u < A * runs; u += 16) {
-        const int a = u / runs, run = u % runs;
-        const int e = __builtin_amdgcn_readfirstlane(active[a]);
-        const int end = __builtin_amdgcn_readfirstlane(first[e]);
-        const int begin = __builtin_amdgcn_readfirstlane(a ? first[active[a - 1]] : 0);
-        const Tile tile(wq, scales, (size_t)e * (H / 16) + blockIdx.x, plan.G);
-        for (int r0 = begin; r0 < end;) {
-            const int left = end - r0;
-            if (FEW || left <= 4) {
-                down_rows<1>(in, list + r0, min(left, 4), tile, run * L, L, plan, root, runs, run);
-                r0 += 4;
-            } else {
-                down_rows<2>(in, list + r0, min(left, 8), tile, run * L, L, plan, root, runs, run);
-                r0 += 8;
-            }
-        }
-    }
-    __syncthreads();
-    for (int o = tid; o < M * 16; o += 1024) {
-        const int m = o >> 4, col = o & 15;
-        float sum = 0.f;
-        for (int j = 0; j < topk; ++j) {
-            const int slot = m * topk + j, x = ids[slot];
-            if (x < 0 || x >= E)
-                continue;
-            float v[16];
-#pragma unroll
-            for (int s = 0; s < 16; ++s)
-                v[s] = s < runs ? root[(slot * runs + s) * 16 + col] : 0.f;
-            sum = __builtin_fmaf(weights[slot], tree_sum<16>(v, runs), sum);
-        }
-        y[(size_t)m * H + 16 * blockIdx.x + col] = sum;
-    }
+    for (int i = 0; i < 4; ++i)  // (y is aligned to 4 bytes)
+        out[i] = sum[i];
 }
 
 size_t up256(size_t n) { return (n + 255) & ~(size_t)255; }
@@ -985,7 +895,7 @@ hipError_t launch_logits(const void *x, int xk, const void *router, int rk, doub
 hipError_t launch_select(const Choice &ch, int *ids, float *weights, const void *x, uint16_t *x16, int *lift, int K,
                          hipStream_t stream)
 {
-    hipLaunchKernelGGL(q4_moe_select_kernel, dim3((unsigned)ch.M), dim3(256),
+    hipLaunchKernelGGL(q4_moe_select_kernel, dim3((unsigned)ch.M), dim3(512),
                        (size_t)(ch.E + ch.topk) * sizeof(double), stream, ch, ids, weights, (const uint16_t *)x, x16,
                        lift, K);
     return hipGetLastError();
@@ -995,6 +905,7 @@ hipError_t launch_select(const Choice &ch, int *ids, float *weights, const void 
 struct MoeRoom {
     uint16_t *hi, *lo, *x16;
     int *shift, *lift;
+    float *t;
     size_t bytes;
     MoeRoom(void *base, int rows, int topk, int H, int I)
     {
@@ -1011,65 +922,78 @@ struct MoeRoom {
         shift = (int *)take(n * shifts_of(I) * 4);
         x16 = (uint16_t *)take((size_t)rows * H * 2);
         lift = (int *)take((size_t)rows * 4);
+        t = (float *)take(n * H * 4);
         bytes = at;
     }
     // an expert row's powers of two, padded to whole quads
     static int shifts_of(int I) { return (I / 32 + 3) / 4 * 4; }
 };
 
-// The largest group of rows the gate/up kernel is built for: by the rows an
-// expert gets on average.
-int up_group(int n, int E)
+// The largest group of rows a product is built for: by the rows an expert gets
+// on average.
+int row_group(int n, int E)
 {
     const int rows = n / std::min(n, E);
     return rows <= 1 ? 1 : rows <= 7 ? 2 : 4;
 }
 
-// gate/up and down of a piece of rows; ch.parts: the gate/up kernel chooses.
+template <typename OP, int RM>
+hipError_t launch_product_r(const Choice &ch, const OP &op, int *ids, float *weights, const uint8_t *wq,
+                            const uint16_t *scales, const Plan &plan, hipStream_t stream)
+{
+    const int n = ch.M * ch.topk;
+    const dim3 grid((unsigned)op.units(), (unsigned)std::min(n, ch.E));
+#ifndef W8
+#define W8 1024
+#endif
+    // eight waves a workgroup while the card is not full, else four
+    const int waves = std::min(plan.S, (size_t)grid.x * grid.y >= W8 ? 4 : 8);
+    size_t lds = (size_t)2 * waves * 4 * RM * 64 * sizeof(float);
+    if (ch.parts)
+        lds = std::max(lds, (size_t)(ch.M * ch.E + n) * sizeof(double));
+    if (lds > 48 * 1024) {
+        const hipError_t e = hipFuncSetAttribute((const void *)q4_moe_product_kernel<OP, RM>,
+                                                 hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
+        if (e != hipSuccess)
+            return e;
+    }
+    hipLaunchKernelGGL((q4_moe_product_kernel<OP, RM>), grid, dim3(64 * waves), lds, stream, ch, op, ids, weights,
+                       wq, scales, plan.S / waves, plan);
+    return hipGetLastError();
+}
+
+template <typename OP>
+hipError_t launch_product(int most, const Choice &ch, const OP &op, int *ids, float *weights, const uint8_t *wq,
+                          const uint16_t *scales, const Plan &plan, hipStream_t stream)
+{
+    const int RM = std::min(most, row_group(ch.M * ch.topk, ch.E));
+    if (RM == 1)
+        return launch_product_r<OP, 1>(ch, op, ids, weights, wq, scales, plan, stream);
+    if (RM == 2)
+        return launch_product_r<OP, 2>(ch, op, ids, weights, wq, scales, plan, stream);
+    if constexpr (std::is_same<OP, Up>::value)
+        return launch_product_r<OP, 4>(ch, op, ids, weights, wq, scales, plan, stream);
+    return hipErrorInvalidValue;
+}
+
+// The products of a piece of rows; ch.parts: the gate/up kernel chooses.
 hipError_t products(const Choice &ch, const uint16_t *x, const int *lift, int *ids, float *weights, const uint8_t *w13,
                     const uint16_t *s13, const uint8_t *w2, const uint16_t *s2, float *y, int H, int I,
                     const MoeRoom &room, hipStream_t stream)
 {
-    const Plan up = make_plan(H), down = make_plan(I);
     const int n = ch.M * ch.topk, shifts = MoeRoom::shifts_of(I);
-    const dim3 grid((unsigned)(I / 32), (unsigned)std::min(n, ch.E));
-    // eight waves a workgroup while the card is not full, else four
-    const int waves = std::min(up.S, (size_t)grid.x * grid.y >= 1024 ? 4 : 8);
-    const int RM = up_group(n, ch.E);
-    size_t lds_up = (size_t)waves * 4 * RM * 64 * sizeof(float);
-    if (ch.parts)
-        lds_up = std::max(lds_up, (size_t)(ch.M * ch.E + n) * sizeof(double));
-    // roots: [slot][run][16], where the kernel keeps slots x runs within kSlots
-    const size_t lds_down = (size_t)std::min(kSlots, 16 * n) * 16 * sizeof(float);
-    const bool few = ch.M <= 4;
-    const void *down_fn = few ? (const void *)q4_moe_down_kernel<true> : (const void *)q4_moe_down_kernel<false>;
-    // (with the kernel's fixed parts, the largest pass the default limit)
-    hipError_t e = hipSuccess;
-    if (lds_down > 32 * 1024)
-        e = hipFuncSetAttribute(down_fn, hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds_down);
+    const Up up{x, lift, room.hi, room.lo, room.shift, ch.M, ch.topk, H, I, shifts};
+    hipError_t e = launch_product(4, ch, up, ids, weights, w13, s13, make_plan(H), stream);
     if (e != hipSuccess)
         return e;
-    const UpArgs u{x, lift, room.hi, room.lo, room.shift, H, I, shifts};
-    const int L = up.S / waves;
-    if (RM == 1)
-        hipLaunchKernelGGL(q4_moe_up_kernel<1>, grid, dim3(64 * waves), lds_up, stream, ch, u, ids, weights, w13, s13, L,
-                           up);
-    else if (RM == 2)
-        hipLaunchKernelGGL(q4_moe_up_kernel<2>, grid, dim3(64 * waves), lds_up, stream, ch, u, ids, weights, w13, s13, L,
-                           up);
-    else
-        hipLaunchKernelGGL(q4_moe_up_kernel<4>, grid, dim3(64 * waves), lds_up, stream, ch, u, ids, weights, w13, s13, L,
-                           up);
-    e = hipGetLastError();
+    Choice given = ch;
+    given.parts = nullptr;
+    const Down down{{room.hi, room.lo, room.shift, n, I, shifts}, room.t, H};
+    e = launch_product(2, given, down, ids, weights, w2, s2, make_plan(I), stream);
     if (e != hipSuccess)
         return e;
-    const DownIn in{room.hi, room.lo, room.shift, n, I, shifts};
-    if (few)
-        hipLaunchKernelGGL(q4_moe_down_kernel<true>, dim3((unsigned)(H / 16)), dim3(1024), lds_down, stream, ids, weights,
-                           in, w2, s2, y, ch.M, ch.topk, ch.E, H, down);
-    else
-        hipLaunchKernelGGL(q4_moe_down_kernel<false>, dim3((unsigned)(H / 16)), dim3(1024), lds_down, stream, ids,
-                           weights, in, w2, s2, y, ch.M, ch.topk, ch.E, H, down);
+    hipLaunchKernelGGL(q4_moe_join_kernel, dim3((unsigned)((H + 1023) / 1024), (unsigned)ch.M), dim3(256), 0, stream, ids,
+                       weights, room.t, y, ch.topk, ch.E, H);
     return hipGetLastError();
 }
 
