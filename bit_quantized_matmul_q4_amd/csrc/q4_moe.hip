@@ -477,9 +477,12 @@ struct FourTiles {
 struct Weights {
     u32x4 codes[4];
     u32x2 scales[4];
-    __device__ __forceinline__ void load(const FourTiles &f, int q)
+    // Quad q of the tiles, or nothing from quad qb on: always the same loads, so
+    // that the wait for the quad before never has to be a wait for them too.
+    __device__ __forceinline__ void load(const FourTiles &f, int q, int qb)
     {
-        const uint32_t lane = threadIdx.x & 63, w_at = 16 * lane, s_at = 8 * (lane & 15);
+        const uint32_t lane = threadIdx.x & 63;
+        const uint32_t w_at = q < qb ? 16 * lane : kNowhere, s_at = q < qb ? 8 * (lane & 15) : kNowhere;
         codes[0] = load_codes(f.t0.w, w_at, q);
         codes[1] = load_codes(f.t1.w, w_at, q);
         codes[2] = load_codes(f.t2.w, w_at, q);
@@ -490,6 +493,13 @@ struct Weights {
         scales[3] = load_scales(f.t3.s, s_at, q);
     }
 };
+
+// Keeps loads ahead of what follows them (no instructions).
+__device__ __forceinline__ void issue_fence()
+{
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
+}
 
 // The rows' operands of one quad: x as it is.
 template <int R>
@@ -573,22 +583,24 @@ struct RowsH {
     }
 };
 
-// The products of up to 4 R rows (operands `rows`) with the wave's run of L <= 4
+// The products of up to 4 R rows (operands ROWS) with the wave's run of L
 // segments of four tiles, a quad of both loaded ahead (the first quad's
-// weights by the caller); the run's roots go to root [tile][r][lane].
+// weights by the caller).  The run's part of the tree waits in the wave's own
+// LDS, stack [level][tile][r][lane] (levels that the trailing one-bits of a
+// segment's number name are merged, left operand first), and ends in level 0.
 template <int R, typename ROWS>
 __device__ __forceinline__ void multiply_run(const FourTiles &tiles, Weights &first, const typename ROWS::In &in, int sa,
-                                             int L, const Plan &plan, float *root)
+                                             int L, const Plan &plan, float *stack)
 {
     const int lane = threadIdx.x & 63;
     const Dequant<false> dq;
     const int qa = (sa * plan.G) >> plan.log2S, qb = ((sa + L) * plan.G) >> plan.log2S;
-    float p[4][R], s0[4][R], s1[4][R];
+    float p[4][R];
 #pragma unroll
     for (int t = 0; t < 4; ++t)
 #pragma unroll
         for (int r = 0; r < R; ++r)
-            p[t][r] = s0[t][r] = s1[t][r] = 0.f;
+            p[t][r] = 0.f;
     int seg = 0, end = ((sa + 1) * plan.G) >> plan.log2S;
     auto multiply = [&](const Weights &w, const ROWS &x, int q) {
 #pragma unroll
@@ -605,21 +617,22 @@ __device__ __forceinline__ void multiply_run(const FourTiles &tiles, Weights &fi
                     p[t][r] = __builtin_fmaf(x.scale(d, r, j), D[j][Slots<R>::comp(j, r)], p[t][r]);
             }
         }
-        if (q + 1 == end) {  // a segment ends: the tree's lower two levels
+        if (q + 1 == end) {  // a segment ends
+            int level = 0;
+            for (; seg >> level & 1; ++level)
+#pragma unroll
+                for (int t = 0; t < 4; ++t)
+#pragma unroll
+                    for (int r = 0; r < R; ++r)
+                        p[t][r] = stack[((level * 4 + t) * R + r) * 64 + lane] + p[t][r];
+            if (seg == L - 1)
+                level = 0;
 #pragma unroll
             for (int t = 0; t < 4; ++t)
 #pragma unroll
                 for (int r = 0; r < R; ++r) {
-                    float v = p[t][r];
-                    if (seg & 1)
-                        v = s0[t][r] + v;
-                    if (seg == 3)
-                        v = s1[t][r] + v;
-                    if (seg & 1)
-                        s1[t][r] = v;
-                    else
-                        s0[t][r] = v;
-                    p[t][r] = seg == L - 1 ? v : 0.f;
+                    stack[((level * 4 + t) * R + r) * 64 + lane] = p[t][r];
+                    p[t][r] = 0.f;
                 }
             ++seg;
             end = ((sa + seg + 1) * plan.G) >> plan.log2S;
@@ -629,35 +642,36 @@ __device__ __forceinline__ void multiply_run(const FourTiles &tiles, Weights &fi
     ROWS xa, xb;
     xa.load(in, qa);
     for (int q = qa; q < qb; q += 2) {
-        if (q + 1 < qb) {
-            second.load(tiles, q + 1);
-            xb.load(in, q + 1);
-        }
+        second.load(tiles, q + 1, qb);
+        xb.load(in, q + 1);
+        issue_fence();
         multiply(first, xa, q);
-        if (q + 1 < qb) {
-            if (q + 2 < qb) {
-                first.load(tiles, q + 2);
-                xa.load(in, q + 2);
-            }
+        first.load(tiles, q + 2, qb);
+        xa.load(in, q + 2);
+        issue_fence();
+        if (q + 1 < qb)
             multiply(second, xb, q + 1);
-        }
     }
-#pragma unroll
-    for (int t = 0; t < 4; ++t)
-#pragma unroll
-        for (int r = 0; r < R; ++r)
-            root[(t * R + r) * 64 + lane] = p[t][r];
 }
 
-// The runs' roots of output (tile, row i) of a group, column c: the tree's top.
+// What the join of a group's sums needs: the waves' roots, `step` numbers apart.
+struct Roots {
+    const float *part;
+    int waves, step;
+};
+
+// Output (tile, row i of a group, column c): the top of the tree.
 template <int R>
-__device__ __forceinline__ float join_runs(const float *part, int waves, int tile, int i, int c)
+__device__ __forceinline__ float join_roots(const Roots &at, int tile, int i, int c)
 {
+    const float *p = at.part + (tile * R + (i >> 2)) * 64 + (i & 3) * 16 + c;
+    if (at.waves == 1)
+        return p[0];
     float v[8];
 #pragma unroll
     for (int w = 0; w < 8; ++w)
-        v[w] = w < waves ? part[((w * 4 + tile) * R + (i >> 2)) * 64 + (i & 3) * 16 + c] : 0.f;
-    return tree_sum<8>(v, waves);
+        v[w] = w < at.waves ? p[w * at.step] : 0.f;
+    return tree_sum<8>(v, at.waves);
 }
 
 // gate and up: a unit is two tiles of gate and two of up, so that it ends with
@@ -669,6 +683,8 @@ struct Up {
     int *shift;
     int M, topk, H, I, shifts;
 
+    // waves of a compute unit's quarter that the registers are to hold
+    static constexpr int waves(int RM) { return RM == 4 ? 3 : 4; }
     template <int R>
     using Rows = RowsX<R>;
     __host__ __device__ int units() const { return I / 32; }
@@ -692,13 +708,13 @@ struct Up {
     }
     // 32 lanes a row: the trees, the activation, the block's power of two
     template <int R>
-    __device__ __forceinline__ void after(const float *part, int waves, const int *back, const uint16_t *list, int rows,
+    __device__ __forceinline__ void after(const Roots &roots, const int *back, const uint16_t *list, int rows,
                                           int unit) const
     {
         for (int o = threadIdx.x; o < rows * 32; o += blockDim.x) {
             const int i = o >> 5, col = o & 31;
-            const float gate = __builtin_ldexpf(join_runs<R>(part, waves, col >> 4, i, col & 15), back[i]);
-            const float up = __builtin_ldexpf(join_runs<R>(part, waves, 2 + (col >> 4), i, col & 15), back[i]);
+            const float gate = __builtin_ldexpf(join_roots<R>(roots, col >> 4, i, col & 15), back[i]);
+            const float up = __builtin_ldexpf(join_roots<R>(roots, 2 + (col >> 4), i, col & 15), back[i]);
             const float h = gate / (1.f + __builtin_expf(-gate)) * up;
             float top = __builtin_fabsf(h) < __builtin_inff() ? __builtin_fabsf(h) : 0.f;
 #pragma unroll
@@ -726,6 +742,7 @@ struct Down {
     float *t;
     int H;
 
+    static constexpr int waves(int RM) { return RM == 1 ? 4 : 3; }
     template <int R>
     using Rows = RowsH<R>;
     __host__ __device__ int units() const { return (H + 63) / 64; }
@@ -744,64 +761,73 @@ struct Down {
     }
     __device__ __forceinline__ int before(const uint16_t *, int) const { return 0; }
     template <int R>
-    __device__ __forceinline__ void after(const float *part, int waves, const int *, const uint16_t *list, int rows,
+    __device__ __forceinline__ void after(const Roots &roots, const int *, const uint16_t *list, int rows,
                                           int unit) const
     {
         for (int o = threadIdx.x; o < rows * 64; o += blockDim.x) {
             const int i = o >> 6, col = 64 * unit + (o & 63);
             if (col < H)
-                t[(size_t)list[i] * H + col] = join_runs<R>(part, waves, (o & 63) >> 4, i, o & 15);
+                t[(size_t)list[i] * H + col] = join_roots<R>(roots, (o & 63) >> 4, i, o & 15);
         }
     }
 };
+
+// Levels of the tree that wait within a run of L segments.
+__host__ __device__ inline int tree_levels(int L)
+{
+    int n = 1;
+    while (2 << n <= L)
+        ++n;
+    return n;
+}
 
 // One product of the layer.  grid = (units, min(slots, E)): a unit of four tiles
 // of one expert a workgroup, its waves on runs of L segments of K.  An expert's
 // rows go 4, 8 or 16 (at most 4 RM) at a time, by how many are left; the
 // weights of the next group's first quad are on their way while this one's
-// sums are joined, and the sums' room in LDS alternates, so that one barrier
-// a group is enough.
+// sums are joined.
 template <typename OP, int RM>
-__global__ __launch_bounds__(512) void q4_moe_product_kernel(Choice ch, OP op, int *__restrict__ ids,
+__global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(OP::waves(RM)))) void q4_moe_product_kernel(Choice ch, OP op, int *__restrict__ ids,
                                                              float *__restrict__ weights,
                                                              const uint8_t *__restrict__ wq,
                                                              const uint16_t *__restrict__ scales, int L, Plan plan)
 {
-    extern __shared__ __attribute__((aligned(16))) float room[];  // 2 x [wave][tile][r][lane]
+    extern __shared__ __attribute__((aligned(16))) float part[];  // [wave][level][tile][r][lane]
     __shared__ Found found;
-    __shared__ int back[2][16];
+    __shared__ int back[16];
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), waves = blockDim.x >> 6;
+    const int levels = tree_levels(L);
     if (ch.parts) {
-        uint64_t *keys = (uint64_t *)room;
+        uint64_t *keys = (uint64_t *)part;
         choose_rows<int16_t>(ch, 0, ch.M, keys, (double *)(keys + ch.M * ch.E), found.who, ids, weights,
                              blockIdx.x == 0 && blockIdx.y == 0);
         __syncthreads();  // (the keys' room is the products' next)
     }
-    const int qa = (wave * L * plan.G) >> plan.log2S;
+    const int qa = (wave * L * plan.G) >> plan.log2S, qb = ((wave + 1) * L * plan.G) >> plan.log2S;
     FourTiles tiles;
     Weights first;
     const int count = find_expert(found, ch.M * ch.topk, ids, ch.parts != nullptr, ch.E, blockIdx.y, [&](int e) {
         tiles = op.tiles(wq, scales, e, blockIdx.x, plan.G);
-        first.load(tiles, qa);
+        first.load(tiles, qa, qb);
     });
-    int turn = 0;
     for (int r0 = 0; r0 < count;) {
         const int left = count - r0;
         const uint16_t *list = found.list + r0;
-        float *part = room + turn * waves * 4 * RM * 64;
         auto group = [&](auto r) {
             constexpr int R = decltype(r)::value;
             const int rows = min(left, 4 * R);
             const int b = op.before(list, rows);
             multiply_run<R, typename OP::template Rows<R>>(tiles, first, op.template in<R>(list, rows, plan.nb),
-                                                           wave * L, L, plan, part + wave * 4 * R * 64);
+                                                           wave * L, L, plan, part + wave * levels * 4 * R * 64);
             if ((int)threadIdx.x < 16)
-                back[turn][threadIdx.x] = b;
+                back[threadIdx.x] = b;
             r0 += 4 * R;
             if (r0 < count)
-                first.load(tiles, qa);
+                first.load(tiles, qa, qb);
             __syncthreads();
-            op.template after<R>(part, waves, back[turn], list, rows, blockIdx.x);
+            op.template after<R>(Roots{part, waves, levels * 4 * R * 64}, back, list, rows, blockIdx.x);
+            if (r0 < count)
+                __syncthreads();  // the sums are read
         };
         if (RM == 1 || left <= 4)
             group(std::integral_constant<int, 1>());
@@ -809,7 +835,6 @@ __global__ __launch_bounds__(512) void q4_moe_product_kernel(Choice ch, OP op, i
             group(std::integral_constant<int, RM == 1 ? 1 : 2>());
         else
             group(std::integral_constant<int, RM>());
-        turn ^= 1;
     }
 }
 
@@ -943,12 +968,14 @@ hipError_t launch_product_r(const Choice &ch, const OP &op, int *ids, float *wei
 {
     const int n = ch.M * ch.topk;
     const dim3 grid((unsigned)op.units(), (unsigned)std::min(n, ch.E));
-#ifndef W8
-#define W8 1024
-#endif
-    // eight waves a workgroup while the card is not full, else four
-    const int waves = std::min(plan.S, (size_t)grid.x * grid.y >= W8 ? 4 : 8);
-    size_t lds = (size_t)2 * waves * 4 * RM * 64 * sizeof(float);
+    // as few waves a unit as fill the card (four a quarter of a compute unit): a
+    // longer stream each, less to join
+    int waves = 1;
+    while (waves < 8 && (size_t)grid.x * grid.y * waves < 4096)
+        waves *= 2;
+    waves = std::min(waves, plan.S);
+    const int L = plan.S / waves;
+    size_t lds = (size_t)waves * tree_levels(L) * 4 * RM * 64 * sizeof(float);
     if (ch.parts)
         lds = std::max(lds, (size_t)(ch.M * ch.E + n) * sizeof(double));
     if (lds > 48 * 1024) {
@@ -958,7 +985,7 @@ hipError_t launch_product_r(const Choice &ch, const OP &op, int *ids, float *wei
             return e;
     }
     hipLaunchKernelGGL((q4_moe_product_kernel<OP, RM>), grid, dim3(64 * waves), lds, stream, ch, op, ids, weights,
-                       wq, scales, plan.S / waves, plan);
+                       wq, scales, L, plan);
     return hipGetLastError();
 }
 
