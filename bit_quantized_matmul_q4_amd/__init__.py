@@ -67,6 +67,24 @@ def _need(t: torch.Tensor, name: str, dtypes, ndim: int, device=None):
         raise ValueError("%s must be contiguous" % name)
 
 
+# The current device and a device's current stream, as a number, without the
+# objects around them (a decode step's calls are short).
+_get_device = torch._C._cuda_getDevice
+_raw_stream = torch._C._cuda_getCurrentRawStream
+
+
+def _call(dev: torch.device, name: str, f, *args) -> None:
+    """f(*args, stream) with dev current; raises on a status."""
+    i = dev.index
+    if _get_device() == i:
+        st = f(*args, _raw_stream(i))
+    else:
+        with torch.cuda.device(dev):
+            st = f(*args, _raw_stream(i))
+    if st:
+        _lib.check(st, name)
+
+
 def packed_sizes(N: int, K: int):
     """(packed code bytes, packed scale bytes) of an N x K matrix."""
     lib = _lib.load()
@@ -328,9 +346,7 @@ def pack_int8(codes: torch.Tensor, scales: torch.Tensor) -> Int8Matrix:
     if scales.numel() != R:
         raise ValueError("scales must be [%d]" % R)
     packed = torch.empty(_int8_bytes(R, K), dtype=torch.int8, device=codes.device)
-    with torch.cuda.device(codes.device):
-        st = lib.q4_int8_pack(codes.data_ptr(), packed.data_ptr(), R, K, _stream(codes.device))
-    _lib.check(st, "q4_int8_pack")
+    _call(codes.device, "q4_int8_pack", lib.q4_int8_pack, codes.data_ptr(), packed.data_ptr(), R, K)
     return Int8Matrix(packed, scales, R, K)
 
 
@@ -394,11 +410,9 @@ def linear_int8(x, w: Int8Matrix, out: torch.Tensor | None = None, out_dtype: to
             raise ValueError("out must be [%d, %d]" % (M, N))
     kind = _DTYPES[x.dtype] if dense else _lib.Q4_I8
     _keep, ws_ptr, ws_len = _workspace(workspace, lib.q4_int8_workspace_bytes(M, N, K, kind), dev)
-    with torch.cuda.device(dev):
-        st = lib.q4_int8_linear(x.data_ptr() if dense else x.codes.data_ptr(), kind,
-                                None if dense else x.scales.data_ptr(), w.codes.data_ptr(), w.scales.data_ptr(),
-                                out.data_ptr(), _DTYPES[out.dtype], M, N, K, ws_ptr, ws_len, _stream(dev))
-    _lib.check(st, "q4_int8_linear")
+    _call(dev, "q4_int8_linear", lib.q4_int8_linear, x.data_ptr() if dense else x.codes.data_ptr(), kind, None if
+          dense else x.scales.data_ptr(), w.codes.data_ptr(), w.scales.data_ptr(), out.data_ptr(),
+          _DTYPES[out.dtype], M, N, K, ws_ptr, ws_len)
     return out
 
 
@@ -466,11 +480,9 @@ def moe_route(x: torch.Tensor, router: torch.Tensor, topk: int, bias: torch.Tens
     ids = torch.empty((M, topk), dtype=torch.int32, device=dev)
     weights = torch.empty((M, topk), dtype=torch.float32, device=dev)
     _keep, ws_ptr, ws_len = _workspace(workspace, lib.q4_moe_route_workspace_bytes(M, E, K), dev)
-    with torch.cuda.device(dev):
-        st = lib.q4_moe_route(x.data_ptr(), _DTYPES[x.dtype], router.data_ptr(), _DTYPES[router.dtype],
-                              None if bias is None else bias.data_ptr(), ids.data_ptr(), weights.data_ptr(), M, E, K,
-                              topk, int(renormalize), ws_ptr, ws_len, _stream(dev))
-    _lib.check(st, "q4_moe_route")
+    _call(dev, "q4_moe_route", lib.q4_moe_route, x.data_ptr(), _DTYPES[x.dtype], router.data_ptr(),
+          _DTYPES[router.dtype], None if bias is None else bias.data_ptr(), ids.data_ptr(), weights.data_ptr(), M,
+          E, K, topk, int(renormalize), ws_ptr, ws_len)
     return ids, weights
 
 
@@ -500,11 +512,9 @@ def moe_experts(x: torch.Tensor, ids: torch.Tensor, weights: torch.Tensor, w13: 
     else:
         _need_out(out, (M, H), (torch.float32,), dev)
     _keep, ws_ptr, ws_len = _workspace(workspace, lib.q4_moe_experts_workspace_bytes(M, H, I, topk), dev)
-    with torch.cuda.device(dev):
-        st = lib.q4_moe_experts(x.data_ptr(), _DTYPES[x.dtype], ids.data_ptr(), weights.data_ptr(),
-                                w13.codes.data_ptr(), w13.scales.data_ptr(), w2.codes.data_ptr(),
-                                w2.scales.data_ptr(), out.data_ptr(), M, E, H, I, topk, ws_ptr, ws_len, _stream(dev))
-    _lib.check(st, "q4_moe_experts")
+    _call(dev, "q4_moe_experts", lib.q4_moe_experts, x.data_ptr(), _DTYPES[x.dtype], ids.data_ptr(),
+          weights.data_ptr(), w13.codes.data_ptr(), w13.scales.data_ptr(), w2.codes.data_ptr(),
+          w2.scales.data_ptr(), out.data_ptr(), M, E, H, I, topk, ws_ptr, ws_len)
     return out
 
 
@@ -524,12 +534,10 @@ def moe(x: torch.Tensor, router: torch.Tensor, w13: Q4Weight, w2: Q4Weight, topk
     else:
         _need_out(out, (M, H), (torch.float32,), dev)
     _keep, ws_ptr, ws_len = _workspace(workspace, lib.q4_moe_layer_workspace_bytes(M, E, H, I, topk), dev)
-    with torch.cuda.device(dev):
-        st = lib.q4_moe_layer(x.data_ptr(), _DTYPES[x.dtype], router.data_ptr(), _DTYPES[router.dtype],
-                              None if bias is None else bias.data_ptr(), w13.codes.data_ptr(), w13.scales.data_ptr(),
-                              w2.codes.data_ptr(), w2.scales.data_ptr(), out.data_ptr(), M, E, H, I, topk,
-                              int(renormalize), ws_ptr, ws_len, _stream(dev))
-    _lib.check(st, "q4_moe_layer")
+    _call(dev, "q4_moe_layer", lib.q4_moe_layer, x.data_ptr(), _DTYPES[x.dtype], router.data_ptr(),
+          _DTYPES[router.dtype], None if bias is None else bias.data_ptr(), w13.codes.data_ptr(),
+          w13.scales.data_ptr(), w2.codes.data_ptr(), w2.scales.data_ptr(), out.data_ptr(), M, E, H, I, topk,
+          int(renormalize), ws_ptr, ws_len)
     return out
 
 

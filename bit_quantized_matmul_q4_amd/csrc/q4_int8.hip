@@ -100,6 +100,71 @@ __device__ __forceinline__ int row_code(float x, const RowScale &r)
     return (int)__builtin_fminf(__builtin_fmaxf(q, -127.f), 127.f);
 }
 
+// 16 values of a row: their largest magnitude's bits, and their codes.
+template <int KIND, int VECS>
+__device__ __forceinline__ uint32_t top_of(const u32x4 (&v)[VECS])
+{
+    uint32_t top = 0;
+#pragma unroll
+    for (int i = 0; i < VECS; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            top = max(top, v[i][j] & kAbsMask<KIND>);
+            if constexpr (KIND != 2)
+                top = max(top, (v[i][j] >> 16) & kAbsMask<KIND>);
+        }
+    return top;
+}
+template <int KIND, int VECS>
+__device__ __forceinline__ float value_of(const u32x4 (&v)[VECS], int e)
+{
+    uint32_t bits;
+    if constexpr (KIND == 2)
+        bits = v[e / 4][e % 4];
+    else
+        bits = (v[e / 8][(e / 2) % 4] >> (16 * (e & 1))) & 0xFFFFu;
+    return elem_value<KIND>(bits);
+}
+
+// The codes by the inverse: one fma rounds x / s (within 127 2^-23 of the
+// quotient) to a whole number in the low bits of 1.5 2^23 + q, and a second
+// one gives what is left, at most 1/2.  Where all 16 are further from a border
+// than the inverse can be off, the codes are exact; else (4 in 100000 values
+// of a smooth distribution), and where the scale is so small that it was
+// lifted, they are taken one by one.
+template <int KIND, int VECS>
+__device__ __forceinline__ u32x4 codes_of(const u32x4 (&v)[VECS], const RowScale &rs)
+{
+    constexpr float magic = 0x1.8p23f;
+    u32x4 out;
+    float left = rs.lift == 1.f ? 0.f : 1.f;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        uint32_t u[4];
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
+            const float x = value_of<KIND>(v, 4 * j + b);
+            const float t = __builtin_fmaf(x, rs.inv, magic);
+            left = __builtin_fmaxf(left, __builtin_fabsf(__builtin_fmaf(x, rs.inv, -(t - magic))));
+            u[b] = __builtin_bit_cast(uint32_t, t);
+        }
+        const uint32_t lo = __builtin_amdgcn_perm(u[1], u[0], 0x0c0c0400u);  // bytes 0 of u[0] and u[1]
+        const uint32_t hi = __builtin_amdgcn_perm(u[3], u[2], 0x04000c0cu);
+        out[j] = lo | hi;
+    }
+    if (!(left < 0.49996f)) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            uint32_t word = 0;
+#pragma unroll
+            for (int b = 0; b < 4; ++b)
+                word |= ((uint32_t)row_code(value_of<KIND>(v, 4 * j + b), rs) & 0xFFu) << (8 * b);
+            out[j] = word;
+        }
+    }
+    return out;
+}
+
 // One workgroup quantizes RW rows (a divisor of 16); a wave's 64 lanes are RW
 // rows by 64 / RW pieces of 16 k, so with RW = 16 both the reads (whole
 // 128-byte lines) and the packed writes (1 KB) are contiguous; fewer rows a
@@ -136,19 +201,6 @@ __global__ __launch_bounds__(kQuantThreads) void q4_int8_quantize_kernel(const v
         for (int i = 0; i < VECS; ++i)
             v[i] = src[i];
     };
-    auto see = [&](const u32x4 (&v)[VECS]) {
-#pragma unroll
-        for (int i = 0; i < VECS; ++i)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                if constexpr (KIND == 2) {
-                    top = max(top, v[i][j] & kAbsMask<KIND>);
-                } else {
-                    top = max(top, v[i][j] & kAbsMask<KIND>);
-                    top = max(top, (v[i][j] >> 16) & kAbsMask<KIND>);
-                }
-            }
-    };
     if (live) {
 #pragma unroll
         for (int h = 0; h < HELD; ++h)
@@ -157,11 +209,11 @@ __global__ __launch_bounds__(kQuantThreads) void q4_int8_quantize_kernel(const v
 #pragma unroll
         for (int h = 0; h < HELD; ++h)
             if (p0 + h * STEP < pieces)
-                see(held[h]);
+                top = max(top, top_of<KIND>(held[h]));
         for (int p = p0 + HELD * STEP; p < pieces; p += STEP) {
             u32x4 v[VECS];
             load(p, v);
-            see(v);
+            top = max(top, top_of<KIND>(v));
         }
     }
     // over the lanes and waves of the same row
@@ -180,25 +232,6 @@ __global__ __launch_bounds__(kQuantThreads) void q4_int8_quantize_kernel(const v
     if (live && threadIdx.x < RW)
         scales[row] = rs.scale;
 
-    auto code = [&](const u32x4 (&v)[VECS]) {
-        u32x4 out;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            uint32_t word = 0;
-#pragma unroll
-            for (int b = 0; b < 4; ++b) {
-                const int e = 4 * j + b;
-                uint32_t bits;
-                if constexpr (KIND == 2)
-                    bits = v[e / 4][e % 4];
-                else
-                    bits = (v[e / 8][(e / 2) % 4] >> (16 * (e & 1))) & 0xFFFFu;
-                word |= ((uint32_t)row_code(elem_value<KIND>(bits), rs) & 0xFFu) << (8 * b);
-            }
-            out[j] = word;
-        }
-        return out;
-    };
     const int tiles = int8_tiles(K);
     const int all = PACKED ? 4 * tiles : pieces;
     auto store = [&](int p, u32x4 v) {
@@ -213,13 +246,13 @@ __global__ __launch_bounds__(kQuantThreads) void q4_int8_quantize_kernel(const v
     for (int h = 0; h < HELD; ++h) {
         const int p = p0 + h * STEP;
         if (p < all)
-            store(p, live && p < pieces ? code(held[h]) : (u32x4){0, 0, 0, 0});
+            store(p, live && p < pieces ? codes_of<KIND>(held[h], rs) : (u32x4){0, 0, 0, 0});
     }
     for (int p = p0 + HELD * STEP; p < all; p += STEP) {
         u32x4 v[VECS];
         if (live && p < pieces) {
             load(p, v);
-            store(p, code(v));
+            store(p, codes_of<KIND>(v, rs));
         } else {
             store(p, (u32x4){0, 0, 0, 0});
         }
@@ -374,17 +407,160 @@ __global__ __launch_bounds__(512) void q4_int8_gemv_kernel(const int8_t *__restr
     }
 }
 
-// -------------------------------------------------------------- many rows
-// LDS-tiled: a workgroup of WM x WN waves owns BM rows by BN columns; steps
-// of 128 k go from memory to LDS directly, two stages deep: the loads of step
-// s + 1 are in flight while step s is multiplied.
-__device__ __forceinline__ void load_lds16(const int8_t *g, int8_t *lds)
+// ------------------------------------------------------- a few dense rows
+// A few dense rows in one launch: a workgroup quantizes all of them into LDS (M
+// K bytes) while its first weights are on their way, then multiplies its tile
+// of W.  A wave takes every eighth k64 step, in chunks of eight steps, one
+// chunk ahead of the products.
+constexpr uint32_t kNowhere = 1u << 31;  // past every tile's range: reads zero, no access
+constexpr int kDecodeWaves = 8, kDecodeChunk = 8;
+
+template <int KIND, int YK>
+__global__ __launch_bounds__(64 * kDecodeWaves) void q4_int8_decode_kernel(const void *__restrict__ x_,
+                                                                           const int8_t *__restrict__ wq,
+                                                                           const float *__restrict__ sw,
+                                                                           void *__restrict__ y, int M, int N, int K,
+                                                                           int vec)
 {
-    __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void *)g,
-                                     (__attribute__((address_space(3))) void *)lds, 16, 0, 0);
+    constexpr int W = kDecodeWaves, U = kDecodeChunk;
+    extern __shared__ __attribute__((aligned(16))) int8_t xl[];  // [k16 piece][row][16]
+    __shared__ i32x4 part[W][64];
+    __shared__ uint32_t tops[16];
+    __shared__ float scale_of[16];
+    const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
+    const int g = lane >> 4, c = min(lane & 15, M - 1);
+    const int steps = int8_tiles(K);
+    const __amdgpu_buffer_rsrc_t wb = __builtin_amdgcn_make_buffer_rsrc(
+        const_cast<int8_t *>(wq + (size_t)blockIdx.x * steps * 1024), (short)0, steps * 1024, 0x00020000);
+    auto fetch = [&](u32x4 (&v)[U], int s0) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int s = s0 + W * u + wave;
+            v[u] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(
+                                                 wb, s < steps ? s * 1024 + lane * 16 : kNowhere, 0, 2));
+        }
+    };
+    u32x4 w0[U], w1[U];
+    fetch(w0, 0);
+
+    // the rows: as many waves each as there are, or a wave several rows in turn
+    {
+        typedef Elem<KIND> E;
+        constexpr int HELD = 2, VECS = (int)sizeof(E);
+        int per = W;
+        while (per > 1 && W / per < M)
+            per /= 2;
+        const int pieces = K / 16, step = 64 * per, p0 = (wave % per) * 64 + lane;
+        if (tid < 16)
+            tops[tid] = 0;
+        __syncthreads();
+        for (int row0 = 0; row0 < M; row0 += W / per) {
+            const int row = row0 + wave / per;
+            const E *x = (const E *)x_ + (size_t)min(row, M - 1) * K;
+            u32x4 held[HELD][VECS];
+            uint32_t top = 0;
+            auto load = [&](int p, u32x4 (&v)[VECS]) {
+#pragma unroll
+                for (int i = 0; i < VECS; ++i)
+                    v[i] = *((const u32x4 *)(x + 16 * (size_t)p) + i);
+            };
+            if (row < M) {
+#pragma unroll
+                for (int h = 0; h < HELD; ++h)
+                    if (p0 + h * step < pieces)
+                        load(p0 + h * step, held[h]);
+#pragma unroll
+                for (int h = 0; h < HELD; ++h)
+                    if (p0 + h * step < pieces)
+                        top = max(top, top_of<KIND>(held[h]));
+                for (int p = p0 + HELD * step; p < pieces; p += step) {
+                    u32x4 v[VECS];
+                    load(p, v);
+                    top = max(top, top_of<KIND>(v));
+                }
+#pragma unroll
+                for (int d = 1; d < 64; d *= 2)
+                    top = max(top, (uint32_t)__shfl_xor((int)top, d));
+                if (lane == 0)
+                    atomicMax(&tops[row], top);
+            }
+            __syncthreads();
+            if (row < M) {
+                const RowScale rs = row_scale<KIND>(tops[row]);
+                if (p0 == 0)
+                    scale_of[row] = rs.scale;
+                for (int h = 0, p = p0; p < 4 * steps; ++h, p += step) {
+                    u32x4 v = {0, 0, 0, 0};
+                    if (p < pieces) {
+                        if (h >= HELD) {
+                            u32x4 raw[VECS];
+                            load(p, raw);
+                            v = codes_of<KIND>(raw, rs);
+                        } else {
+                            v = codes_of<KIND>(h == 0 ? held[0] : held[1], rs);
+                        }
+                    }
+                    *(u32x4 *)(xl + ((size_t)p * M + row) * 16) = v;
+                }
+            }
+        }
+        __syncthreads();
+    }
+
+    const int8_t *xr = xl + (g * M + c) * 16;
+    i32x4 acc = {0, 0, 0, 0};
+    auto multiply = [&](const u32x4 (&v)[U], int s0) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) {  // (steps past the end: zero weights, the last values again)
+            const int s = min(s0 + W * u + wave, steps - 1);
+            const i32x4 b = *(const i32x4 *)(xr + (size_t)s * 64 * M);
+            acc = __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(i32x4, v[u]), b, acc, 0, 0, 0);
+        }
+    };
+    for (int s0 = 0; s0 < steps; s0 += 2 * W * U) {
+        fetch(w1, s0 + W * U);
+        multiply(w0, s0);
+        fetch(w0, s0 + 2 * W * U);
+        if (s0 + W * U < steps)
+            multiply(w1, s0 + W * U);
+    }
+    part[wave][lane] = acc;
+    __syncthreads();
+    if (wave == 0) {
+        i32x4 s = part[0][lane];
+#pragma unroll
+        for (int j = 1; j < W; ++j)
+            s += part[j][lane];
+        const int m = lane & 15, n = 16 * blockIdx.x + 4 * g;
+        if (m < M && n < N) {
+            Scale ws[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                ws[i] = split_scale(n + i < N ? sw[n + i] : 0.f);
+            store4<YK>(y, (size_t)m * N + n, N - n, vec, scaled4(s, split_scale(scale_of[m]), ws));
+        }
+    }
 }
 
-template <int BM, int BN, int WM, int WN, int YK>
+// -------------------------------------------------------------- many rows
+// LDS-tiled: a workgroup of WM x WN waves owns BM rows by BN columns; steps of
+// 128 k go from memory to LDS directly, NS stages deep.  Within a step a wave
+// reads the operands of one half (64 k) from LDS while it multiplies the
+// other: the barrier that frees a stage falls between the halves, when both
+// halves' operands of the step are in registers, so that neither the LDS reads
+// nor the loads of the next stages hold up the matrix cores.
+__device__ __forceinline__ void load_lds(__amdgpu_buffer_rsrc_t src, int8_t *lds, int lane_at, int at)
+{
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(src, (__attribute__((address_space(3))) void *)lds, 16, lane_at, at, 0, 0);
+}
+
+template <int N>
+__device__ __forceinline__ void wait_loads()
+{
+    asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
+}
+
+template <int BM, int BN, int WM, int WN, int NS, int YK>
 __global__ __launch_bounds__(64 * WM *WN) void q4_int8_gemm_kernel(
     const int8_t *__restrict__ xq, const float *__restrict__ sx, const int8_t *__restrict__ wq,
     const float *__restrict__ sw, void *__restrict__ y, int *__restrict__ partial, int M, int N, int K, int steps_per,
@@ -393,7 +569,7 @@ __global__ __launch_bounds__(64 * WM *WN) void q4_int8_gemm_kernel(
     constexpr int WAVES = WM * WN;
     constexpr int TM = BM / 16 / WM, TN = BN / 16 / WN;  // a wave's row tiles of x and of W
     constexpr int CHUNKS = (BM + BN) / 16 * 2;           // 1 KB pieces of a stage
-    static_assert(CHUNKS % WAVES == 0, "every wave loads as many pieces");
+    static_assert(CHUNKS % WAVES == 0 && BM / 16 * 2 % (CHUNKS / WAVES) == 0, "a wave loads pieces of one operand");
     constexpr int PER = CHUNKS / WAVES;
     constexpr int STAGE = CHUNKS * 1024;
     extern __shared__ __attribute__((aligned(16))) int8_t lds[];
@@ -413,25 +589,24 @@ __global__ __launch_bounds__(64 * WM *WN) void q4_int8_gemm_kernel(
     const int bm = id % gm, bn = id / gm;
     const int s0 = blockIdx.y * steps_per, s1 = min(tiles / 2, s0 + steps_per);
 
-    // the pieces this wave loads: the first BM / 16 pairs are rows of x
-    const int8_t *src[PER];
+    // the pieces this wave loads: PER of x or of W (row tiles past the end: the
+    // last one, its outputs are not stored)
+    const int ch0 = wave * PER;
+    const bool of_x = ch0 < BM / 16 * 2;
+    const int t0 = of_x ? bm * (BM / 16) : bn * (BN / 16), t_all = of_x ? tm_all : tn_all;
+    const int rel = (of_x ? ch0 : ch0 - BM / 16 * 2) / 2;
+    const __amdgpu_buffer_rsrc_t src = __builtin_amdgcn_make_buffer_rsrc(
+        const_cast<int8_t *>((of_x ? xq : wq) + (size_t)t0 * tiles * 1024), (short)0,
+        min(t_all - t0, (of_x ? BM : BN) / 16) * tiles * 1024, 0x00020000);
+    int at[PER];
 #pragma unroll
-    for (int i = 0; i < PER; ++i) {
-        const int ch = wave * PER + i;
-        const int t = ch >> 1;
-        const int8_t *base;
-        if (t < BM / 16)  // (a row tile past the end: the last one, its outputs are not stored)
-            base = xq + (size_t)min(bm * (BM / 16) + t, tm_all - 1) * tiles * 1024;
-        else
-            base = wq + (size_t)min(bn * (BN / 16) + t - BM / 16, tn_all - 1) * tiles * 1024;
-        src[i] = base + (ch & 1) * 1024 + lane * 16 + (size_t)s0 * 2048;
-    }
-    auto fetch = [&](int stage) {
+    for (int i = 0; i < PER; ++i)
+        at[i] = min(rel + i / 2, t_all - 1 - t0) * tiles * 1024 + ((ch0 + i) & 1) * 1024;
+    auto fetch = [&](int step) {  // (past the last step: the last again, so that the counts stay)
+        const int stage = (step - s0) % NS, off = min(step, s1 - 1) * 2048;
 #pragma unroll
-        for (int i = 0; i < PER; ++i) {
-            load_lds16(src[i], lds + stage * STAGE + (wave * PER + i) * 1024);
-            src[i] += 2048;
-        }
+        for (int i = 0; i < PER; ++i)
+            load_lds(src, lds + stage * STAGE + (ch0 + i) * 1024, lane * 16, at[i] + off);
     };
     i32x4 acc[TN][TM];
 #pragma unroll
@@ -439,30 +614,49 @@ __global__ __launch_bounds__(64 * WM *WN) void q4_int8_gemm_kernel(
 #pragma unroll
         for (int j = 0; j < TM; ++j)
             acc[i][j] = (i32x4){0, 0, 0, 0};
-    if (s0 < s1)
-        fetch(0);
-    for (int s = s0; s < s1; ++s) {
-        const int stage = (s - s0) & 1;
-        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // this wave's pieces of step s
-        __syncthreads();                                  // every wave's, and step s - 1 is read
-        if (s + 1 < s1)
-            fetch(stage ^ 1);
-        const int8_t *at = lds + stage * STAGE + lane * 16;
+    i32x4 a[2][TN], b[2][TM];
+    auto read = [&](int half, int step) {
+        const int8_t *p = lds + (step - s0) % NS * STAGE + lane * 16 + half * 1024;
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            i32x4 a[TN], b[TM];
+        for (int j = 0; j < TM; ++j)
+            b[half][j] = *(const i32x4 *)(p + (wm * TM + j) * 2048);
+#pragma unroll
+        for (int i = 0; i < TN; ++i)
+            a[half][i] = *(const i32x4 *)(p + (BM / 16 + wn * TN + i) * 2048);
+    };
+    auto multiply = [&](int half) {
+#pragma unroll
+        for (int i = 0; i < TN; ++i)
 #pragma unroll
             for (int j = 0; j < TM; ++j)
-                b[j] = *(const i32x4 *)(at + ((wm * TM + j) * 2 + h) * 1024);
+                acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(a[half][i], b[half][j], acc[i][j], 0, 0, 0);
+    };
+    if (s0 < s1) {
 #pragma unroll
-            for (int i = 0; i < TN; ++i)
-                a[i] = *(const i32x4 *)(at + ((BM / 16 + wn * TN + i) * 2 + h) * 1024);
-#pragma unroll
-            for (int i = 0; i < TN; ++i)
-#pragma unroll
-                for (int j = 0; j < TM; ++j)
-                    acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(a[i], b[j], acc[i][j], 0, 0, 0);
+        for (int i = 0; i < NS; ++i)
+            fetch(s0 + i);
+        wait_loads<PER *(NS - 1)>();
+        __builtin_amdgcn_s_barrier();
+        asm volatile("" ::: "memory");
+        read(0, s0);
+        for (int s = s0; s < s1; ++s) {
+            read(1, s);
+            __builtin_amdgcn_sched_barrier(0);
+            multiply(0);
+            __builtin_amdgcn_sched_barrier(0);
+            // this wave's reads of step s are done, and its pieces of step s + 1 here
+            asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+            wait_loads<PER *(NS - 2)>();
+            __builtin_amdgcn_s_barrier();
+            asm volatile("" ::: "memory");
+            fetch(s + NS);
+            if (s + 1 < s1)
+                read(0, s + 1);
+            __builtin_amdgcn_sched_barrier(0);
+            multiply(1);
+            __builtin_amdgcn_sched_barrier(0);
         }
+        wait_loads<0>();  // (the loads past the end: nothing is in flight into LDS when the workgroup ends)
     }
     // lane (g, c) holds row c of a tile of x, rows 4 g .. 4 g + 3 of one of W
     const int m0 = bm * BM + wm * TM * 16 + (lane & 15), n0 = bn * BN + wn * TN * 16 + 4 * (lane >> 4);
@@ -527,14 +721,19 @@ constexpr int kUnits = 256;  // compute units
 
 // The tile and the split of K for a shape.
 struct Int8Shape {
-    bool gemv;
+    bool decode, gemv;
     int bm, bn, split;
 };
 
-Int8Shape int8_shape(int M, int N, int K)
+Int8Shape int8_shape(bool dense, int M, int N, int K)
 {
-    Int8Shape s{M <= 64, 0, 0, 1};
-    if (s.gemv)
+    // quantizing within the product saves a launch while that is less work than
+    // the launch's 2 us: 3584 x 3584 at 1 / 2 / 4 / 8 rows 5.1 / 5.7 / 6.6 / 7.6
+    // against 7.2 / 7.3 / 7.8 / 7.9 us, at 12 rows 10.4 against 7.9; 18944 x
+    // 3584 (more than two tiles a compute unit, each quantizing again) at one
+    // row 17.0 against 14.8
+    Int8Shape s{dense && M <= 4 && M * int8_tiles(K) * 64 <= 20 * 1024 && N <= 8192, M <= 64, 0, 0, 1};
+    if (s.decode || s.gemv)
         return s;
     const int big = ((M + 255) / 256) * ((N + 255) / 256);
     s.bm = s.bn = big >= kUnits ? 256 : 128;
@@ -556,9 +755,15 @@ void launch_rows(const void *x, int8_t *codes, float *scales, int rows, int K, h
 template <int KIND, bool PACKED>
 void launch_rows_k(const void *x, int8_t *codes, float *scales, int rows, int K, hipStream_t stream)
 {
-    if (rows >= 4096)
+#ifndef RW16
+#define RW16 1073741824
+#endif
+#ifndef RW4
+#define RW4 2048
+#endif
+    if (rows >= RW16)
         launch_rows<KIND, 16, PACKED>(x, codes, scales, rows, K, stream);
-    else if (rows >= 1024)
+    else if (rows >= RW4)
         launch_rows<KIND, 4, PACKED>(x, codes, scales, rows, K, stream);
     else
         launch_rows<KIND, 1, PACKED>(x, codes, scales, rows, K, stream);
@@ -577,33 +782,53 @@ void launch_gemv_rt(int yk, const int8_t *xq, const float *sx, const int8_t *wq,
         hipLaunchKernelGGL((q4_int8_gemv_kernel<RT, 0>), grid, block, 0, stream, xq, sx, wq, sw, y, M, N, K, vec);
 }
 
-template <int BM, int BN, int WM, int WN, int YK>
+template <int BM, int BN, int WM, int WN, int NS, int YK>
 hipError_t launch_tile_y(const int8_t *xq, const float *sx, const int8_t *wq, const float *sw, void *y, int *partial,
                          int M, int N, int K, int split, int vec, hipStream_t stream)
 {
-    constexpr int kLds = 2 * (BM + BN) / 16 * 2 * 1024;
+    constexpr int kLds = NS * (BM + BN) / 16 * 2 * 1024;
     if (kLds > 64 * 1024) {
-        const hipError_t e = hipFuncSetAttribute((const void *)q4_int8_gemm_kernel<BM, BN, WM, WN, YK>,
+        const hipError_t e = hipFuncSetAttribute((const void *)q4_int8_gemm_kernel<BM, BN, WM, WN, NS, YK>,
                                                  hipFuncAttributeMaxDynamicSharedMemorySize, kLds);
         if (e != hipSuccess)
             return e;
     }
     const int steps = int8_tiles(K) / 2;
     const dim3 grid((unsigned)((M + BM - 1) / BM * ((N + BN - 1) / BN)), (unsigned)split);
-    hipLaunchKernelGGL((q4_int8_gemm_kernel<BM, BN, WM, WN, YK>), grid, dim3(64 * WM * WN), kLds, stream, xq, sx, wq, sw,
+    hipLaunchKernelGGL((q4_int8_gemm_kernel<BM, BN, WM, WN, NS, YK>), grid, dim3(64 * WM * WN), kLds, stream, xq, sx, wq, sw,
                        y, partial, M, N, K, (steps + split - 1) / split, vec);
     return hipGetLastError();
 }
 
-template <int BM, int BN, int WM, int WN>
+template <int BM, int BN, int WM, int WN, int NS>
 hipError_t launch_tile(int yk, const int8_t *xq, const float *sx, const int8_t *wq, const float *sw, void *y,
                        int *partial, int M, int N, int K, int split, int vec, hipStream_t stream)
 {
     if (yk == 2)
-        return launch_tile_y<BM, BN, WM, WN, 2>(xq, sx, wq, sw, y, partial, M, N, K, split, vec, stream);
+        return launch_tile_y<BM, BN, WM, WN, NS, 2>(xq, sx, wq, sw, y, partial, M, N, K, split, vec, stream);
     if (yk == 1)
-        return launch_tile_y<BM, BN, WM, WN, 1>(xq, sx, wq, sw, y, partial, M, N, K, split, vec, stream);
-    return launch_tile_y<BM, BN, WM, WN, 0>(xq, sx, wq, sw, y, partial, M, N, K, split, vec, stream);
+        return launch_tile_y<BM, BN, WM, WN, NS, 1>(xq, sx, wq, sw, y, partial, M, N, K, split, vec, stream);
+    return launch_tile_y<BM, BN, WM, WN, NS, 0>(xq, sx, wq, sw, y, partial, M, N, K, split, vec, stream);
+}
+
+template <int KIND, int YK>
+hipError_t launch_decode_y(const void *x, const int8_t *wq, const float *sw, void *y, int M, int N, int K, int vec,
+                           hipStream_t stream)
+{
+    hipLaunchKernelGGL((q4_int8_decode_kernel<KIND, YK>), dim3((unsigned)((N + 15) / 16)), dim3(64 * kDecodeWaves),
+                       (size_t)M * int8_tiles(K) * 64, stream, x, wq, sw, y, M, N, K, vec);
+    return hipGetLastError();
+}
+
+template <int KIND>
+hipError_t launch_decode(const void *x, const int8_t *wq, const float *sw, void *y, int yk, int M, int N, int K, int vec,
+                         hipStream_t stream)
+{
+    if (yk == 2)
+        return launch_decode_y<KIND, 2>(x, wq, sw, y, M, N, K, vec, stream);
+    if (yk == 1)
+        return launch_decode_y<KIND, 1>(x, wq, sw, y, M, N, K, vec, stream);
+    return launch_decode_y<KIND, 0>(x, wq, sw, y, M, N, K, vec, stream);
 }
 
 size_t up256(size_t n) { return (n + 255) & ~(size_t)255; }
@@ -643,9 +868,9 @@ hipError_t launch_int8_pack(const int8_t *codes, int8_t *packed, int rows, int K
 
 size_t int8_workspace_bytes(bool dense, int M, int N, int K)
 {
-    const Int8Shape sh = int8_shape(M, N, K);
+    const Int8Shape sh = int8_shape(dense, M, N, K);
     size_t n = 0;
-    if (dense)
+    if (dense && !sh.decode)
         n += up256(int8_packed_bytes(M, K)) + up256((size_t)M * sizeof(float));
     if (sh.split > 1)
         n += (size_t)sh.split * M * N * sizeof(int);
@@ -655,7 +880,12 @@ size_t int8_workspace_bytes(bool dense, int M, int N, int K)
 hipError_t launch_int8_linear(const void *x, int x_kind, const float *x_scales, const int8_t *wq, const float *w_scales,
                               void *y, int y_kind, int M, int N, int K, void *workspace, hipStream_t stream)
 {
-    const Int8Shape sh = int8_shape(M, N, K);
+    const Int8Shape sh = int8_shape(x_kind >= 0, M, N, K);
+    const int size = y_kind == 2 ? 4 : 2;
+    const int vec = N % 4 == 0 && ((uintptr_t)y & (4 * size - 1)) == 0;
+    if (sh.decode)
+        return x_kind == 1 ? launch_decode<1>(x, wq, w_scales, y, y_kind, M, N, K, vec, stream)
+                           : launch_decode<0>(x, wq, w_scales, y, y_kind, M, N, K, vec, stream);
     uint8_t *ws = (uint8_t *)workspace;
     const int8_t *xq = (const int8_t *)x;
     const float *sx = x_scales;
@@ -670,8 +900,6 @@ hipError_t launch_int8_linear(const void *x, int x_kind, const float *x_scales, 
         xq = q;
         sx = s;
     }
-    const int size = y_kind == 2 ? 4 : 2;
-    const int vec = N % 4 == 0 && ((uintptr_t)y & (4 * size - 1)) == 0;
     if (sh.gemv) {
         const int rt = (M + 15) / 16;
         if (rt == 1)
@@ -685,9 +913,9 @@ hipError_t launch_int8_linear(const void *x, int x_kind, const float *x_scales, 
     int *partial = sh.split > 1 ? (int *)ws : nullptr;
     hipError_t e;
     if (sh.bm == 256)
-        e = launch_tile<256, 256, 2, 4>(y_kind, xq, sx, wq, w_scales, y, partial, M, N, K, sh.split, vec, stream);
+        e = launch_tile<256, 256, 2, 4, 2>(y_kind, xq, sx, wq, w_scales, y, partial, M, N, K, sh.split, vec, stream);
     else
-        e = launch_tile<128, 128, 2, 2>(y_kind, xq, sx, wq, w_scales, y, partial, M, N, K, sh.split, vec, stream);
+        e = launch_tile<128, 128, 2, 2, 4>(y_kind, xq, sx, wq, w_scales, y, partial, M, N, K, sh.split, vec, stream);
     if (e != hipSuccess || !partial)
         return e;
     const size_t mn = (size_t)M * N;
