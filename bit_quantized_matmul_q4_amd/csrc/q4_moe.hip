@@ -838,40 +838,46 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(OP::waves(R
     }
 }
 
-// y[m] = sum_j weights[m][j] t[m, j], in the order of j.  grid = (1024 columns,
-// rows).
-__global__ __launch_bounds__(256) void q4_moe_join_kernel(const int *__restrict__ ids, const float *__restrict__ weights,
-                                                          const float *__restrict__ t, float *__restrict__ y, int topk,
-                                                          int E, int H)
+// y[m] = sum_j weights[m][j] t[m, j], in the order of j.  grid = (256 columns,
+// rows).  The choice and the products are loaded together, whether a slot has
+// an expert or not (a slot without one holds no product: its values are not
+// used).
+__global__ __launch_bounds__(64) void q4_moe_join_kernel(const int *__restrict__ ids, const float *__restrict__ weights,
+                                                         const float *__restrict__ t, float *__restrict__ y, int topk,
+                                                         int E, int H, int vec)
 {
-    const int col = (blockIdx.x * 256 + threadIdx.x) * 4;
+    const int col = (blockIdx.x * 64 + threadIdx.x) * 4;
     const size_t m = blockIdx.y;
     if (col >= H)
         return;
     f32x4 sum = {0.f, 0.f, 0.f, 0.f};
     for (int j0 = 0; j0 < topk; j0 += 8) {
         f32x4 v[8];
-        bool has[8];
+        float w[8];
+        int id[8];
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-            const size_t slot = m * topk + j0 + j;
-            has[j] = j0 + j < topk && slot_expert(ids[slot], E) >= 0;
-            if (has[j])
-                v[j] = *(const f32x4 *)(t + slot * H + col);
+            const size_t slot = m * topk + min(j0 + j, topk - 1);
+            id[j] = ids[slot];
+            w[j] = weights[slot];
+            v[j] = *(const f32x4 *)(t + slot * H + col);
         }
 #pragma unroll
         for (int j = 0; j < 8; ++j)
-            if (has[j]) {
-                const float w = weights[m * topk + j0 + j];
+            if (j0 + j < topk && slot_expert(id[j], E) >= 0) {
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
-                    sum[i] = __builtin_fmaf(w, v[j][i], sum[i]);
+                    sum[i] = __builtin_fmaf(w[j], v[j][i], sum[i]);
             }
     }
     float *out = y + m * H + col;
+    if (vec) {
+        *(f32x4 *)out = sum;
+    } else {
 #pragma unroll
-    for (int i = 0; i < 4; ++i)  // (y is aligned to 4 bytes)
-        out[i] = sum[i];
+        for (int i = 0; i < 4; ++i)
+            out[i] = sum[i];
+    }
 }
 
 size_t up256(size_t n) { return (n + 255) & ~(size_t)255; }
@@ -1019,8 +1025,8 @@ hipError_t products(const Choice &ch, const uint16_t *x, const int *lift, int *i
     e = launch_product(2, given, down, ids, weights, w2, s2, make_plan(I), stream);
     if (e != hipSuccess)
         return e;
-    hipLaunchKernelGGL(q4_moe_join_kernel, dim3((unsigned)((H + 1023) / 1024), (unsigned)ch.M), dim3(256), 0, stream, ids,
-                       weights, room.t, y, ch.topk, ch.E, H);
+    hipLaunchKernelGGL(q4_moe_join_kernel, dim3((unsigned)((H + 255) / 256), (unsigned)ch.M), dim3(64), 0, stream, ids,
+                       weights, room.t, y, ch.topk, ch.E, H, ((uintptr_t)y & 15) == 0);
     return hipGetLastError();
 }
 
@@ -1108,16 +1114,16 @@ hipError_t launch_moe_layer(const void *x, int x_kind, const void *router, int r
     const MoeRoom room(rest, M, topk, H, I);
     const uint16_t *xp = bf16 ? room.x16 : (const uint16_t *)x;
     const int *lift = bf16 ? room.lift : nullptr;
-    // (the part form of the logits, which is all that few rows use, takes x to
-    // binary16 on the side; otherwise the select kernel does)
-    const bool fused = (long long)M * E * E <= kFused && !(count == 1 && H > kPart);
-    hipError_t e = launch_logits(x, x_kind, router, r_kind, parts, bf16 && fused ? room.x16 : nullptr, room.lift, M, E,
-                                 H, stream);
+    // x goes to binary16 beside the logits' parts, or beside the choice
+    const bool by_rows = count == 1 && H > kPart;
+    const bool fused = (long long)M * E * E <= kFused && !by_rows;
+    hipError_t e = launch_logits(x, x_kind, router, r_kind, parts, bf16 && !by_rows ? room.x16 : nullptr, room.lift, M,
+                                 E, H, stream);
     if (e != hipSuccess)
         return e;
     if (fused)
         return products(ch, xp, lift, ids, weights, w13, s13, w2, s2, y, H, I, room, stream);
-    e = launch_select(ch, ids, weights, x, bf16 ? room.x16 : nullptr, room.lift, H, stream);
+    e = launch_select(ch, ids, weights, x, bf16 && by_rows ? room.x16 : nullptr, room.lift, H, stream);
     if (e != hipSuccess)
         return e;
     const Choice given{nullptr, nullptr, 0, M, E, topk, 0};
