@@ -569,8 +569,8 @@ __global__ __launch_bounds__(64 * WM *WN) void q4_int8_gemm_kernel(
     constexpr int WAVES = WM * WN;
     constexpr int TM = BM / 16 / WM, TN = BN / 16 / WN;  // a wave's row tiles of x and of W
     constexpr int CHUNKS = (BM + BN) / 16 * 2;           // 1 KB pieces of a stage
-    static_assert(CHUNKS % WAVES == 0 && BM / 16 * 2 % (CHUNKS / WAVES) == 0, "a wave loads pieces of one operand");
-    constexpr int PER = CHUNKS / WAVES;
+    static_assert(BM / 8 % WAVES == 0 && BN / 8 % WAVES == 0, "every wave loads as many pieces of each operand");
+    constexpr int PER = CHUNKS / WAVES, PER_X = BM / 8 / WAVES;
     constexpr int STAGE = CHUNKS * 1024;
     extern __shared__ __attribute__((aligned(16))) int8_t lds[];
 
@@ -589,24 +589,26 @@ __global__ __launch_bounds__(64 * WM *WN) void q4_int8_gemm_kernel(
     const int bm = id % gm, bn = id / gm;
     const int s0 = blockIdx.y * steps_per, s1 = min(tiles / 2, s0 + steps_per);
 
-    // the pieces this wave loads: PER of x or of W (row tiles past the end: the
-    // last one, its outputs are not stored)
-    const int ch0 = wave * PER;
-    const bool of_x = ch0 < BM / 16 * 2;
-    const int t0 = of_x ? bm * (BM / 16) : bn * (BN / 16), t_all = of_x ? tm_all : tn_all;
-    const int rel = (of_x ? ch0 : ch0 - BM / 16 * 2) / 2;
-    const __amdgpu_buffer_rsrc_t src = __builtin_amdgcn_make_buffer_rsrc(
-        const_cast<int8_t *>((of_x ? xq : wq) + (size_t)t0 * tiles * 1024), (short)0,
-        min(t_all - t0, (of_x ? BM : BN) / 16) * tiles * 1024, 0x00020000);
+    // the pieces this wave loads, every WAVES-th: first of x, then of W (row
+    // tiles past the end: the last one, its outputs are not stored)
+    const int mt = bm * (BM / 16), nt = bn * (BN / 16);
+    const __amdgpu_buffer_rsrc_t xb = __builtin_amdgcn_make_buffer_rsrc(
+        const_cast<int8_t *>(xq + (size_t)mt * tiles * 1024), (short)0, min(tm_all - mt, BM / 16) * tiles * 1024,
+        0x00020000);
+    const __amdgpu_buffer_rsrc_t wb = __builtin_amdgcn_make_buffer_rsrc(
+        const_cast<int8_t *>(wq + (size_t)nt * tiles * 1024), (short)0, min(tn_all - nt, BN / 16) * tiles * 1024,
+        0x00020000);
     int at[PER];
 #pragma unroll
-    for (int i = 0; i < PER; ++i)
-        at[i] = min(rel + i / 2, t_all - 1 - t0) * tiles * 1024 + ((ch0 + i) & 1) * 1024;
+    for (int i = 0; i < PER; ++i) {
+        const int ch = (i < PER_X ? i : i - PER_X) * WAVES + wave;
+        at[i] = min(ch / 2, i < PER_X ? tm_all - 1 - mt : tn_all - 1 - nt) * tiles * 1024 + (ch & 1) * 1024;
+    }
     auto fetch = [&](int step) {  // (past the last step: the last again, so that the counts stay)
         const int stage = (step - s0) % NS, off = min(step, s1 - 1) * 2048;
 #pragma unroll
         for (int i = 0; i < PER; ++i)
-            load_lds(src, lds + stage * STAGE + (ch0 + i) * 1024, lane * 16, at[i] + off);
+            load_lds(i < PER_X ? xb : wb, lds + stage * STAGE + (i * WAVES + wave) * 1024, lane * 16, at[i] + off);
     };
     i32x4 acc[TN][TM];
 #pragma unroll
@@ -660,20 +662,15 @@ __global__ __launch_bounds__(64 * WM *WN) void q4_int8_gemm_kernel(
     }
     // lane (g, c) holds row c of a tile of x, rows 4 g .. 4 g + 3 of one of W
     const int m0 = bm * BM + wm * TM * 16 + (lane & 15), n0 = bn * BN + wn * TN * 16 + 4 * (lane >> 4);
-    if (partial) {
-        int *out = partial + (size_t)blockIdx.y * M * N;
+    if (partial) {  // a split's sums as they lie: [split][tile of W][tile of x][lane]
+        i32x4 *out = (i32x4 *)partial + (size_t)blockIdx.y * tn_all * tm_all * 64 + lane;
 #pragma unroll
         for (int i = 0; i < TN; ++i)
 #pragma unroll
             for (int j = 0; j < TM; ++j) {
-                const int m = m0 + 16 * j, n = n0 + 16 * i;
-                if (m < M && n < N) {
-                    int *p = out + (size_t)m * N + n;
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        if (n + e < N)
-                            p[e] = acc[i][j][e];
-                }
+                const int tn = nt + wn * TN + i, tm = mt + wm * TM + j;
+                if (tn < tn_all && tm < tm_all)
+                    out[((size_t)tn * tm_all + tm) * 64] = acc[i][j];
             }
         return;
     }
@@ -697,24 +694,35 @@ __global__ __launch_bounds__(64 * WM *WN) void q4_int8_gemm_kernel(
     }
 }
 
-// The split's integer sums, added and scaled.
+// The splits' sums, added and scaled: a wave a tile of 16 x 16.
 template <int YK>
-__global__ __launch_bounds__(256) void q4_int8_join_kernel(const int *__restrict__ partial, const float *__restrict__ sx,
-                                                           const float *__restrict__ sw, void *__restrict__ y, int N,
-                                                           size_t mn, int split)
+__global__ __launch_bounds__(256) void q4_int8_join_kernel(const i32x4 *__restrict__ partial,
+                                                           const float *__restrict__ sx, const float *__restrict__ sw,
+                                                           void *__restrict__ y, int M, int N, int split, int vec)
 {
-    const size_t i = (size_t)blockIdx.x * 256 + threadIdx.x;
-    if (i >= mn)
+    const int tm_all = (M + 15) / 16, tn_all = (N + 15) / 16, lane = threadIdx.x & 63;
+    const int all = tm_all * tn_all, tile = blockIdx.x * 4 + (threadIdx.x >> 6);
+    if (tile >= all)
         return;
-    int s = 0;
-    for (int j = 0; j < split; ++j)
-        s += partial[j * mn + i];
-    const size_t m = i / N;
-    const float v = scaled(s, split_scale(sx[m]), split_scale(sw[i - m * N]));
-    if constexpr (YK == 2)
-        ((float *)y)[i] = v;
-    else
-        ((uint16_t *)y)[i] = YK == 1 ? bf16_bits(v) : f16_bits(v);
+    const int m = tile % tm_all * 16 + (lane & 15), n = tile / tm_all * 16 + 4 * (lane >> 4);
+    i32x4 s = {0, 0, 0, 0};
+    for (int j0 = 0; j0 < split; j0 += 8) {
+        i32x4 v[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            v[j] = partial[((size_t)min(j0 + j, split - 1) * all + tile) * 64 + lane];
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            if (j0 + j < split)
+                s += v[j];
+    }
+    if (m >= M || n >= N)
+        return;
+    Scale ws[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        ws[i] = split_scale(n + i < N ? sw[n + i] : 0.f);
+    store4<YK>(y, (size_t)m * N + n, N - n, vec, scaled4(s, split_scale(sx[m]), ws));
 }
 
 constexpr int kUnits = 256;  // compute units
@@ -735,11 +743,32 @@ Int8Shape int8_shape(bool dense, int M, int N, int K)
     Int8Shape s{dense && M <= 4 && M * int8_tiles(K) * 64 <= 20 * 1024 && N <= 8192, M <= 64, 0, 0, 1};
     if (s.decode || s.gemv)
         return s;
-    const int big = ((M + 255) / 256) * ((N + 255) / 256);
-    s.bm = s.bn = big >= kUnits ? 256 : 128;
-    const int wgs = ((M + s.bm - 1) / s.bm) * ((N + s.bn - 1) / s.bn);
+    // The largest tile that still fills the card, and K split while half the
+    // workgroups that fit at once are missing.  Measured (us, 256 x 256 / 128 x
+    // 128 / 128 x 64 / 64 x 64, the others' splits as here): 4096 x 3584 x 18944
+    // (224 tiles of 256) 292 / 452 / - / -; 2048 x 3584 x 3584 (448 tiles of 128)
+    // - / 42.6 / 51.9 / 62.3; 333 x 18944 x 3584 (444) - / 38.3 / 43.5 / 48.3;
+    // 1024 x 3584 x 3584 (224) - / 33.3 / 28.1 / 34.8; 512 x 3584 x 3584 (112) -
+    // / 25.9 / 24.5 / 21.9; 124 x 3584 x 18944 (28) - / 34.1 / 33.0 / 30.5.
+    const auto count = [&](int bm, int bn) { return (long long)((M + bm - 1) / bm) * ((N + bn - 1) / bn); };
+    int at_once;
+    if (count(256, 256) >= 200) {
+        s.bm = s.bn = 256;
+        at_once = kUnits;
+    } else if (count(128, 128) >= 400) {
+        s.bm = s.bn = 128;
+        at_once = 2 * kUnits;
+    } else if (count(128, 128) >= 200) {
+        s.bm = 128;
+        s.bn = 64;
+        at_once = 2 * kUnits;
+    } else {
+        s.bm = s.bn = 64;
+        at_once = 3 * kUnits;
+    }
+    const long long wgs = count(s.bm, s.bn);
     const int steps = int8_tiles(K) / 2;
-    while (2 * wgs * s.split <= kUnits && steps / (2 * s.split) >= 4)
+    while (2 * wgs * s.split <= at_once && steps / (2 * s.split) >= 4)
         s.split *= 2;
     return s;
 }
@@ -755,15 +784,9 @@ void launch_rows(const void *x, int8_t *codes, float *scales, int rows, int K, h
 template <int KIND, bool PACKED>
 void launch_rows_k(const void *x, int8_t *codes, float *scales, int rows, int K, hipStream_t stream)
 {
-#ifndef RW16
-#define RW16 1073741824
-#endif
-#ifndef RW4
-#define RW4 2048
-#endif
-    if (rows >= RW16)
-        launch_rows<KIND, 16, PACKED>(x, codes, scales, rows, K, stream);
-    else if (rows >= RW4)
+    // rows a workgroup: one spreads few rows over the card (4096 x 3584: 23 us
+    // with 16 rows, 12 with 4); from 2048 on four make the packed writes wider
+    if (rows >= 2048)
         launch_rows<KIND, 4, PACKED>(x, codes, scales, rows, K, stream);
     else
         launch_rows<KIND, 1, PACKED>(x, codes, scales, rows, K, stream);
@@ -873,7 +896,7 @@ size_t int8_workspace_bytes(bool dense, int M, int N, int K)
     if (dense && !sh.decode)
         n += up256(int8_packed_bytes(M, K)) + up256((size_t)M * sizeof(float));
     if (sh.split > 1)
-        n += (size_t)sh.split * M * N * sizeof(int);
+        n += (size_t)sh.split * ((M + 15) / 16) * ((N + 15) / 16) * 1024;
     return n;
 }
 
@@ -914,18 +937,25 @@ hipError_t launch_int8_linear(const void *x, int x_kind, const float *x_scales, 
     hipError_t e;
     if (sh.bm == 256)
         e = launch_tile<256, 256, 2, 4, 2>(y_kind, xq, sx, wq, w_scales, y, partial, M, N, K, sh.split, vec, stream);
+    else if (sh.bn == 128)
+        e = launch_tile<128, 128, 2, 2, 2>(y_kind, xq, sx, wq, w_scales, y, partial, M, N, K, sh.split, vec, stream);
+    else if (sh.bm == 128)
+        e = launch_tile<128, 64, 2, 2, 3>(y_kind, xq, sx, wq, w_scales, y, partial, M, N, K, sh.split, vec, stream);
     else
-        e = launch_tile<128, 128, 2, 2, 4>(y_kind, xq, sx, wq, w_scales, y, partial, M, N, K, sh.split, vec, stream);
+        e = launch_tile<64, 64, 2, 2, 3>(y_kind, xq, sx, wq, w_scales, y, partial, M, N, K, sh.split, vec, stream);
     if (e != hipSuccess || !partial)
         return e;
-    const size_t mn = (size_t)M * N;
-    const dim3 grid((unsigned)((mn + 255) / 256));
+    const dim3 grid((unsigned)(((M + 15) / 16 * ((N + 15) / 16) + 3) / 4));
+    const i32x4 *sums = (const i32x4 *)partial;
     if (y_kind == 2)
-        hipLaunchKernelGGL(q4_int8_join_kernel<2>, grid, dim3(256), 0, stream, partial, sx, w_scales, y, N, mn, sh.split);
+        hipLaunchKernelGGL(q4_int8_join_kernel<2>, grid, dim3(256), 0, stream, sums, sx, w_scales, y, M, N, sh.split,
+                           vec);
     else if (y_kind == 1)
-        hipLaunchKernelGGL(q4_int8_join_kernel<1>, grid, dim3(256), 0, stream, partial, sx, w_scales, y, N, mn, sh.split);
+        hipLaunchKernelGGL(q4_int8_join_kernel<1>, grid, dim3(256), 0, stream, sums, sx, w_scales, y, M, N, sh.split,
+                           vec);
     else
-        hipLaunchKernelGGL(q4_int8_join_kernel<0>, grid, dim3(256), 0, stream, partial, sx, w_scales, y, N, mn, sh.split);
+        hipLaunchKernelGGL(q4_int8_join_kernel<0>, grid, dim3(256), 0, stream, sums, sx, w_scales, y, M, N, sh.split,
+                           vec);
     return hipGetLastError();
 }
 
