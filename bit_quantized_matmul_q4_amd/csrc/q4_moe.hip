@@ -288,10 +288,14 @@ __device__ __forceinline__ void choose_rows(const Choice &ch, int m0, int rows, 
         const int row = p / E, e = p - row * E;
         const uint64_t key = keys[p], *k = keys + row * E;
         int rank = 0;
-#pragma unroll 8
-        for (int f = at; f < E; f += share) {
-            const uint64_t o = k[f];
-            rank += (o > key) | ((o == key) & (f < e));
+        for (int f0 = at; f0 < E; f0 += 8 * share) {  // (eight at a time: one wait for LDS; 0 is below every key)
+            uint64_t o[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                o[i] = f0 + i * share < E ? k[f0 + i * share] : 0ull;
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                rank += (o[i] > key) | ((o[i] == key) & (f0 + i * share < e));
         }
         for (int d = 1; d < share; d *= 2)
             rank += __shfl_xor(rank, d);
