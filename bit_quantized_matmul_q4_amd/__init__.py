@@ -53,6 +53,9 @@ def _stream(dev: torch.device):
 
 
 def _need(t: torch.Tensor, name: str, dtypes, ndim: int, device=None):
+    if (type(t) is torch.Tensor and t.is_cuda and t.dtype in dtypes and t.dim() == ndim and t.is_contiguous()
+            and (device is None or t.device == device)):
+        return
     if not isinstance(t, torch.Tensor):
         raise TypeError("%s must be a torch.Tensor" % name)
     if t.device.type != "cuda":
@@ -303,7 +306,7 @@ _DTYPES = {torch.float32: _lib.Q4_F32, torch.bfloat16: _lib.Q4_BF16, torch.float
 
 
 def _int8_bytes(rows: int, K: int) -> int:
-    n = int(_lib.load().q4_int8_packed_bytes(rows, K))
+    n = _lib.load().q4_int8_packed_bytes(rows, K)
     if n == 0:
         raise ValueError("bad shape %d x %d (K must be a positive multiple of 32, at most 131040)" % (rows, K))
     return n
@@ -329,10 +332,8 @@ def quantize_int8(w: torch.Tensor):
     R, K = w.shape
     codes = torch.empty((R, K), dtype=torch.int8, device=w.device)
     scales = torch.empty(R, dtype=torch.float32, device=w.device)
-    with torch.cuda.device(w.device):
-        st = lib.q4_int8_quantize(w.data_ptr(), _DTYPES[w.dtype], codes.data_ptr(), scales.data_ptr(), R, K,
-                                  _stream(w.device))
-    _lib.check(st, "q4_int8_quantize")
+    _call(w.device, "q4_int8_quantize", lib.q4_int8_quantize, w.data_ptr(), _DTYPES[w.dtype], codes.data_ptr(),
+          scales.data_ptr(), R, K)
     return codes, scales
 
 
@@ -358,11 +359,15 @@ def quantize_pack_int8(w: torch.Tensor) -> Int8Matrix:
     R, K = w.shape
     packed = torch.empty(_int8_bytes(R, K), dtype=torch.int8, device=w.device)
     scales = torch.empty(R, dtype=torch.float32, device=w.device)
-    with torch.cuda.device(w.device):
-        st = lib.q4_int8_quantize_pack(w.data_ptr(), _DTYPES[w.dtype], packed.data_ptr(), scales.data_ptr(), R, K,
-                                       _stream(w.device))
-    _lib.check(st, "q4_int8_quantize_pack")
+    _call(w.device, "q4_int8_quantize_pack", lib.q4_int8_quantize_pack, w.data_ptr(), _DTYPES[w.dtype],
+          packed.data_ptr(), scales.data_ptr(), R, K)
     return Int8Matrix(packed, scales, R, K)
+
+
+def _need_out(out, shape, dtypes, dev):
+    _need(out, "out", dtypes, 2, dev)
+    if tuple(out.shape) != shape:
+        raise ValueError("out must be [%d, %d]" % shape)
 
 
 def _workspace(workspace, need: int, dev):
@@ -388,13 +393,14 @@ def linear_int8(x, w: Int8Matrix, out: torch.Tensor | None = None, out_dtype: to
     used as given; False/None for calls that need none.
     """
     lib = _lib.load()
-    dense = not isinstance(x, Int8Matrix)
-    if dense:
+    if not isinstance(x, Int8Matrix):
         _need(x, "x", (torch.bfloat16, torch.float16), 2)
         M, K = x.shape
+        kind, x_ptr, xs_ptr = _DTYPES[x.dtype], x.data_ptr(), None
     else:
         _need_int8(x, "x")
         M, K = x.rows, x.K
+        kind, x_ptr, xs_ptr = _lib.Q4_I8, x.codes.data_ptr(), x.scales.data_ptr()
     dev = x.device
     _need_int8(w, "w", dev)
     N = w.rows
@@ -405,14 +411,10 @@ def linear_int8(x, w: Int8Matrix, out: torch.Tensor | None = None, out_dtype: to
             raise TypeError("out_dtype must be one of %s" % (tuple(_DTYPES),))
         out = torch.empty((M, N), dtype=out_dtype, device=dev)
     else:
-        _need(out, "out", tuple(_DTYPES), 2, dev)
-        if tuple(out.shape) != (M, N):
-            raise ValueError("out must be [%d, %d]" % (M, N))
-    kind = _DTYPES[x.dtype] if dense else _lib.Q4_I8
+        _need_out(out, (M, N), _DTYPES, dev)
     _keep, ws_ptr, ws_len = _workspace(workspace, lib.q4_int8_workspace_bytes(M, N, K, kind), dev)
-    _call(dev, "q4_int8_linear", lib.q4_int8_linear, x.data_ptr() if dense else x.codes.data_ptr(), kind, None if
-          dense else x.scales.data_ptr(), w.codes.data_ptr(), w.scales.data_ptr(), out.data_ptr(),
-          _DTYPES[out.dtype], M, N, K, ws_ptr, ws_len)
+    _call(dev, "q4_int8_linear", lib.q4_int8_linear, x_ptr, kind, xs_ptr, w.codes.data_ptr(), w.scales.data_ptr(),
+          out.data_ptr(), _DTYPES[out.dtype], M, N, K, ws_ptr, ws_len)
     return out
 
 
@@ -444,12 +446,6 @@ def _need_experts(x, w13, w2):
         raise ValueError("x [%d, %d] with w13 %d x %d and w2 %d x %d: w13 is (E 2 I) x H, w2 (E H) x I"
                          % (M, H, w13.N, w13.K, w2.N, w2.K))
     return E, I
-
-
-def _need_out(out, shape, dtypes, dev):
-    _need(out, "out", dtypes, 2, dev)
-    if tuple(out.shape) != shape:
-        raise ValueError("out must be [%d, %d]" % shape)
 
 
 def _need_q4(w, name: str, dev):

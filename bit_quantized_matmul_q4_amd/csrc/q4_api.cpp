@@ -94,7 +94,7 @@ int check_int8(long long rows, long long N, long long K)
 {
     if (rows < 1 || N < 1 || K < 32 || K % 32 != 0 || K > Q4_INT8_MAX_K)
         return Q4_ERR_SHAPE;
-    const long long lim = 1LL << 26;
+    const long long lim = 1LL << 24;
     if (rows > lim || N > lim || rows > (1LL << 36) / N)
         return Q4_ERR_SHAPE;
     return Q4_OK;

@@ -166,14 +166,15 @@ __device__ __forceinline__ u32x4 codes_of(const u32x4 (&v)[VECS], const RowScale
 }
 
 // One workgroup quantizes RW rows (a divisor of 16); a wave's 64 lanes are RW
-// rows by 64 / RW pieces of 16 k, so with RW = 16 both the reads (whole
-// 128-byte lines) and the packed writes (1 KB) are contiguous; fewer rows a
-// workgroup spread few rows over more compute units.  Two passes over the
-// row: the largest |x|, then the codes; the second reads the first HELD
-// pieces of each lane from registers and the rest from the L2.
+// rows by 64 / RW pieces of 16 k.  One row a workgroup spreads few rows over
+// the card, several make the pieces of a packed tile that a wave writes lie
+// together.  Two passes over the row: the largest |x|, then the codes; the
+// second takes the first HELD pieces of each lane from registers (a row of
+// 32768 with one row a workgroup) and the rest from the L2.
 // PACKED: the packed layout (padding written), else codes [rows][K].
 // grid = row groups (PACKED: of the padded rows, so that padding rows are
-// written too).
+// written too).  Bound by memory latency for few rows (4 us at 124 x 3584), by
+// memory for many: 4096 x 3584 in 12 us, 3.7 TB/s.
 constexpr int kQuantThreads = 512;
 
 template <int KIND, int RW, bool PACKED>
@@ -425,8 +426,8 @@ __global__ __launch_bounds__(64 * kDecodeWaves) void q4_int8_decode_kernel(const
     constexpr int W = kDecodeWaves, U = kDecodeChunk;
     extern __shared__ __attribute__((aligned(16))) int8_t xl[];  // [k16 piece][row][16]
     __shared__ i32x4 part[W][64];
-    __shared__ uint32_t tops[16];
-    __shared__ float scale_of[16];
+    __shared__ uint32_t tops[4];
+    __shared__ float scale_of[4];
     const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
     const int g = lane >> 4, c = min(lane & 15, M - 1);
     const int steps = int8_tiles(K);
@@ -443,65 +444,62 @@ __global__ __launch_bounds__(64 * kDecodeWaves) void q4_int8_decode_kernel(const
     u32x4 w0[U], w1[U];
     fetch(w0, 0);
 
-    // the rows: as many waves each as there are, or a wave several rows in turn
+    // the rows: W / per of them at once, at least M (at most 4: see int8_shape)
     {
         typedef Elem<KIND> E;
         constexpr int HELD = 2, VECS = (int)sizeof(E);
         int per = W;
-        while (per > 1 && W / per < M)
+        while (W / per < M)
             per /= 2;
-        const int pieces = K / 16, step = 64 * per, p0 = (wave % per) * 64 + lane;
-        if (tid < 16)
+        const int row = wave / per, pieces = K / 16, step = 64 * per, p0 = (wave % per) * 64 + lane;
+        const E *x = (const E *)x_ + (size_t)min(row, M - 1) * K;
+        u32x4 held[HELD][VECS];
+        uint32_t top = 0;
+        auto load = [&](int p, u32x4 (&v)[VECS]) {
+#pragma unroll
+            for (int i = 0; i < VECS; ++i)
+                v[i] = *((const u32x4 *)(x + 16 * (size_t)p) + i);
+        };
+        if (tid < 4)
             tops[tid] = 0;
         __syncthreads();
-        for (int row0 = 0; row0 < M; row0 += W / per) {
-            const int row = row0 + wave / per;
-            const E *x = (const E *)x_ + (size_t)min(row, M - 1) * K;
-            u32x4 held[HELD][VECS];
-            uint32_t top = 0;
-            auto load = [&](int p, u32x4 (&v)[VECS]) {
+        if (row < M) {
 #pragma unroll
-                for (int i = 0; i < VECS; ++i)
-                    v[i] = *((const u32x4 *)(x + 16 * (size_t)p) + i);
-            };
-            if (row < M) {
+            for (int h = 0; h < HELD; ++h)
+                if (p0 + h * step < pieces)
+                    load(p0 + h * step, held[h]);
 #pragma unroll
-                for (int h = 0; h < HELD; ++h)
-                    if (p0 + h * step < pieces)
-                        load(p0 + h * step, held[h]);
-#pragma unroll
-                for (int h = 0; h < HELD; ++h)
-                    if (p0 + h * step < pieces)
-                        top = max(top, top_of<KIND>(held[h]));
-                for (int p = p0 + HELD * step; p < pieces; p += step) {
-                    u32x4 v[VECS];
-                    load(p, v);
-                    top = max(top, top_of<KIND>(v));
-                }
-#pragma unroll
-                for (int d = 1; d < 64; d *= 2)
-                    top = max(top, (uint32_t)__shfl_xor((int)top, d));
-                if (lane == 0)
-                    atomicMax(&tops[row], top);
+            for (int h = 0; h < HELD; ++h)
+                if (p0 + h * step < pieces)
+                    top = max(top, top_of<KIND>(held[h]));
+            for (int p = p0 + HELD * step; p < pieces; p += step) {
+                u32x4 v[VECS];
+                load(p, v);
+                top = max(top, top_of<KIND>(v));
             }
-            __syncthreads();
-            if (row < M) {
-                const RowScale rs = row_scale<KIND>(tops[row]);
-                if (p0 == 0)
-                    scale_of[row] = rs.scale;
-                for (int h = 0, p = p0; p < 4 * steps; ++h, p += step) {
-                    u32x4 v = {0, 0, 0, 0};
-                    if (p < pieces) {
-                        if (h >= HELD) {
-                            u32x4 raw[VECS];
-                            load(p, raw);
-                            v = codes_of<KIND>(raw, rs);
-                        } else {
-                            v = codes_of<KIND>(h == 0 ? held[0] : held[1], rs);
-                        }
+#pragma unroll
+            for (int d = 1; d < 64; d *= 2)
+                top = max(top, (uint32_t)__shfl_xor((int)top, d));
+            if (lane == 0)
+                atomicMax(&tops[row], top);
+        }
+        __syncthreads();
+        if (row < M) {
+            const RowScale rs = row_scale<KIND>(tops[row]);
+            if (p0 == 0)
+                scale_of[row] = rs.scale;
+            for (int h = 0, p = p0; p < 4 * steps; ++h, p += step) {
+                u32x4 v = {0, 0, 0, 0};
+                if (p < pieces) {
+                    if (h >= HELD) {
+                        u32x4 raw[VECS];
+                        load(p, raw);
+                        v = codes_of<KIND>(raw, rs);
+                    } else {
+                        v = codes_of<KIND>(h == 0 ? held[0] : held[1], rs);
                     }
-                    *(u32x4 *)(xl + ((size_t)p * M + row) * 16) = v;
                 }
+                *(u32x4 *)(xl + ((size_t)p * M + row) * 16) = v;
             }
         }
         __syncthreads();
@@ -787,8 +785,9 @@ void launch_rows(const void *x, int8_t *codes, float *scales, int rows, int K, h
 template <int KIND, bool PACKED>
 void launch_rows_k(const void *x, int8_t *codes, float *scales, int rows, int K, hipStream_t stream)
 {
-    // rows a workgroup: one spreads few rows over the card (4096 x 3584: 23 us
-    // with 16 rows, 12 with 4); from 2048 on four make the packed writes wider
+    // rows a workgroup (16 were slower everywhere: 4096 x 3584 in 23 us against
+    // 12 with four; one against four at 1024 rows 31.2 against 32.5 us with the
+    // product, at 4096 rows 306 against 299)
     if (rows >= 2048)
         launch_rows<KIND, 4, PACKED>(x, codes, scales, rows, K, stream);
     else

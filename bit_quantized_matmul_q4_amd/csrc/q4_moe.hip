@@ -687,6 +687,7 @@ struct Up {
     int *shift;
     int M, topk, H, I, shifts;
 
+    static constexpr int most = 4;  // the largest RM
     // waves of a compute unit's quarter that the registers are to hold
     static constexpr int waves(int RM) { return RM == 4 ? 3 : 4; }
     template <int R>
@@ -746,6 +747,7 @@ struct Down {
     float *t;
     int H;
 
+    static constexpr int most = 2;  // (two operands a row: 16 rows do not fit the registers)
     static constexpr int waves(int RM) { return RM == 1 ? 4 : 3; }
     template <int R>
     using Rows = RowsH<R>;
@@ -988,29 +990,21 @@ hipError_t launch_product_r(const Choice &ch, const OP &op, int *ids, float *wei
     size_t lds = (size_t)waves * tree_levels(L) * 4 * RM * 64 * sizeof(float);
     if (ch.parts)
         lds = std::max(lds, (size_t)(ch.M * ch.E + n) * sizeof(double));
-    if (lds > 48 * 1024) {
-        const hipError_t e = hipFuncSetAttribute((const void *)q4_moe_product_kernel<OP, RM>,
-                                                 hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
-        if (e != hipSuccess)
-            return e;
-    }
     hipLaunchKernelGGL((q4_moe_product_kernel<OP, RM>), grid, dim3(64 * waves), lds, stream, ch, op, ids, weights,
                        wq, scales, L, plan);
     return hipGetLastError();
 }
 
 template <typename OP>
-hipError_t launch_product(int most, const Choice &ch, const OP &op, int *ids, float *weights, const uint8_t *wq,
+hipError_t launch_product(const Choice &ch, const OP &op, int *ids, float *weights, const uint8_t *wq,
                           const uint16_t *scales, const Plan &plan, hipStream_t stream)
 {
-    const int RM = std::min(most, row_group(ch.M * ch.topk, ch.E));
+    const int RM = row_group(ch.M * ch.topk, ch.E);
     if (RM == 1)
         return launch_product_r<OP, 1>(ch, op, ids, weights, wq, scales, plan, stream);
-    if (RM == 2)
+    if (RM == 2 || OP::most == 2)
         return launch_product_r<OP, 2>(ch, op, ids, weights, wq, scales, plan, stream);
-    if constexpr (std::is_same<OP, Up>::value)
-        return launch_product_r<OP, 4>(ch, op, ids, weights, wq, scales, plan, stream);
-    return hipErrorInvalidValue;
+    return launch_product_r<OP, OP::most>(ch, op, ids, weights, wq, scales, plan, stream);
 }
 
 // The products of a piece of rows; ch.parts: the gate/up kernel chooses.
@@ -1020,13 +1014,13 @@ hipError_t products(const Choice &ch, const uint16_t *x, const int *lift, int *i
 {
     const int n = ch.M * ch.topk, shifts = MoeRoom::shifts_of(I);
     const Up up{x, lift, room.hi, room.lo, room.shift, ch.M, ch.topk, H, I, shifts};
-    hipError_t e = launch_product(4, ch, up, ids, weights, w13, s13, make_plan(H), stream);
+    hipError_t e = launch_product(ch, up, ids, weights, w13, s13, make_plan(H), stream);
     if (e != hipSuccess)
         return e;
     Choice given = ch;
     given.parts = nullptr;
     const Down down{{room.hi, room.lo, room.shift, n, I, shifts}, room.t, H};
-    e = launch_product(2, given, down, ids, weights, w2, s2, make_plan(I), stream);
+    e = launch_product(given, down, ids, weights, w2, s2, make_plan(I), stream);
     if (e != hipSuccess)
         return e;
     hipLaunchKernelGGL(q4_moe_join_kernel, dim3((unsigned)((H + 255) / 256), (unsigned)ch.M), dim3(64), 0, stream, ids,

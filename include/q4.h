@@ -236,7 +236,7 @@ int q4_quantize(const void *w, int w_dtype, uint8_t *codes, void *scales, int N,
  * and W alone (not on M, the row's place, the kernel or the split of K).
  * The value is formed in binary32 (at most three roundings, and no overflow
  * or underflow on the way), then rounded to the output type.  K is a multiple of 32, at most Q4_INT8_MAX_K (the sum stays exact
- * for codes down to -128); rows and N are at most 2^26, rows N at most 2^36.
+ * for codes down to -128); rows and N are at most 2^24, rows N at most 2^36.
  *
  * Canonical form: codes int8 [rows][K], scales float32 [rows], row-major.
  * Packed form: tiles of 16 rows by 64 k (t = row / 16, q = k / 64), tile

@@ -136,6 +136,19 @@ def test_route_masked_and_not_finite(renormalize):
     assert torch.isnan(w[2]).all() and ((ids[2] >= 0) & (ids[2] < E)).all()
 
 
+def test_route_rows_do_not_depend_on_the_form():
+    """Enough tiles for the form that keeps a row's whole sum in a wave: the bits of the one that splits it."""
+    gu.note("moe_route forms")
+    g = gen(14)
+    for t in (torch.bfloat16, torch.float32):
+        x = torch.randn(530, 832, generator=g).bfloat16().cuda()
+        r = (torch.randn(512, 832, generator=g) / 29).to(t).cuda()
+        ids, w = q4.moe_route(x, r, 5, None, False)
+        i, v = q4.moe_route(x[500:].contiguous(), r, 5, None, False)
+        torch.cuda.synchronize()
+        assert torch.equal(i, ids[500:]) and torch.equal(v.view(torch.int32), w[500:].view(torch.int32))
+
+
 def test_route_rows_do_not_depend_on_the_batch():
     gu.note("moe_route rows")
     g = gen(4)
@@ -318,7 +331,9 @@ def test_rows_do_not_depend_on_the_batch(H, I):
 @pytest.mark.parametrize("M,E,H,I,topk,xt", [(1, 8, 96, 64, 2, "bf16"), (4, 128, 288, 32, 8, "f16"),
                                               (16, 64, 512, 96, 5, "bf16"), (17, 64, 512, 96, 5, "bf16"),
                                               (9, 120, 160, 32, 3, "bf16"), (3, 5, 4256, 32, 2, "bf16"),
-                                              (300, 12, 64, 32, 6, "bf16"), (300, 12, 64, 32, 6, "f16")])
+                                              (300, 12, 64, 32, 6, "bf16"), (300, 12, 64, 32, 6, "f16"),
+                                              (1024, 1, 64, 32, 1, "bf16"), (1000, 4, 64, 32, 1, "f16"),
+                                              (1024, 256, 288, 32, 1, "bf16")])
 @pytest.mark.parametrize("renormalize", [True, False])
 def test_layer_is_route_and_experts(M, E, H, I, topk, xt, renormalize):
     """The whole layer in one call, in each of its forms: the bits of its two parts."""
