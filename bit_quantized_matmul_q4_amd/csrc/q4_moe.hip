@@ -980,10 +980,15 @@ hipError_t launch_product_r(const Choice &ch, const OP &op, int *ids, float *wei
 {
     const int n = ch.M * ch.topk;
     const dim3 grid((unsigned)op.units(), (unsigned)std::min(n, ch.E));
-    // as few waves a unit as fill the card (four a quarter of a compute unit): a
-    // longer stream each, less to join
+    // waves a unit: as many as the card runs at once (and half as many again,
+    // for experts that nobody chose), and runs of at most 8 quads.  Measured, gate/up +
+    // down: 64 experts 3584 x 1792 at 64 rows with 4 + 2 waves 102 + 74 us,
+    // with 2 + 2 123 + 74, with 4 + 4 102 + 87; 8 experts 3584 x 2560 at 64
+    // rows, the layer with 4 waves 102 us, with 8 112; 64 experts 2048 x 1024 at
+    // 4 rows with 4 waves 39 us, with 2 43, with 8 47.
+    const size_t units = (size_t)grid.x * grid.y;
     int waves = 1;
-    while (waves < 8 && (size_t)grid.x * grid.y * waves < 4096)
+    while (waves < 8 && (2 * waves * units <= (size_t)1536 * OP::waves(RM) || plan.G > 8 * waves))
         waves *= 2;
     waves = std::min(waves, plan.S);
     const int L = plan.S / waves;
