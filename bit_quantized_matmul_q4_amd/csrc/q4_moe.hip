@@ -687,9 +687,8 @@ struct Up {
     int *shift;
     int M, topk, H, I, shifts;
 
-    static constexpr int most = 4;  // the largest RM
     // waves of a compute unit's quarter that the registers are to hold
-    static constexpr int waves(int RM) { return RM == 4 ? 3 : 4; }
+    static constexpr int waves(int RM) { return RM == 1 ? 4 : 3; }
     template <int R>
     using Rows = RowsX<R>;
     __host__ __device__ int units() const { return I / 32; }
@@ -747,8 +746,7 @@ struct Down {
     float *t;
     int H;
 
-    static constexpr int most = 2;  // (two operands a row: 16 rows do not fit the registers)
-    static constexpr int waves(int RM) { return RM == 1 ? 4 : 3; }
+    static constexpr int waves(int RM) { return RM == 1 ? 4 : RM == 2 ? 3 : 2; }
     template <int R>
     using Rows = RowsH<R>;
     __host__ __device__ int units() const { return (H + 63) / 64; }
@@ -966,12 +964,15 @@ struct MoeRoom {
     static int shifts_of(int I) { return (I / 32 + 3) / 4 * 4; }
 };
 
-// The largest group of rows a product is built for: by the rows an expert gets
-// on average.
+// The largest group of rows a product is built for (4 RM): by the rows an
+// expert gets on average.  A group takes a weight through its dequantization
+// once, a larger one costs registers: 64 experts 3584 x 1792 with 6 rows each
+// in groups of at most 8 / 16 188 / 168 us, 128 experts 2048 x 768 with 4 rows
+// each 96 / 98 us.
 int row_group(int n, int E)
 {
     const int rows = n / std::min(n, E);
-    return rows <= 1 ? 1 : rows <= 7 ? 2 : 4;
+    return rows <= 1 ? 1 : rows <= 4 ? 2 : 4;
 }
 
 template <typename OP, int RM>
@@ -1007,9 +1008,9 @@ hipError_t launch_product(const Choice &ch, const OP &op, int *ids, float *weigh
     const int RM = row_group(ch.M * ch.topk, ch.E);
     if (RM == 1)
         return launch_product_r<OP, 1>(ch, op, ids, weights, wq, scales, plan, stream);
-    if (RM == 2 || OP::most == 2)
+    if (RM == 2)
         return launch_product_r<OP, 2>(ch, op, ids, weights, wq, scales, plan, stream);
-    return launch_product_r<OP, OP::most>(ch, op, ids, weights, wq, scales, plan, stream);
+    return launch_product_r<OP, 4>(ch, op, ids, weights, wq, scales, plan, stream);
 }
 
 // The products of a piece of rows; ch.parts: the gate/up kernel chooses.
