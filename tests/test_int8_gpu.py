@@ -241,6 +241,8 @@ def test_refusals():
         q4.linear_int8(x, w, out_dtype=torch.float64)
     with pytest.raises(q4.Q4Error):
         q4.linear_int8(x[:0], w)
+    with pytest.raises(q4.Q4Error):  # two bytes off
+        q4.linear_int8(torch.zeros(4 * 64 + 1, dtype=torch.bfloat16, device="cuda")[1:].view(4, 64), w)
     with pytest.raises(ValueError):
         q4.linear_int8(x, q4.Int8Matrix(w.codes[:1024], w.scales, 8, 64))
     with pytest.raises(ValueError):

@@ -229,7 +229,8 @@ def choose(g, M, E, topk):
 
 SHAPES = [(1, 1, 32, 32, 1), (1, 4, 64, 96, 2), (2, 3, 160, 32, 3), (3, 8, 896, 160, 4), (5, 6, 128, 1376, 2),
           (8, 16, 224, 544, 8), (9, 40, 512, 64, 3), (17, 7, 288, 96, 5), (30, 3, 96, 128, 2), (64, 12, 544, 288, 4),
-          (4, 2, 3584, 2592, 2), (1, 2, 4256, 64, 1), (12, 2, 64, 4128, 1)]
+          (4, 2, 3584, 2592, 2), (1, 2, 4256, 64, 1), (12, 2, 64, 4128, 1), (40, 1024, 32, 32, 20), (60, 70, 64, 32, 17),
+          (33, 2, 2080, 160, 1)]
 
 
 @pytest.mark.parametrize("M,E,H,I,topk", SHAPES)
@@ -427,6 +428,29 @@ def test_layer_together_graph_and_streams():
             assert all(torch.equal(p, q) for p, q in zip(out, eager)), i
 
 
+def test_two_streams_at_once():
+    """Two streams with calls of their own in flight together, and a third of both operators' inputs shared."""
+    gu.note("two streams")
+    E, H, I, topk = 24, 512, 160, 4
+    layer = Layer(E, H, I, 10)
+    g = gen(10)
+    r = (torch.randn(E, H, generator=g) / H**0.5).bfloat16().cuda()
+    w = q4.quantize_pack_int8((torch.randn(2000, H, generator=g) / 22).cuda())
+    xs = [torch.randn(M, H, generator=g).bfloat16().cuda() for M in (3, 70)]
+    ref = [(q4.moe(x, r, layer.w13, layer.w2, topk), q4.linear_int8(x, w)) for x in xs]
+    streams = [torch.cuda.Stream() for _ in xs]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(20):
+        for i, (s, x) in enumerate(zip(streams, xs)):
+            with torch.cuda.stream(s):
+                got[i].append((q4.moe(x, r, layer.w13, layer.w2, topk), q4.linear_int8(x, w)))
+    torch.cuda.synchronize()
+    for i in range(2):
+        for a, b in got[i]:
+            assert torch.equal(a, ref[i][0]) and torch.equal(b, ref[i][1])
+
+
 def test_workspace_and_output_guards():
     gu.note("moe guards")
     layer = Layer(4, 96, 64, 8)
@@ -470,6 +494,11 @@ def test_refusals():
         q4.moe_route(x, r.cpu(), 2)
     with pytest.raises(q4.Q4Error):
         q4.moe_route(x[:0], r, 2)
+    off = torch.zeros(3 * 96 + 1, dtype=torch.bfloat16, device="cuda")[1:].view(3, 96)  # two bytes off
+    with pytest.raises(q4.Q4Error):
+        q4.moe_route(off, r, 2)
+    with pytest.raises(q4.Q4Error):
+        q4.moe(off, r, layer.w13, layer.w2, 2)
     with pytest.raises(TypeError):
         q4.moe_experts(x, ids.long(), w, layer.w13, layer.w2)
     with pytest.raises(ValueError):
