@@ -785,11 +785,11 @@ __host__ __device__ inline int tree_levels(int L)
     return n;
 }
 
-// One product of the layer.  grid = (units, min(slots, E)): a unit of four tiles
-// of one expert a workgroup, its waves on runs of L segments of K.  An expert's
-// rows go 4, 8 or 16 (at most 4 RM) at a time, by how many are left; the
-// weights of the next group's first quad are on their way while this one's
-// sums are joined.
+// One product of the layer.  grid = (units, min(slots, E), Z): a unit of four
+// tiles of one expert a workgroup, its waves on runs of L segments of K.  An
+// expert's rows go 4 RM at a time (the last ones 4, 8 or 16, by how many are
+// left), group r to the workgroup z = r mod Z; the weights of the next group's
+// first quad are on their way while this one's sums are joined.
 template <typename OP, int RM>
 __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(OP::waves(RM)))) void q4_moe_product_kernel(Choice ch, OP op, int *__restrict__ ids,
                                                              float *__restrict__ weights,
@@ -814,23 +814,22 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(OP::waves(R
         tiles = op.tiles(wq, scales, e, blockIdx.x, plan.G);
         first.load(tiles, qa, qb);
     });
-    for (int r0 = 0; r0 < count;) {
-        const int left = count - r0;
+    const int step = 4 * RM * gridDim.z;
+    for (int r0 = 4 * RM * blockIdx.z; r0 < count; r0 += step) {
+        const int left = min(count - r0, 4 * RM);
         const uint16_t *list = found.list + r0;
         auto group = [&](auto r) {
             constexpr int R = decltype(r)::value;
-            const int rows = min(left, 4 * R);
-            const int b = op.before(list, rows);
-            multiply_run<R, typename OP::template Rows<R>>(tiles, first, op.template in<R>(list, rows, plan.nb),
+            const int b = op.before(list, left);
+            multiply_run<R, typename OP::template Rows<R>>(tiles, first, op.template in<R>(list, left, plan.nb),
                                                            wave * L, L, plan, part + wave * levels * 4 * R * 64);
             if ((int)threadIdx.x < 16)
                 back[threadIdx.x] = b;
-            r0 += 4 * R;
-            if (r0 < count)
+            if (r0 + step < count)
                 first.load(tiles, qa, qb);
             __syncthreads();
-            op.template after<R>(Roots{part, waves, levels * 4 * R * 64}, back, list, rows, blockIdx.x);
-            if (r0 < count)
+            op.template after<R>(Roots{part, waves, levels * 4 * R * 64}, back, list, left, blockIdx.x);
+            if (r0 + step < count)
                 __syncthreads();  // the sums are read
         };
         if (RM == 1 || left <= 4)
@@ -980,14 +979,19 @@ hipError_t launch_product_r(const Choice &ch, const OP &op, int *ids, float *wei
                             const uint16_t *scales, const Plan &plan, hipStream_t stream)
 {
     const int n = ch.M * ch.topk;
-    const dim3 grid((unsigned)op.units(), (unsigned)std::min(n, ch.E));
+    // as many workgroups for an expert's rows as it has groups of 16 on average,
+    // up to four: the layer of 8 experts 2048 x 512 with 64 rows each 71 us with
+    // one, 53 with four; 1024 x 1024 with 256 rows each 285, 151, without a
+    // limit 238 (each reads the weights again)
+    const int experts = std::min(n, ch.E), groups = RM == 4 ? std::min(n / experts / 16 + 1, 4) : 1;
+    const dim3 grid((unsigned)op.units(), (unsigned)experts, (unsigned)groups);
     // waves a unit: as many as the card runs at once (and half as many again,
     // for experts that nobody chose), and runs of at most 8 quads.  Measured, gate/up +
     // down: 64 experts 3584 x 1792 at 64 rows with 4 + 2 waves 102 + 74 us,
     // with 2 + 2 123 + 74, with 4 + 4 102 + 87; 8 experts 3584 x 2560 at 64
     // rows, the layer with 4 waves 102 us, with 8 112; 64 experts 2048 x 1024 at
     // 4 rows with 4 waves 39 us, with 2 43, with 8 47.
-    const size_t units = (size_t)grid.x * grid.y;
+    const size_t units = (size_t)grid.x * grid.y * grid.z;
     int waves = 1;
     while (waves < 8 && (2 * waves * units <= (size_t)1536 * OP::waves(RM) || plan.G > 8 * waves))
         waves *= 2;

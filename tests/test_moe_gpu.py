@@ -230,7 +230,7 @@ def choose(g, M, E, topk):
 SHAPES = [(1, 1, 32, 32, 1), (1, 4, 64, 96, 2), (2, 3, 160, 32, 3), (3, 8, 896, 160, 4), (5, 6, 128, 1376, 2),
           (8, 16, 224, 544, 8), (9, 40, 512, 64, 3), (17, 7, 288, 96, 5), (30, 3, 96, 128, 2), (64, 12, 544, 288, 4),
           (4, 2, 3584, 2592, 2), (1, 2, 4256, 64, 1), (12, 2, 64, 4128, 1), (40, 1024, 32, 32, 20), (60, 70, 64, 32, 17),
-          (33, 2, 2080, 160, 1)]
+          (33, 2, 2080, 160, 1), (100, 2, 96, 160, 2), (64, 3, 544, 96, 3), (70, 1, 160, 64, 1)]
 
 
 @pytest.mark.parametrize("M,E,H,I,topk", SHAPES)
