@@ -317,7 +317,8 @@ def _need_int8(w, name: str, device=None):
         raise TypeError("%s must be an Int8Matrix (see pack_int8)" % name)
     _need(w.codes, name + ".codes", (torch.int8,), 1, device)
     _need(w.scales, name + ".scales", (torch.float32,), 1, w.codes.device)
-    if w.codes.numel() != _int8_bytes(w.rows, w.K) or w.scales.numel() != w.rows:
+    tiles = -(-w.rows // 16) * 2 * -(-w.K // 128)  # (q4_int8_packed_bytes, without the call)
+    if w.K % 32 or tiles < 1 or w.codes.numel() != 1024 * tiles or w.scales.numel() != w.rows:
         raise ValueError("%s does not hold %d x %d packed codes and %d scales" % (name, w.rows, w.K, w.rows))
 
 
@@ -453,8 +454,8 @@ def _need_q4(w, name: str, dev):
         raise TypeError("%s must be a Q4Weight (see pack)" % name)
     _need(w.codes, name + ".codes", (torch.uint8,), 1, dev)
     _need(w.scales, name + ".scales", (torch.float16,), 1, dev)
-    cb, sb = packed_sizes(w.N, w.K)
-    if w.codes.numel() != cb or w.scales.numel() * 2 != sb:
+    tiles = -(-w.N // 16) * -(-w.K // 128)  # (q4_packed_code_bytes, without the calls)
+    if w.K % 32 or tiles < 1 or w.codes.numel() != 1024 * tiles or w.scales.numel() != 64 * tiles:
         raise ValueError("packed %s sizes do not match N=%d K=%d" % (name, w.N, w.K))
 
 
