@@ -170,6 +170,10 @@ __global__ __launch_bounds__(256) void q4_moe_lift_kernel(const uint16_t *__rest
 
 // Few rows: grid = (16-expert tiles, 16-row tiles, parts), a wave a chain; the
 // reader adds the parts.  One more z takes the rows to binary16 (x16 given).
+// One row of 64 experts over 2048: 3.3 us, launch and latency (a workgroup per
+// 16 experts over all of K, its waves on every 16th chunk, took 7).  201 rows of
+// 127 experts over 3584, binary32 router: 9 us, conversions to binary64 and
+// the products.
 template <int XK, int RK>
 __global__ __launch_bounds__(256) void q4_moe_logits_kernel(const uint16_t *__restrict__ x,
                                                             const void *__restrict__ router,
@@ -335,6 +339,7 @@ __device__ __forceinline__ void choose_rows(const Choice &ch, int m0, int rows, 
 }
 
 // A workgroup a row; with x16, the last wave takes the row to binary16 first.
+// 3.6 us at one row of 64 experts, 5.4 at 201 rows of 127: latency.
 __global__ __launch_bounds__(512) void q4_moe_select_kernel(Choice ch, int *__restrict__ ids,
                                                             float *__restrict__ weights,
                                                             const uint16_t *__restrict__ x,
@@ -417,7 +422,9 @@ __device__ __forceinline__ f32x4 dot16(u32x4 a, u32x4 b, f32x4 c) { return block
 
 // Up to kFused compares of two logits the gate/up kernel chooses the experts
 // itself, so that the layer is four launches instead of five: every workgroup
-// ranks all rows, and the first writes the choice for the down kernel.
+// ranks all rows, and the first writes the choice for the down kernel.  One
+// row of 64 experts: 2.7 us more in gate/up against 3.7 us for the launch; 8
+// rows of 128 experts (131072 compares): gate/up 98 us against 22 + 6.
 constexpr int kFused = 16384;
 
 __device__ __forceinline__ int slot_expert(int id, int E) { return id >= 0 && id < E ? id : -1; }
@@ -790,11 +797,16 @@ __host__ __device__ inline int tree_levels(int L)
 // expert's rows go 4 RM at a time (the last ones 4, 8 or 16, by how many are
 // left), group r to the workgroup z = r mod Z; the weights of the next group's
 // first quad are on their way while this one's sums are joined.
+// Few rows: bound by launch and memory latency (64 experts 2048 x 1024 at one
+// row: gate/up with its choice 9.9 us, down 6.7 us).  Many: by the weights'
+// stream and the dequantization's issue (47 VALU operations a tile and quad, half of
+// the cycles) that overlap in part: 64 experts 3584 x 1792 at 64 rows, gate/up
+// 94 us (4.9 TB/s), down 68 us (3.4 TB/s); without the products the layer takes
+// 152 of then 205 us.
 template <typename OP, int RM>
-__global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(OP::waves(RM)))) void q4_moe_product_kernel(Choice ch, OP op, int *__restrict__ ids,
-                                                             float *__restrict__ weights,
-                                                             const uint8_t *__restrict__ wq,
-                                                             const uint16_t *__restrict__ scales, int L, Plan plan)
+__global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(OP::waves(RM)))) void q4_moe_product_kernel(
+    Choice ch, OP op, int *__restrict__ ids, float *__restrict__ weights, const uint8_t *__restrict__ wq,
+    const uint16_t *__restrict__ scales, int L, Plan plan)
 {
     extern __shared__ __attribute__((aligned(16))) float part[];  // [wave][level][tile][r][lane]
     __shared__ Found found;
@@ -804,7 +816,7 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(OP::waves(R
     if (ch.parts) {
         uint64_t *keys = (uint64_t *)part;
         choose_rows<int16_t>(ch, 0, ch.M, keys, (double *)(keys + ch.M * ch.E), found.who, ids, weights,
-                             blockIdx.x == 0 && blockIdx.y == 0);
+                             blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0);
         __syncthreads();  // (the keys' room is the products' next)
     }
     const int qa = (wave * L * plan.G) >> plan.log2S, qb = ((wave + 1) * L * plan.G) >> plan.log2S;
@@ -844,7 +856,7 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(OP::waves(R
 // y[m] = sum_j weights[m][j] t[m, j], in the order of j.  grid = (256 columns,
 // rows).  The choice and the products are loaded together, whether a slot has
 // an expert or not (a slot without one holds no product: its values are not
-// used).
+// used).  One memory latency: 2 to 4 us.
 __global__ __launch_bounds__(64) void q4_moe_join_kernel(const int *__restrict__ ids, const float *__restrict__ weights,
                                                          const float *__restrict__ t, float *__restrict__ y, int topk,
                                                          int E, int H, int vec)

@@ -340,7 +340,7 @@ int q4_moe_experts(const void *x, int x_dtype, const int *ids, const float *weig
 
 /*
  * The whole layer: q4_moe_route and q4_moe_experts (the same bits as the two
- * calls) in three launches for a few rows (M E <= 1024), four above.
+ * calls) in four launches for a few rows (M E E <= 16384), five above.
  * Arguments as theirs, with K = H; workspace of at least
  * q4_moe_layer_workspace_bytes(M, E, H, I, topk) bytes.
  */
