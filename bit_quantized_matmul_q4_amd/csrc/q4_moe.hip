@@ -14,11 +14,14 @@
 // Operands.  The matrix cores take the codes as exact binary16 q - 8
 // (Dequant<false>).  bfloat16 x becomes binary16 after a power of two for
 // each row that puts its largest value in [2^14, 2^15): exact for every value
-// down to 2^-31 of the largest, and off by at most 2^-40 of the largest below
-// that, which a 32-bit sum beside the largest cannot hold either.  h is kept as
-// two binary16 numbers (the value and what its rounding left) after a power
-// of two for each 32 values, 22 bits or more of each block's largest.  All
-// sums are binary32.
+// down to 2^-31 of the largest.  A row is wide where that is not enough for a
+// block of 32 whose largest value is below 2^-8 of the row's: then each block
+// gets a further power of two that puts its own largest there.  So a value is
+// exact down to 2^-23 of its block's largest and off by at most 2^-31 of it
+// below (or 2^-164 of the row's, in blocks below 2^-125 of that), whatever the
+// weights of the row's largest values are.  h is kept as two binary16 numbers
+// (the value and what its rounding left) after a power of two for each 32
+// values, 22 bits or more of each block's largest.  All sums are binary32.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -129,23 +132,91 @@ __device__ __forceinline__ float largest(u32x4 v, float top)
     return top;
 }
 
-// One row of bfloat16 x by one wave: x16 and its lift.
-__device__ __forceinline__ void lift_row(const uint16_t *x, uint16_t *x16, int *lift, int K)
+// The smallest magnitude of eight bfloat16 values that is not zero, less one
+// (in both halves, as bits), with `low`.
+typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
+__device__ __forceinline__ u16x2 smallest(u32x4 v, u16x2 low)
+{
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        low = __builtin_elementwise_min(low, __builtin_bit_cast(u16x2, v[i] & 0x7FFF7FFFu) - (u16x2)(1));
+    return low;
+}
+// Whether one of them, times 2^lift, may lie below 2^-17, from where on a
+// bfloat16 number's eight bits do not fit a binary16's steps of 2^-24.
+__device__ __forceinline__ bool below(u16x2 low, int lift)
+{
+    const uint32_t least = __builtin_bit_cast(uint32_t, __builtin_ldexpf(1.f, -17 - lift)) >> 16;
+    return low.x + 1u < least || low.y + 1u < least;
+}
+
+// bfloat16 x as binary16: the rows' powers of two, which rows are wide, and
+// the wide rows' further powers of two of their blocks (negative: as the
+// products take them back).
+struct Lifted {
+    uint16_t *x16;
+    int *lift, *wide;
+    int8_t *shift;  // [row][quads_of(K)][4]
+};
+
+__host__ __device__ inline int quads_of(int K) { return (K / 32 + 3) / 4; }
+
+constexpr int kSpread = 8;  // (see Operands above)
+
+// Whether a row needs its blocks' own powers of two, and those: by one wave,
+// four lanes a block (K % 32 = 0 keeps them together).  A further power of two
+// is at most 2^125: a block scale times 2^-125 is exact (a multiple of 2^-149).
+__device__ __forceinline__ bool lift_blocks(const uint16_t *x, uint16_t *x16, int8_t *shift, int up, int K)
+{
+    const int lane = threadIdx.x & 63;
+    auto more_of = [&](u32x4 b) {
+        float t = largest(b, 0.f);
+        t = __builtin_fmaxf(t, __shfl_xor(t, 1));
+        t = __builtin_fmaxf(t, __shfl_xor(t, 2));
+        return t > 0.f ? min(lift_of(t) - up, 125) : 0;
+    };
+    bool need = false;
+    for (int k = 8 * lane; k < K; k += 512) {
+        const u32x4 b = *(const u32x4 *)(x + k);
+        need |= more_of(b) > kSpread && below(smallest(b, (u16x2)(0xFFFF)), up);
+    }
+    if (!__any(need))
+        return false;
+    for (int k = 8 * lane; k < K; k += 512) {
+        const u32x4 b = *(const u32x4 *)(x + k);
+        const int more = more_of(b);
+        *(u32x4 *)(x16 + k) = lifted(b, up + more);
+        if ((lane & 3) == 0)
+            shift[k / 32] = (int8_t)-more;
+    }
+    return true;
+}
+
+// Row m of bfloat16 x by one wave.
+__device__ __forceinline__ void lift_row(const uint16_t *x_, const Lifted &to, size_t m, int K)
 {
     const int lane = threadIdx.x & 63;
     constexpr int HELD = 4;  // rows up to 2048 long are read once
+    const uint16_t *x = x_ + m * K;
+    uint16_t *x16 = to.x16 + m * K;
     u32x4 v[HELD];
     float top = 0.f;
+    u16x2 low = (u16x2)(0xFFFF);
 #pragma unroll
     for (int i = 0; i < HELD; ++i)
         if (8 * (lane + 64 * i) < K)
             v[i] = *(const u32x4 *)(x + 8 * (lane + 64 * i));
 #pragma unroll
     for (int i = 0; i < HELD; ++i)
-        if (8 * (lane + 64 * i) < K)
+        if (8 * (lane + 64 * i) < K) {
             top = largest(v[i], top);
-    for (int k = 8 * (lane + 64 * HELD); k < K; k += 512)
-        top = largest(*(const u32x4 *)(x + k), top);
+            low = smallest(v[i], low);
+        }
+    for (int k = 8 * (lane + 64 * HELD); k < K; k += 512) {
+        const u32x4 b = *(const u32x4 *)(x + k);
+        top = largest(b, top);
+        low = smallest(b, low);
+    }
 #pragma unroll
     for (int d = 1; d < 64; d *= 2)
         top = __builtin_fmaxf(top, __shfl_xor(top, d));
@@ -156,20 +227,22 @@ __device__ __forceinline__ void lift_row(const uint16_t *x, uint16_t *x16, int *
             *(u32x4 *)(x16 + 8 * (lane + 64 * i)) = lifted(v[i], up);
     for (int k = 8 * (lane + 64 * HELD); k < K; k += 512)
         *(u32x4 *)(x16 + k) = lifted(*(const u32x4 *)(x + k), up);
-    if (lane == 0)
-        *lift = up;
+    const bool wide = __any(below(low, up)) && lift_blocks(x, x16, to.shift + m * 4 * quads_of(K), up, K);
+    if (lane == 0) {
+        to.lift[m] = up;
+        to.wide[m] = wide;
+    }
 }
 
-__global__ __launch_bounds__(256) void q4_moe_lift_kernel(const uint16_t *__restrict__ x, uint16_t *__restrict__ x16,
-                                                          int *__restrict__ lift, int M, int K)
+__global__ __launch_bounds__(256) void q4_moe_lift_kernel(const uint16_t *__restrict__ x, Lifted to, int M, int K)
 {
     const int m = blockIdx.x * 4 + (threadIdx.x >> 6);
     if (m < M)
-        lift_row(x + (size_t)m * K, x16 + (size_t)m * K, lift + m, K);
+        lift_row(x, to, m, K);
 }
 
 // Few rows: grid = (16-expert tiles, 16-row tiles, parts), a wave a chain; the
-// reader adds the parts.  One more z takes the rows to binary16 (x16 given).
+// reader adds the parts.  One more z takes the rows to binary16 (to.x16 given).
 // One row of 64 experts over 2048: 3.3 us, launch and latency (a workgroup per
 // 16 experts over all of K, its waves on every 16th chunk, took 7).  201 rows of
 // 127 experts over 3584, binary32 router: 9 us, conversions to binary64 and
@@ -177,15 +250,15 @@ __global__ __launch_bounds__(256) void q4_moe_lift_kernel(const uint16_t *__rest
 template <int XK, int RK>
 __global__ __launch_bounds__(256) void q4_moe_logits_kernel(const uint16_t *__restrict__ x,
                                                             const void *__restrict__ router,
-                                                            double *__restrict__ parts, uint16_t *__restrict__ x16,
-                                                            int *__restrict__ lift, int M, int E, int K)
+                                                            double *__restrict__ parts, Lifted to, int M, int E,
+                                                            int K)
 {
     const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, c = lane & 15, g = lane >> 4;
     const int part = blockIdx.z;
     if (part * kPart >= K) {
         const int all = gridDim.x * gridDim.y * 4;
         for (int m = (blockIdx.y * gridDim.x + blockIdx.x) * 4 + wave; m < M; m += all)
-            lift_row(x + (size_t)m * K, x16 + (size_t)m * K, lift + m, K);
+            lift_row(x, to, m, K);
         return;
     }
     const int e = min((int)blockIdx.x * 16 + c, E - 1), m = min((int)blockIdx.y * 16 + c, M - 1);
@@ -338,17 +411,16 @@ __device__ __forceinline__ void choose_rows(const Choice &ch, int m0, int rows, 
     }
 }
 
-// A workgroup a row; with x16, the last wave takes the row to binary16 first.
+// A workgroup a row; with to.x16, the last wave takes the row to binary16 first.
 // 3.6 us at one row of 64 experts, 5.4 at 201 rows of 127: latency.
 __global__ __launch_bounds__(512) void q4_moe_select_kernel(Choice ch, int *__restrict__ ids,
                                                             float *__restrict__ weights,
-                                                            const uint16_t *__restrict__ x,
-                                                            uint16_t *__restrict__ x16, int *__restrict__ lift, int K)
+                                                            const uint16_t *__restrict__ x, Lifted to, int K)
 {
     extern __shared__ double row[];  // E keys, then topk chosen logits
     const size_t m = blockIdx.x;
-    if (x16 && threadIdx.x >= 448)
-        lift_row(x + m * K, x16 + m * K, lift + m, K);
+    if (to.x16 && threadIdx.x >= 448)
+        lift_row(x, to, m, K);
     choose_rows<int>(ch, (int)m, 1, (uint64_t *)row, row + ch.E, nullptr, ids, weights, true);
 }
 
@@ -512,19 +584,43 @@ __device__ __forceinline__ void issue_fence()
     __builtin_amdgcn_sched_barrier(0);
 }
 
-// The rows' operands of one quad: x as it is.
-template <int R>
+// x as the gate/up kernel takes it: binary16, with the rows' powers of two and
+// wide rows where it was bfloat16 (else null).
+struct UpIn {
+    const uint16_t *x;
+    const int *lift, *wide;
+    const int8_t *shift;
+    int M, H;
+};
+
+// The rows' operands of one quad; where WIDE, with the further powers of two of
+// the rows whose values the lane group accumulates (rows that are not wide:
+// none, and the same bits).  row(i): the batch row of row i of the group.
+template <int R, bool WIDE>
 struct RowsX {
     u32x4 x[R];
+    uint32_t shift[WIDE ? R : 1];
     struct In {
-        __amdgpu_buffer_rsrc_t x;
-        uint32_t at;
+        __amdgpu_buffer_rsrc_t x, shift;
+        uint32_t at, shift_at[WIDE ? R : 1];
         int nb;
     };
-    static __device__ __forceinline__ In in(const uint16_t *x, int rows_all, int K, int nb, int row, bool live)
+    template <typename ROW>
+    static __device__ __forceinline__ In in(const UpIn &u, ROW row, int rows, int nb)
     {
-        const uint32_t g = (threadIdx.x & 63) >> 4;
-        return In{buffer_of(x, (size_t)rows_all * K * 2), live ? (uint32_t)row * 2u * K + 16 * g : kNowhere, nb};
+        const int lane = threadIdx.x & 63, g = lane >> 4, i = Slots<R>::row(lane & 15);
+        In in;
+        in.x = buffer_of(u.x, (size_t)u.M * u.H * 2);
+        in.at = i < rows ? (uint32_t)row(i) * 2u * u.H + 16 * g : kNowhere;
+        if constexpr (WIDE) {
+            const int pitch = 4 * quads_of(u.H);
+            in.shift = buffer_of(u.shift, (size_t)u.M * pitch);
+#pragma unroll
+            for (int r = 0; r < R; ++r)
+                in.shift_at[r] = 4 * r + g < rows && u.wide[row(4 * r + g)] ? (uint32_t)row(4 * r + g) * pitch : kNowhere;
+        }
+        in.nb = nb;
+        return in;
     }
     __device__ __forceinline__ void load(const In &in, int q)
     {
@@ -534,9 +630,19 @@ struct RowsX {
             const int b = Slots<R>::block(o, c);
             x[o] = load16(in.x, 4 * q + b < in.nb ? in.at + 64 * b : kNowhere, 256 * q);
         }
+        if constexpr (WIDE)
+#pragma unroll
+            for (int r = 0; r < R; ++r)
+                shift[r] = __builtin_amdgcn_raw_buffer_load_b32(in.shift, in.shift_at[r], 4 * q, 0);
     }
     __device__ __forceinline__ f32x4 dot(int j, u32x4 b) const { return blockdot<false>(x[Slots<R>::operand(j)], b); }
-    __device__ __forceinline__ float scale(float d, int, int) const { return d; }
+    __device__ __forceinline__ float scale(float d, int r, int j) const
+    {
+        if constexpr (WIDE)
+            return __builtin_ldexpf(d, (int)(int8_t)(shift[r] >> (8 * j)));
+        else
+            return d;
+    }
 };
 
 // h as the gate/up kernel leaves it.
@@ -599,7 +705,8 @@ struct RowsH {
 // weights by the caller).  The run's part of the tree waits in the wave's own
 // LDS, stack [level][tile][r][lane] (levels that the trailing one-bits of a
 // segment's number name are merged, left operand first), and ends in level 0.
-template <int R, typename ROWS>
+// AHEAD false: one quad at a time, in fewer registers.
+template <int R, typename ROWS, bool AHEAD>
 __device__ __forceinline__ void multiply_run(const FourTiles &tiles, Weights &first, const typename ROWS::In &in, int sa,
                                              int L, const Plan &plan, float *stack)
 {
@@ -649,9 +756,19 @@ __device__ __forceinline__ void multiply_run(const FourTiles &tiles, Weights &fi
             end = ((sa + seg + 1) * plan.G) >> plan.log2S;
         }
     };
-    Weights second;
-    ROWS xa, xb;
+    ROWS xa;
     xa.load(in, qa);
+    if constexpr (!AHEAD) {
+        for (int q = qa; q < qb; ++q) {
+            multiply(first, xa, q);
+            first.load(tiles, q + 1, qb);
+            xa.load(in, q + 1);
+            issue_fence();
+        }
+        return;
+    }
+    Weights second;
+    ROWS xb;
     for (int q = qa; q < qb; q += 2) {
         second.load(tiles, q + 1, qb);
         xb.load(in, q + 1);
@@ -688,16 +805,26 @@ __device__ __forceinline__ float join_roots(const Roots &at, int tile, int i, in
 // gate and up: a unit is two tiles of gate and two of up, so that it ends with
 // 32 values of h, one block of the down product.
 struct Up {
-    const uint16_t *x;
-    const int *lift;  // or null: x as given
+    UpIn x;
     uint16_t *hi, *lo;
     int *shift;
-    int M, topk, H, I, shifts;
+    int topk, I, shifts;
 
     // waves of a compute unit's quarter that the registers are to hold
     static constexpr int waves(int RM) { return RM == 1 ? 4 : 3; }
-    template <int R>
-    using Rows = RowsX<R>;
+    template <int R, bool WIDE>
+    using Rows = RowsX<R, WIDE>;
+    static constexpr bool kWide = true;
+    // what a lane knows of the wide rows of the batch: loaded first, used after
+    // the weights are on their way
+    __device__ __forceinline__ int wide() const
+    {
+        int m = threadIdx.x & 63, any = x.wide && m < x.M ? x.wide[m] : 0;
+        if (x.wide && x.M > 64)
+            for (m += 64; m < x.M; m += 64)
+                any |= x.wide[m];
+        return any;
+    }
     __host__ __device__ int units() const { return I / 32; }
     __device__ __forceinline__ FourTiles tiles(const uint8_t *wq, const uint16_t *scales, int e, int unit, int G) const
     {
@@ -705,17 +832,15 @@ struct Up {
         return FourTiles{Tile(wq, scales, gate, G), Tile(wq, scales, gate + 1, G), Tile(wq, scales, up, G),
                          Tile(wq, scales, up + 1, G)};
     }
-    template <int R>
-    __device__ __forceinline__ typename RowsX<R>::In in(const uint16_t *list, int rows, int nb) const
+    template <int R, bool WIDE>
+    __device__ __forceinline__ typename RowsX<R, WIDE>::In in(const uint16_t *list, int rows, int nb) const
     {
-        const int row = Slots<R>::row(threadIdx.x & 15);
-        const bool live = row < rows;
-        return RowsX<R>::in(x, M, H, nb, live ? list[row] / topk : 0, live);
+        return RowsX<R, WIDE>::in(x, [&](int i) { return list[i] / topk; }, rows, nb);
     }
     // (loaded before the products, used after them)
     __device__ __forceinline__ int before(const uint16_t *list, int rows) const
     {
-        return lift && (int)threadIdx.x < rows ? -lift[list[threadIdx.x] / topk] : 0;
+        return x.lift && (int)threadIdx.x < rows ? -x.lift[list[threadIdx.x] / topk] : 0;
     }
     // 32 lanes a row: the trees, the activation, the block's power of two
     template <int R>
@@ -754,8 +879,10 @@ struct Down {
     int H;
 
     static constexpr int waves(int RM) { return RM == 1 ? 4 : RM == 2 ? 3 : 2; }
-    template <int R>
+    template <int R, bool>
     using Rows = RowsH<R>;
+    static constexpr bool kWide = false;
+    __device__ __forceinline__ int wide() const { return 0; }
     __host__ __device__ int units() const { return (H + 63) / 64; }
     // (past the last column: the last tile, its values are not stored)
     __device__ __forceinline__ FourTiles tiles(const uint8_t *wq, const uint16_t *scales, int e, int unit, int G) const
@@ -765,7 +892,7 @@ struct Down {
         return FourTiles{Tile(wq, scales, base + at, G), Tile(wq, scales, base + min(at + 1, last), G),
                          Tile(wq, scales, base + min(at + 2, last), G), Tile(wq, scales, base + min(at + 3, last), G)};
     }
-    template <int R>
+    template <int R, bool>
     __device__ __forceinline__ typename RowsH<R>::In in(const uint16_t *list, int rows, int nb) const
     {
         return RowsH<R>::in(h, list, rows, nb);
@@ -796,7 +923,11 @@ __host__ __device__ inline int tree_levels(int L)
 // tiles of one expert a workgroup, its waves on runs of L segments of K.  An
 // expert's rows go 4 RM at a time (the last ones 4, 8 or 16, by how many are
 // left), group r to the workgroup z = r mod Z; the weights of the next group's
-// first quad are on their way while this one's sums are joined.
+// first quad are on their way while this one's sums are joined.  With a wide
+// row in the batch the rows go 4 at a time, to the same bits: the powers of two
+// of 16 rows do not fit the registers, and where groups are of 4 anyway, a quad
+// ahead would take the fifth wave from batches without such a row (128 experts
+// 2048 x 768 at 8 rows: gate/up 23.6 us with four waves, 21.6 with five).
 // Few rows: bound by launch and memory latency (64 experts 2048 x 1024 at one
 // row: gate/up with its choice 9.9 us, down 6.7 us).  Many: by the weights'
 // stream and the dequantization's issue (47 VALU operations a tile and quad, half of
@@ -813,6 +944,7 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(OP::waves(R
     __shared__ int back[16];
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), waves = blockDim.x >> 6;
     const int levels = tree_levels(L);
+    const int wide_lane = op.wide();
     if (ch.parts) {
         uint64_t *keys = (uint64_t *)part;
         choose_rows<int16_t>(ch, 0, ch.M, keys, (double *)(keys + ch.M * ch.E), found.who, ids, weights,
@@ -826,15 +958,18 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(OP::waves(R
         tiles = op.tiles(wq, scales, e, blockIdx.x, plan.G);
         first.load(tiles, qa, qb);
     });
-    const int step = 4 * RM * gridDim.z;
-    for (int r0 = 4 * RM * blockIdx.z; r0 < count; r0 += step) {
-        const int left = min(count - r0, 4 * RM);
+    const bool wide = __any(wide_lane);
+    const int most = wide ? 4 : 4 * RM, step = most * gridDim.z;
+    for (int r0 = most * blockIdx.z; r0 < count; r0 += step) {
+        const int left = min(count - r0, most);
         const uint16_t *list = found.list + r0;
-        auto group = [&](auto r) {
+        auto group = [&](auto r, auto w) {
             constexpr int R = decltype(r)::value;
+            constexpr bool WIDE = decltype(w)::value;
             const int b = op.before(list, left);
-            multiply_run<R, typename OP::template Rows<R>>(tiles, first, op.template in<R>(list, left, plan.nb),
-                                                           wave * L, L, plan, part + wave * levels * 4 * R * 64);
+            multiply_run<R, typename OP::template Rows<R, WIDE>, !WIDE || RM != 1>(
+                tiles, first, op.template in<R, WIDE>(list, left, plan.nb), wave * L, L, plan,
+                part + wave * levels * 4 * R * 64);
             if ((int)threadIdx.x < 16)
                 back[threadIdx.x] = b;
             if (r0 + step < count)
@@ -844,12 +979,14 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(OP::waves(R
             if (r0 + step < count)
                 __syncthreads();  // the sums are read
         };
-        if (RM == 1 || left <= 4)
-            group(std::integral_constant<int, 1>());
+        if (OP::kWide && wide)
+            group(std::integral_constant<int, 1>(), std::integral_constant<bool, OP::kWide>());
+        else if (RM == 1 || left <= 4)
+            group(std::integral_constant<int, 1>(), std::false_type());
         else if (RM == 2 || left <= 8)
-            group(std::integral_constant<int, RM == 1 ? 1 : 2>());
+            group(std::integral_constant<int, RM == 1 ? 1 : 2>(), std::false_type());
         else
-            group(std::integral_constant<int, RM>());
+            group(std::integral_constant<int, RM>(), std::false_type());
     }
 }
 
@@ -910,8 +1047,8 @@ int logit_parts(int M, int E, int K)
 }
 
 template <int XK, int RK>
-void launch_logits_k(const uint16_t *x, const void *router, double *parts, uint16_t *x16, int *lift, int M, int E,
-                     int K, hipStream_t stream)
+void launch_logits_k(const uint16_t *x, const void *router, double *parts, const Lifted &to, int M, int E, int K,
+                     hipStream_t stream)
 {
     const int count = logit_parts(M, E, K);
     const unsigned et = (unsigned)((E + 15) / 16), mt = (unsigned)((M + 15) / 16);
@@ -919,38 +1056,39 @@ void launch_logits_k(const uint16_t *x, const void *router, double *parts, uint1
         hipLaunchKernelGGL((q4_moe_logits_rows_kernel<XK, RK>), dim3(et, (mt + 3) / 4), dim3(256), 0, stream, x, router,
                            parts, M, E, K);
     else
-        hipLaunchKernelGGL((q4_moe_logits_kernel<XK, RK>), dim3(et, mt, (unsigned)(count + (x16 ? 1 : 0))), dim3(256), 0,
-                           stream, x, router, parts, x16, lift, M, E, K);
+        hipLaunchKernelGGL((q4_moe_logits_kernel<XK, RK>), dim3(et, mt, (unsigned)(count + (to.x16 ? 1 : 0))), dim3(256),
+                           0, stream, x, router, parts, to, M, E, K);
 }
 
-hipError_t launch_logits(const void *x, int xk, const void *router, int rk, double *parts, uint16_t *x16, int *lift,
-                         int M, int E, int K, hipStream_t stream)
+hipError_t launch_logits(const void *x, int xk, const void *router, int rk, double *parts, const Lifted &to, int M,
+                         int E, int K, hipStream_t stream)
 {
     const uint16_t *xp = (const uint16_t *)x;
     if (xk == 1 && rk == 2)
-        launch_logits_k<1, 2>(xp, router, parts, x16, lift, M, E, K, stream);
+        launch_logits_k<1, 2>(xp, router, parts, to, M, E, K, stream);
     else if (xk == 1)
-        launch_logits_k<1, 1>(xp, router, parts, x16, lift, M, E, K, stream);
+        launch_logits_k<1, 1>(xp, router, parts, to, M, E, K, stream);
     else if (rk == 2)
-        launch_logits_k<0, 2>(xp, router, parts, x16, lift, M, E, K, stream);
+        launch_logits_k<0, 2>(xp, router, parts, to, M, E, K, stream);
     else
-        launch_logits_k<0, 0>(xp, router, parts, x16, lift, M, E, K, stream);
+        launch_logits_k<0, 0>(xp, router, parts, to, M, E, K, stream);
     return hipGetLastError();
 }
 
-hipError_t launch_select(const Choice &ch, int *ids, float *weights, const void *x, uint16_t *x16, int *lift, int K,
+hipError_t launch_select(const Choice &ch, int *ids, float *weights, const void *x, const Lifted &to, int K,
                          hipStream_t stream)
 {
     hipLaunchKernelGGL(q4_moe_select_kernel, dim3((unsigned)ch.M), dim3(512),
-                       (size_t)(ch.E + ch.topk) * sizeof(double), stream, ch, ids, weights, (const uint16_t *)x, x16,
-                       lift, K);
+                       (size_t)(ch.E + ch.topk) * sizeof(double), stream, ch, ids, weights, (const uint16_t *)x, to,
+                       K);
     return hipGetLastError();
 }
 
 // Where the parts of a workspace lie; sizes of a piece of rows.
 struct MoeRoom {
-    uint16_t *hi, *lo, *x16;
-    int *shift, *lift;
+    uint16_t *hi, *lo;
+    int *shift;
+    Lifted x;  // where x is bfloat16
     float *t;
     size_t bytes;
     MoeRoom(void *base, int rows, int topk, int H, int I)
@@ -966,13 +1104,21 @@ struct MoeRoom {
         hi = (uint16_t *)take(n * I * 2);
         lo = (uint16_t *)take(n * I * 2);
         shift = (int *)take(n * shifts_of(I) * 4);
-        x16 = (uint16_t *)take((size_t)rows * H * 2);
-        lift = (int *)take((size_t)rows * 4);
+        x.x16 = (uint16_t *)take((size_t)rows * H * 2);
+        x.lift = (int *)take((size_t)rows * 4);
+        x.wide = (int *)take((size_t)rows * 4);
+        x.shift = (int8_t *)take((size_t)rows * 4 * quads_of(H));
         t = (float *)take(n * H * 4);
         bytes = at;
     }
+    // What gate/up reads: binary16 x as given, or what lift_row leaves.
+    UpIn in(const void *given, bool bf16, int M, int H) const
+    {
+        return bf16 ? UpIn{x.x16, x.lift, x.wide, x.shift, M, H}
+                    : UpIn{(const uint16_t *)given, nullptr, nullptr, nullptr, M, H};
+    }
     // an expert row's powers of two, padded to whole quads
-    static int shifts_of(int I) { return (I / 32 + 3) / 4 * 4; }
+    static int shifts_of(int I) { return 4 * quads_of(I); }
 };
 
 // The largest group of rows a product is built for (4 RM): by the rows an
@@ -1030,12 +1176,11 @@ hipError_t launch_product(const Choice &ch, const OP &op, int *ids, float *weigh
 }
 
 // The products of a piece of rows; ch.parts: the gate/up kernel chooses.
-hipError_t products(const Choice &ch, const uint16_t *x, const int *lift, int *ids, float *weights, const uint8_t *w13,
-                    const uint16_t *s13, const uint8_t *w2, const uint16_t *s2, float *y, int H, int I,
-                    const MoeRoom &room, hipStream_t stream)
+hipError_t products(const Choice &ch, const UpIn &x, int *ids, float *weights, const uint8_t *w13, const uint16_t *s13,
+                    const uint8_t *w2, const uint16_t *s2, float *y, int I, const MoeRoom &room, hipStream_t stream)
 {
-    const int n = ch.M * ch.topk, shifts = MoeRoom::shifts_of(I);
-    const Up up{x, lift, room.hi, room.lo, room.shift, ch.M, ch.topk, H, I, shifts};
+    const int n = ch.M * ch.topk, H = x.H, shifts = MoeRoom::shifts_of(I);
+    const Up up{x, room.hi, room.lo, room.shift, ch.topk, I, shifts};
     hipError_t e = launch_product(ch, up, ids, weights, w13, s13, make_plan(H), stream);
     if (e != hipSuccess)
         return e;
@@ -1062,11 +1207,11 @@ hipError_t launch_moe_route(const void *x, int x_kind, const void *router, int r
                             hipStream_t stream)
 {
     double *parts = (double *)workspace;
-    const hipError_t e = launch_logits(x, x_kind, router, r_kind, parts, nullptr, nullptr, M, E, K, stream);
+    const hipError_t e = launch_logits(x, x_kind, router, r_kind, parts, Lifted{}, M, E, K, stream);
     if (e != hipSuccess)
         return e;
     const Choice ch{parts, bias, logit_parts(M, E, K), M, E, topk, renormalize};
-    return launch_select(ch, ids, weights, nullptr, nullptr, nullptr, K, stream);
+    return launch_select(ch, ids, weights, nullptr, Lifted{}, K, stream);
 }
 
 size_t moe_workspace_bytes(int M, int H, int I, int topk)
@@ -1084,17 +1229,16 @@ hipError_t launch_moe_experts(const void *x, bool bf16, const int *ids, const fl
         const int now = std::min(rows, M - m);
         const uint16_t *xm = (const uint16_t *)x + (size_t)m * H;
         if (bf16) {
-            hipLaunchKernelGGL(q4_moe_lift_kernel, dim3((unsigned)((now + 3) / 4)), dim3(256), 0, stream, xm, room.x16,
-                               room.lift, now, H);
+            hipLaunchKernelGGL(q4_moe_lift_kernel, dim3((unsigned)((now + 3) / 4)), dim3(256), 0, stream, xm, room.x,
+                               now, H);
             const hipError_t e = hipGetLastError();
             if (e != hipSuccess)
                 return e;
         }
         const Choice ch{nullptr, nullptr, 0, now, E, topk, 0};
-        const hipError_t e = products(ch, bf16 ? room.x16 : xm, bf16 ? room.lift : nullptr,
-                                      const_cast<int *>(ids) + (size_t)m * topk,
+        const hipError_t e = products(ch, room.in(xm, bf16, now, H), const_cast<int *>(ids) + (size_t)m * topk,
                                       const_cast<float *>(weights) + (size_t)m * topk, w13, s13, w2, s2,
-                                      y + (size_t)m * H, H, I, room, stream);
+                                      y + (size_t)m * H, I, room, stream);
         if (e != hipSuccess)
             return e;
     }
@@ -1132,22 +1276,20 @@ hipError_t launch_moe_layer(const void *x, int x_kind, const void *router, int r
         return launch_moe_experts(x, bf16, ids, weights, w13, s13, w2, s2, y, M, topk, E, H, I, rest, stream);
     }
     const MoeRoom room(rest, M, topk, H, I);
-    const uint16_t *xp = bf16 ? room.x16 : (const uint16_t *)x;
-    const int *lift = bf16 ? room.lift : nullptr;
+    const UpIn in = room.in(x, bf16, M, H);
     // x goes to binary16 beside the logits' parts, or beside the choice
     const bool by_rows = count == 1 && H > kPart;
     const bool fused = (long long)M * E * E <= kFused && !by_rows;
-    hipError_t e = launch_logits(x, x_kind, router, r_kind, parts, bf16 && !by_rows ? room.x16 : nullptr, room.lift, M,
-                                 E, H, stream);
+    hipError_t e = launch_logits(x, x_kind, router, r_kind, parts, bf16 && !by_rows ? room.x : Lifted{}, M, E, H, stream);
     if (e != hipSuccess)
         return e;
     if (fused)
-        return products(ch, xp, lift, ids, weights, w13, s13, w2, s2, y, H, I, room, stream);
-    e = launch_select(ch, ids, weights, x, bf16 && by_rows ? room.x16 : nullptr, room.lift, H, stream);
+        return products(ch, in, ids, weights, w13, s13, w2, s2, y, I, room, stream);
+    e = launch_select(ch, ids, weights, x, bf16 && by_rows ? room.x : Lifted{}, H, stream);
     if (e != hipSuccess)
         return e;
     const Choice given{nullptr, nullptr, 0, M, E, topk, 0};
-    return products(given, xp, lift, ids, weights, w13, s13, w2, s2, y, H, I, room, stream);
+    return products(given, in, ids, weights, w13, s13, w2, s2, y, I, room, stream);
 }
 
 }  // namespace q4

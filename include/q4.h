@@ -318,7 +318,10 @@ int q4_moe_route(const void *x, int x_dtype, const void *router, int router_dtyp
  *     [g | u] = x[m] . dequant(W13[e])^T     for e = ids[m][j]
  *     h       = g / (1 + exp(-g)) u
  *     y[m]    = sum_j weights[m][j] (h . dequant(W2[e])^T), in the order of j
- * with binary32 sums throughout; h keeps 22 bits or more of the largest of
+ * with binary32 sums throughout.  bfloat16 x is held as binary16 times powers
+ * of two, exact down to 2^-23 of the largest of its block of 32 values and
+ * off by at most 2^-31 of that below it (in blocks below 2^-125 of the row's
+ * largest value: 2^-164 of that); h keeps 22 bits or more of the largest of
  * each 32 values.  An id outside 0 .. E - 1 (-1, or an expert that another
  * device holds) adds nothing; a row without experts gets zeros; an expert may
  * appear twice in a row.

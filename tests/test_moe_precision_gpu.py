@@ -1,0 +1,138 @@
+"""Where the expert layer's operands are held in fewer bits than binary32,
+against plain 64-bit computations and the bounds of test_moe_gpu.py.
+
+bfloat16 x is held as binary16 times powers of two: exact down to 2^-23 of the
+largest of its block of 32, and off by at most 2^-31 of it below that, so such a
+value moves a gate or up sum by at most |w| 2^-31 of its block's largest."""
+import pytest
+import torch
+
+import bit_quantized_matmul_q4_amd as q4
+from tests import gpu_util as gu
+from tests.test_moe_gpu import U, blocks_of, gen
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def gpu():
+    gu.require_gpu()
+
+
+class Codes:
+    """Experts from given codes and scales: dense values in 64 bits, packed on demand."""
+
+    def __init__(self, E, H, I, seed):
+        g = gen(seed)
+        self.E, self.H, self.I = E, H, I
+        self.c13 = torch.randint(0, 16, (E * 2 * I, H), generator=g, dtype=torch.uint8)
+        self.c2 = torch.randint(0, 16, (E * H, I), generator=g, dtype=torch.uint8)
+        self.s13 = ((torch.rand(E * 2 * I, H // 32, generator=g) + 0.5) / (4.6 * H**0.5)).half()
+        self.s2 = ((torch.rand(E * H, I // 32, generator=g) + 0.5) / (4.6 * I**0.5)).half()
+
+    def done(self):
+        E, H, I = self.E, self.H, self.I
+        self.w13, self.w2 = q4.pack(self.c13.cuda(), self.s13.cuda()), q4.pack(self.c2.cuda(), self.s2.cuda())
+        self.d13 = ((self.c13.double() - 8) * self.s13.double().repeat_interleave(32, 1)).view(E, 2 * I, H)
+        self.d2 = ((self.c2.double() - 8) * self.s2.double().repeat_interleave(32, 1)).view(E, H, I)
+        return self
+
+
+def check(layer, x, e, what):
+    """One expert a row, weight 1, with the bounds of test_moe_gpu.py and x's own."""
+    M, I = x.shape[0], layer.I
+    ids = torch.full((M, 1), e, dtype=torch.int32).cuda()
+    y = q4.moe_experts(x.cuda(), ids, torch.ones(M, 1).cuda(), layer.w13, layer.w2)
+    torch.cuda.synchronize()
+    xd = x.double()
+    held = torch.zeros_like(xd)
+    if x.dtype == torch.bfloat16:
+        top = xd.abs().view(M, -1, 32).amax(2).repeat_interleave(32, 1)
+        held = torch.where(xd.abs() < 2.0**-23 * top, 2.0**-31 * top, held)
+    w13, w2 = layer.d13[e], layer.d2[e]
+    gu_ = xd @ w13.T
+    d = (blocks_of(layer.H) * U) * (xd.abs() @ w13.abs().T) + held @ w13.abs().T
+    g, u, dg, du = gu_[:, :I], gu_[:, I:], d[:, :I], d[:, I:]
+    act = g * torch.sigmoid(g)
+    h = act * u
+    # silu's slope is at most 1.1, and at -10 and below at most (1 - g) exp(g)
+    slope = torch.where(g + dg < -10, (1 - g + dg) * torch.exp(g + dg), torch.full_like(g, 1.1))
+    dh = slope * dg * (u.abs() + du) + act.abs() * du + 8 * U * h.abs()
+    dh = dh + 2.0**-22 * h.abs().view(M, -1, 32).amax(2).repeat_interleave(32, 1)
+    ref = h @ w2.T
+    tol = (dh @ w2.abs().T) * (1 + 1e-4) + (blocks_of(I) * U) * (h.abs() @ w2.abs().T) + 2 * U * ref.abs()
+    tol = tol * (1 + 1e-3) + 2.0**-148 * I  # (a product below the smallest normal number: half its step each)
+    off = (y.cpu().double() - ref).abs()
+    assert torch.isfinite(ref).all()
+    assert (off <= tol).all(), "%s: off by %.3g times the bound, %.3g of the largest output, rows %s" % (
+        what, float((off / tol).max()), float(off.max() / ref.abs().max()),
+        torch.nonzero((off > tol).any(1)).flatten().tolist()[:8])
+
+
+OUTLIERS = [10, 20, 31, 33, 38, 45, 60, 90, 120]
+
+
+@pytest.mark.parametrize("how", ["code 8", "zero scale"])
+@pytest.mark.parametrize("M", [1, 7, 9])
+@pytest.mark.parametrize("H", [64, 288, 2080])
+def test_outlier_without_weight(H, M, how):
+    """A value far above the others of its row whose weight is zero: the sums are the other values'."""
+    layer = Codes(2, H, 64, H)
+    at = 37
+    if how == "code 8":
+        layer.c13[:, at] = 8
+    else:
+        layer.s13[:, at // 32] = 0
+    layer.done()
+    for up in OUTLIERS:
+        gu.note("moe_experts H=%d M=%d outlier 2^%d, %s" % (H, M, up, how))
+        x = torch.randn(M, H, generator=gen(up))
+        x[:, at] = 2.0**up
+        check(layer, x.bfloat16(), 1, "2^%d" % up)
+
+
+@pytest.mark.parametrize("M", [1, 6, 16, 20])
+def test_blocks_of_very_different_size(M):
+    """Blocks of 32 values from 2^-60 to 2^60 in one row, the largest ones without weight."""
+    gu.note("moe_experts blocks M=%d" % M)
+    H = 1056
+    layer = Codes(2, H, 96, M)
+    size = torch.randint(-60, 61, (H // 32,), generator=gen(M)).float()
+    layer.s13[:, size > 0] = 0
+    layer.done()
+    x = torch.randn(M, H, generator=gen(M + 1)) * (2.0**size).repeat_interleave(32)
+    check(layer, x.bfloat16(), 0, "blocks")
+
+
+@pytest.mark.parametrize("M,E,topk", [(5, 3, 2), (40, 2, 1), (64, 2, 2), (70, 40, 3)])
+def test_wide_rows_do_not_change_the_others(M, E, topk):
+    """Rows keep their bits beside rows that need powers of two for their blocks, in calls of the parts and the layer."""
+    H, I = 416, 96
+    layer = Codes(E, H, I, M)
+    layer.s13[:, 3] = 0
+    layer.done()
+    g = gen(M)
+    x = torch.randn(M, H, generator=g)
+    r = (torch.randn(E, H, generator=g) / H**0.5).bfloat16().cuda()
+    r[:, 96:128] = 0
+    good = x.bfloat16().cuda()
+    wide = x.clone()
+    wide[::7, 100] = 2.0**50
+    wide = wide.bfloat16().cuda()
+    rest = [m for m in range(M) if m % 7]
+    gu.note("moe wide rows M=%d E=%d" % (M, E))
+    ids, w = q4.moe_route(good, r, topk)
+    a = q4.moe_experts(good, ids, w, layer.w13, layer.w2)
+    b = q4.moe_experts(wide, ids, w, layer.w13, layer.w2)
+    c = q4.moe(good, r, layer.w13, layer.w2, topk)
+    d = q4.moe(wide, r, layer.w13, layer.w2, topk)
+    torch.cuda.synchronize()
+    assert torch.equal(a[rest].view(torch.int32), b[rest].view(torch.int32))
+    assert torch.equal(a.view(torch.int32), c.view(torch.int32)) and torch.equal(b.view(torch.int32), d.view(torch.int32))
+    for m in range(0, M, 7):  # alone
+        one = q4.moe(wide[m:m + 1].contiguous(), r, layer.w13, layer.w2, topk)
+        torch.cuda.synchronize()
+        assert torch.equal(one.view(torch.int32), b[m:m + 1].view(torch.int32)), m
+    # the outlier meets no weight, so the outputs are those without it, but for 2^-31 of a block's largest a value:
+    # a sum of 416 of them moves by about 2^-26 of its size
+    assert ((b - a).abs() <= 2.0**-18 * a.abs().amax()).all()
