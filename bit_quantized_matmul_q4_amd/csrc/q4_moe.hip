@@ -856,7 +856,9 @@ struct Up {
 #pragma unroll
             for (int d = 1; d < 32; d *= 2)
                 top = __builtin_fmaxf(top, __shfl_xor(top, d));
-            const int raise = lift_of(top);
+            // (at most 2^125: a block scale times 2^-125 in the down product is exact, a
+            // multiple of 2^-149, and h 2^125 one of 2^-24, as binary16 holds it)
+            const int raise = min(lift_of(top), 125);
             const float v = __builtin_ldexpf(h, raise);
             const _Float16 vh = (_Float16)v;
             const float rest = v - (float)vh;

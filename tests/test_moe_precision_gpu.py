@@ -3,7 +3,9 @@ against plain 64-bit computations and the bounds of test_moe_gpu.py.
 
 bfloat16 x is held as binary16 times powers of two: exact down to 2^-23 of the
 largest of its block of 32, and off by at most 2^-31 of it below that, so such a
-value moves a gate or up sum by at most |w| 2^-31 of its block's largest."""
+value moves a gate or up sum by at most |w| 2^-31 of its block's largest.  h
+keeps 22 bits of the largest of its block of 32 down to the smallest normal
+binary32 number."""
 import pytest
 import torch
 
@@ -136,3 +138,20 @@ def test_wide_rows_do_not_change_the_others(M, E, topk):
     # the outlier meets no weight, so the outputs are those without it, but for 2^-31 of a block's largest a value:
     # a sum of 416 of them moves by about 2^-26 of its size
     assert ((b - a).abs() <= 2.0**-18 * a.abs().amax()).all()
+@pytest.mark.parametrize("M", [1, 5, 12])
+@pytest.mark.parametrize("xt", [torch.bfloat16, torch.float16])
+def test_small_h(M, xt):
+    """h down to the smallest normal numbers: outputs that are normal keep their bits."""
+    layer = Codes(1, 96, 64, M)
+    layer.s2[:] = ((torch.rand(96, 2, generator=gen(M + 7)) + 0.5) / 64).half()
+    layer.s2[::3] *= 2.0**-6
+    layer.s2[1::3] *= 2.0**10
+    if xt == torch.float16:  # gate and up by the scales, down to 2^-24 each, and x to 2^-14: about 2^-70 at the least
+        layer.s13[:] = 2.0**-22
+    layer.done()
+    for low in ((-10, -40, -52, -55, -57, -58, -60) if xt == torch.bfloat16 else (0, -7, -14)):
+        gu.note("moe_experts small h M=%d 2^%d" % (M, low))
+        x = torch.randn(M, 96, generator=gen(M)).sign() * 2.0**low
+        check(layer, x.to(xt), 0, "x of 2^%d" % low)
+
+
