@@ -851,7 +851,15 @@ struct Up {
             const int i = o >> 5, col = o & 31;
             const float gate = __builtin_ldexpf(join_roots<R>(roots, col >> 4, i, col & 15), back[i]);
             const float up = __builtin_ldexpf(join_roots<R>(roots, 2 + (col >> 4), i, col & 15), back[i]);
-            const float h = gate / (1.f + __builtin_expf(-gate)) * up;
+            // exp(-gate) passes the largest number from -88.8 down; there h is gate exp(gate) up within
+            // 2^-115 of it, by halves of the exponential, so that no factor underflows before h does
+            float h;
+            if (gate < -80.f) {
+                const float e = __builtin_expf(0.5f * gate);
+                h = (gate * e) * (up * e);
+            } else {
+                h = gate / (1.f + __builtin_expf(-gate)) * up;
+            }
             float top = __builtin_fabsf(h) < __builtin_inff() ? __builtin_fabsf(h) : 0.f;
 #pragma unroll
             for (int d = 1; d < 32; d *= 2)

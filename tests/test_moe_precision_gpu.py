@@ -155,3 +155,21 @@ def test_small_h(M, xt):
         check(layer, x.to(xt), 0, "x of 2^%d" % low)
 
 
+@pytest.mark.parametrize("xt", [torch.bfloat16, torch.float16])
+def test_far_negative_gate(xt):
+    """silu where exp(-gate) passes the largest binary32 number: gate exp(gate), still normal at -89, times a large up."""
+    H, I = 64, 64
+    layer = Codes(1, H, I, 5)
+    layer.c13[:I, :32], layer.c13[:I, 32:] = 9, 8  # gate: the sum of the first 32 values
+    layer.c13[I:, :32], layer.c13[I:, 32:] = 8, 9  # up: of the others
+    layer.s13[:] = 1
+    layer.done()
+    gates = torch.tensor([-60.0, -79, -81, -86, -88, -89, -90, -91, -95, -100, -103, -120, -1000])
+    for big in (1.0, 1000.0):
+        gu.note("moe_experts far negative gates, up %g" % big)
+        x = torch.full((len(gates), H), big)
+        x[:, :32] = 0
+        x[:, 3] = gates
+        check(layer, x.to(xt), 0, "gates")
+
+
