@@ -138,7 +138,7 @@ const char *q4_strerror(int status)
     case Q4_ERR_ALIGN: return "misaligned pointer (x, Wq, quantizer w and codes: 16 B; packed scales: 8 B; y: 4 B; workspace: 256 B)";
     case Q4_ERR_ENUM: return "unknown dtype or kernel selector";
     case Q4_ERR_HIP: return "HIP launch error (see q4_last_hip_error)";
-    case Q4_ERR_WORKSPACE: return "workspace_bytes > 0 with a NULL workspace";
+    case Q4_ERR_WORKSPACE: return "workspace too small or absent in a call that needs one, or workspace_bytes > 0 with a NULL workspace";
     case Q4_ERR_SCRATCH: return "the call needs more than the library's fixed scratch buffer (Q4_SCRATCH_BYTES)";
     default: return "unknown status";
     }
