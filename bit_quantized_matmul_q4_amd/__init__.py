@@ -71,9 +71,10 @@ def _need(t: torch.Tensor, name: str, dtypes, ndim: int, device=None):
 
 
 # The current device and a device's current stream, as a number, without the
-# objects around them (a decode step's calls are short).
-_get_device = torch._C._cuda_getDevice
-_raw_stream = torch._C._cuda_getCurrentRawStream
+# objects around them (a decode step's calls are short).  A torch without GPU
+# support has neither, and no GPU tensor that a call would accept.
+_get_device = getattr(torch._C, "_cuda_getDevice", None)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
 def _call(dev: torch.device, name: str, f, *args) -> None:

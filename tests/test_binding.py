@@ -23,3 +23,23 @@ def test_workspace_status_text(lib):
     """The status of a workspace that is absent, NULL with a size, or too small: its text holds for all three."""
     text = lib.q4_strerror(_lib.Q4_ERR_WORKSPACE).decode()
     assert "NULL" in text and "too small" in text and "needs" in text
+
+
+def run(code, **kw):
+    return subprocess.run([sys.executable, "-c", code], cwd=ROOT, stdout=subprocess.PIPE, stderr=subprocess.STDOUT,
+                          text=True, timeout=300, **kw)
+
+
+def test_import_without_torch_gpu_support(lib):
+    """A torch built without GPU support: the import and the host-side calls work."""
+    p = run("import torch\n"
+            "for name in ('_cuda_getDevice', '_cuda_getCurrentRawStream'):\n"
+            "    if hasattr(torch._C, name):\n"
+            "        delattr(torch._C, name)\n"
+            "import bit_quantized_matmul_q4_amd as q4\n"
+            "assert q4.packed_sizes(16, 32) == (1024, 128) and q4.segments(3584) == 16\n"
+            "try:\n"
+            "    q4.quantize_int8(torch.zeros(4, 64))\n"
+            "except ValueError as e:\n"
+            "    print('refused:', e)\n")
+    assert p.returncode == 0 and "refused: w must be a GPU tensor" in p.stdout, p.stdout
