@@ -130,22 +130,34 @@ def _declare(lib):
     return lib
 
 
+def _open(path: str):
+    """The library at path, declared; ImportError if it is not one this binding can use."""
+    lib = ctypes.CDLL(path)
+    if not hasattr(lib, "q4_abi_version"):
+        raise ImportError("%s has no q4_abi_version: not a libq4.so" % path)
+    lib.q4_abi_version.argtypes, lib.q4_abi_version.restype = [], ctypes.c_int
+    if lib.q4_abi_version() != ABI_VERSION:
+        raise ImportError("libq4.so ABI %d, binding expects %d" % (lib.q4_abi_version(), ABI_VERSION))
+    # an ABI version gains functions without a new number: an earlier build has fewer
+    missing = [f for f in EXPORTS if not hasattr(lib, f)]
+    if missing:
+        raise ImportError("%s is an earlier build without %s; run `python -m bit_quantized_matmul_q4_amd.build`"
+                          % (path, ", ".join(missing)))
+    return _declare(lib)
+
+
 def load(path: str | None = None):
     """Load libq4.so (default: the in-tree build).  Raises if it is missing."""
     global _lib
     if path is not None:
-        return _declare(ctypes.CDLL(path))
+        return _open(path)
     with _lock:
         if _lib is None:
             if not os.path.exists(LIB_PATH):
                 raise ImportError(
                     "libq4.so is not built (%s); run `python -m bit_quantized_matmul_q4_amd.build`"
                     % LIB_PATH)
-            lib = _declare(ctypes.CDLL(LIB_PATH))
-            if lib.q4_abi_version() != ABI_VERSION:
-                raise ImportError("libq4.so ABI %d, binding expects %d"
-                                  % (lib.q4_abi_version(), ABI_VERSION))
-            _lib = lib
+            _lib = _open(LIB_PATH)
     return _lib
 
 

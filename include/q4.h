@@ -58,6 +58,7 @@
 extern "C" {
 #endif
 
+/* Changes when a function or a layout changes; new functions leave it. */
 #define Q4_ABI_VERSION 6
 
 enum q4_status {

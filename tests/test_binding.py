@@ -43,3 +43,28 @@ def test_import_without_torch_gpu_support(lib):
             "except ValueError as e:\n"
             "    print('refused:', e)\n")
     assert p.returncode == 0 and "refused: w must be a GPU tensor" in p.stdout, p.stdout
+
+
+def stub(tmp_path, name, body):
+    cc = shutil.which("gcc") or shutil.which("cc")
+    if cc is None:
+        pytest.skip("no C compiler")
+    src, out = tmp_path / (name + ".c"), tmp_path / (name + ".so")
+    src.write_text(body)
+    subprocess.run([cc, "-shared", "-fPIC", str(src), "-o", str(out)], check=True)
+    return str(out)
+
+
+def test_other_builds_of_the_library_are_named(tmp_path, monkeypatch):
+    """A library without some of the functions, of another ABI version, or of another kind: an ImportError that says so."""
+    older = stub(tmp_path, "older", "int q4_abi_version(void) { return %d; } int q4_linear(void) { return 0; }"
+                 % _lib.ABI_VERSION)
+    other = stub(tmp_path, "other", "int q4_abi_version(void) { return %d; }" % (_lib.ABI_VERSION + 1))
+    alien = stub(tmp_path, "alien", "int f(void) { return 0; }")
+    for path, text in ((older, "q4_int8_linear"), (other, "ABI %d" % (_lib.ABI_VERSION + 1)), (alien, "q4_abi_version")):
+        with pytest.raises(ImportError, match=text):
+            _lib.load(path)
+        monkeypatch.setattr(_lib, "LIB_PATH", path)
+        monkeypatch.setattr(_lib, "_lib", None)
+        with pytest.raises(ImportError, match=text):
+            _lib.load()
