@@ -1,0 +1,65 @@
+// q4_int8_plan.hpp -- which kernel of the 8-bit product a shape takes (host),
+// and the size of its packed rows.  See q4_int8.hip for the kernels.
+#pragma once
+
+#include <hip/hip_runtime.h>
+
+namespace q4 {
+
+// k64 tiles of a packed row tile (K padded to 128)
+__host__ __device__ inline int int8_tiles(int K) { return 2 * ((K + 127) / 128); }
+
+constexpr int kUnits = 256;  // compute units
+
+// The tile and the split of K for a shape.
+struct Int8Shape {
+    bool decode, gemv;
+    int bm, bn, split;
+};
+
+inline Int8Shape int8_shape(bool dense, int M, int N, int K)
+{
+    // quantizing within the product saves a launch while that is less work than
+    // the launch's 2 us: 3584 x 3584 at 1 / 2 / 4 / 8 rows 5.1 / 5.7 / 6.6 / 7.6
+    // against 7.2 / 7.3 / 7.8 / 7.9 us, at 12 rows 10.4 against 7.9; 18944 x
+    // 3584 (more than two tiles a compute unit, each quantizing again) at one
+    // row 17.0 against 14.8
+    Int8Shape s{dense && M <= 4 && M * int8_tiles(K) * 64 <= 20 * 1024 && N <= 8192, M <= 64, 0, 0, 1};
+    if (s.decode || s.gemv)
+        return s;
+    // The largest tile that still fills the card, and K split while half the
+    // workgroups that fit at once are missing.  Measured (us, 256 x 256 / 128 x
+    // 128 / 128 x 64 / 64 x 64, the others' splits as here): 4096 x 3584 x 18944
+    // (224 tiles of 256) 292 / 452 / - / -; 2048 x 3584 x 3584 (448 tiles of 128)
+    // - / 42.6 / 51.9 / 62.3; 333 x 18944 x 3584 (444) - / 38.3 / 43.5 / 48.3;
+    // 1024 x 3584 x 3584 (224) - / 33.3 / 28.1 / 34.8; 512 x 3584 x 3584 (112) -
+    // / 25.9 / 24.5 / 21.9; 124 x 3584 x 18944 (28) - / 34.1 / 33.0 / 30.5.
+    const auto count = [&](int bm, int bn) { return (long long)((M + bm - 1) / bm) * ((N + bn - 1) / bn); };
+    int at_once;
+    if (count(256, 256) >= 200) {
+        s.bm = s.bn = 256;
+        at_once = kUnits;
+    } else if (count(128, 128) >= 400) {
+        s.bm = s.bn = 128;
+        at_once = 2 * kUnits;
+    } else if (count(128, 128) >= 200) {
+        s.bm = 128;
+        s.bn = 64;
+        at_once = 2 * kUnits;
+    } else {
+        s.bm = s.bn = 64;
+        at_once = 3 * kUnits;
+    }
+    const long long wgs = count(s.bm, s.bn);
+    const int steps = int8_tiles(K) / 2;
+    while (2 * wgs * s.split <= at_once && steps / (2 * s.split) >= 4)
+        s.split *= 2;
+    return s;
+}
+
+// Rows a workgroup of the quantizer (16 were slower everywhere: 4096 x 3584 in
+// 23 us against 12 with four; one against four at 1024 rows 31.2 against 32.5 us
+// with the product, at 4096 rows 306 against 299).
+inline int quant_rows(int rows) { return rows >= 2048 ? 4 : 1; }
+
+}  // namespace q4

@@ -25,6 +25,7 @@
 #include <stdint.h>
 
 #include "q4_device.hpp"
+#include "q4_int8_plan.hpp"
 
 namespace {
 
@@ -305,6 +306,22 @@ int q4probe_fma0(const void *d, const void *s, void *out, int n, void *stream)
     hipLaunchKernelGGL(probe_fma0, dim3((n + 255) / 256), dim3(256), 0, (hipStream_t)stream,
                        (const float *)d, (const float *)s, (float *)out, n);
     return hipGetLastError() == hipSuccess ? 0 : -5;
+}
+
+// The form of the 8-bit product that a shape takes, for the tests that name
+// what they run (host only): {quantized within the product, one column tile a
+// workgroup, rows and columns of the tile, split of K, rows a workgroup of the
+// quantizer}.
+int q4probe_int8_form(int dense, int M, int N, int K, int *form)
+{
+    const q4::Int8Shape s = q4::int8_shape(dense != 0, M, N, K);
+    form[0] = s.decode;
+    form[1] = s.gemv;
+    form[2] = s.bm;
+    form[3] = s.bn;
+    form[4] = s.split;
+    form[5] = q4::quant_rows(M);
+    return 0;
 }
 
 }  // extern "C"
