@@ -7,8 +7,9 @@ from bit_quantized_matmul_q4_amd import build
 # split.  Odd N, short last steps of K, rows past the last tile, and more than
 # one band of four row tiles with every remainder (9, 11, 14, 17 and 13 of them).
 FORMS = {
-    "decode": [(3, 40, 64), (4, 31, 96)],
-    "gemv": [(3, 8200, 64), (33, 300, 9984)],
+    "decode": [(1, 40, 18944), (1, 33, 20480), (2, 40, 9984), (2, 31, 10240), (3, 17, 6752), (3, 40, 64),
+               (4, 100, 5120), (4, 31, 96), (4, 48, 4128)],
+    "gemv": [(1, 21, 20512), (3, 8200, 64), (5, 40, 18944), (33, 300, 9984), (64, 33, 20480)],
     "64x64": [(65, 12001, 96), (333, 4863, 896)],
     "64x64/s": [(124, 301, 18944), (70, 33, 20512)],
     "128x64": [(1030, 3101, 160), (1400, 2503, 96), (1793, 1666, 544)],

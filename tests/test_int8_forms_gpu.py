@@ -7,7 +7,7 @@ import torch
 import bit_quantized_matmul_q4_amd as q4
 from tests import gpu_util as gu
 from tests.int8_forms import FORMS, form_of
-from tests.test_int8_gpu import DTYPES, check_y, codes_of, gen, tricky_rows
+from tests.test_int8_gpu import DTYPES, check_y, codes_of, gen, tiles_of, tricky_rows
 
 pytestmark = pytest.mark.gpu
 
@@ -57,3 +57,19 @@ def test_rows_have_the_bits_of_the_smaller_forms(form, shape):
             part = q4.linear_int8(x[at:at + rows].contiguous(), w)
             torch.cuda.synchronize()
             assert torch.equal(part.view(torch.int32), whole[at:at + rows].view(torch.int32)), (rows, at)
+
+
+@pytest.mark.parametrize("dtype", list(DTYPES))
+@pytest.mark.parametrize("R,K", [(2050, 8480), (2051, 4128), (3, 33024), (1, 131040)])
+def test_quantizers_reload_what_they_do_not_hold(R, K, dtype):
+    """Rows longer than the pieces that a lane keeps in registers, in both quantizers."""
+    gu.note("quantize_int8 %dx%d %s" % (R, K, dtype))
+    x = tricky_rows(gen(R + K), R, K, DTYPES[dtype])
+    q, s = codes_of(x)
+    codes, scales = q4.quantize_int8(x.cuda())
+    packed = q4.quantize_pack_int8(x.cuda())
+    torch.cuda.synchronize()
+    assert torch.equal(scales.cpu().view(torch.int32), s.view(torch.int32))
+    assert torch.equal(codes.cpu(), q.to(torch.int8))
+    assert torch.equal(packed.codes.cpu(), tiles_of(codes.cpu()))
+    assert torch.equal(packed.scales.cpu().view(torch.int32), s.view(torch.int32))
