@@ -30,6 +30,7 @@
 
 #include "q4_device.hpp"
 #include "q4_launch.hpp"
+#include "q4_moe_plan.hpp"
 
 namespace q4 {
 
@@ -70,8 +71,6 @@ struct Eight {
         }
     }
 };
-
-constexpr int kPart = 256;  // k of a part
 
 // The chain of the 64 k from k0 on (short at the end of the row): lane (g, c)
 // holds expert c's (A) and row c's (B) values k = 32 s + 8 g + i of step i.
@@ -491,13 +490,6 @@ __device__ __forceinline__ float quad_scale(u32x2 s, int j)
 }
 
 __device__ __forceinline__ f32x4 dot16(u32x4 a, u32x4 b, f32x4 c) { return blockdot_acc<false>(a, b, c); }
-
-// Up to kFused compares of two logits the gate/up kernel chooses the experts
-// itself, so that the layer is four launches instead of five: every workgroup
-// ranks all rows, and the first writes the choice for the down kernel.  One
-// row of 64 experts: 2.7 us more in gate/up against 3.7 us for the launch; 8
-// rows of 128 experts (131072 compares): gate/up 98 us against 22 + 6.
-constexpr int kFused = 16384;
 
 __device__ __forceinline__ int slot_expert(int id, int E) { return id >= 0 && id < E ? id : -1; }
 
@@ -1047,22 +1039,13 @@ size_t up256(size_t n) { return (n + 255) & ~(size_t)255; }
 // Rows one launch handles.
 int chunk_rows(int M, int topk) { return std::min(M, kSlots / topk); }
 
-// Parts of the logits in memory: all of K's for few rows, else one (the sum).
-// The part form fills the card from one row on; from about a tile a compute
-// unit on, the row form needs no room for parts.
-int logit_parts(int M, int E, int K)
-{
-    const long long tiles = (long long)((M + 15) / 16) * ((E + 15) / 16);
-    return tiles >= 1024 ? 1 : (K + kPart - 1) / kPart;
-}
-
 template <int XK, int RK>
 void launch_logits_k(const uint16_t *x, const void *router, double *parts, const Lifted &to, int M, int E, int K,
                      hipStream_t stream)
 {
     const int count = logit_parts(M, E, K);
     const unsigned et = (unsigned)((E + 15) / 16), mt = (unsigned)((M + 15) / 16);
-    if (count == 1 && K > kPart)
+    if (moe_by_rows(M, E, K))
         hipLaunchKernelGGL((q4_moe_logits_rows_kernel<XK, RK>), dim3(et, (mt + 3) / 4), dim3(256), 0, stream, x, router,
                            parts, M, E, K);
     else
@@ -1288,8 +1271,8 @@ hipError_t launch_moe_layer(const void *x, int x_kind, const void *router, int r
     const MoeRoom room(rest, M, topk, H, I);
     const UpIn in = room.in(x, bf16, M, H);
     // x goes to binary16 beside the logits' parts, or beside the choice
-    const bool by_rows = count == 1 && H > kPart;
-    const bool fused = (long long)M * E * E <= kFused && !by_rows;
+    const bool by_rows = moe_by_rows(M, E, H);
+    const bool fused = moe_fused(M, E, H);
     hipError_t e = launch_logits(x, x_kind, router, r_kind, parts, bf16 && !by_rows ? room.x : Lifted{}, M, E, H, stream);
     if (e != hipSuccess)
         return e;

@@ -26,6 +26,7 @@
 
 #include "q4_device.hpp"
 #include "q4_int8_plan.hpp"
+#include "q4_moe_plan.hpp"
 
 namespace {
 
@@ -321,6 +322,15 @@ int q4probe_int8_form(int dense, int M, int N, int K, int *form)
     form[3] = s.bn;
     form[4] = s.split;
     form[5] = q4::quant_rows(M);
+    return 0;
+}
+
+// The same for the expert layer: {experts chosen within gate/up, logits by
+// rows}.
+int q4probe_moe_form(int M, int E, int H, int *form)
+{
+    form[0] = q4::moe_fused(M, E, H);
+    form[1] = q4::moe_by_rows(M, E, H);
     return 0;
 }
 

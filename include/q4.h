@@ -344,7 +344,8 @@ int q4_moe_experts(const void *x, int x_dtype, const int *ids, const float *weig
 
 /*
  * The whole layer: q4_moe_route and q4_moe_experts (the same bits as the two
- * calls) in four launches for a few rows (M E E <= 16384), five above.
+ * calls) in four launches for a few rows (at most 32, M E <= 256, M E E <=
+ * 16384 and M E ceil(H / 256) <= 2048), five above.
  * Arguments as theirs, with K = H; workspace of at least
  * q4_moe_layer_workspace_bytes(M, E, H, I, topk) bytes.
  */
