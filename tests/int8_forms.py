@@ -9,8 +9,9 @@ from bit_quantized_matmul_q4_amd import build
 FORMS = {
     "decode": [(1, 40, 18944), (1, 33, 20480), (2, 40, 9984), (2, 31, 10240), (3, 17, 6752), (3, 40, 64),
                (4, 100, 5120), (4, 31, 96), (4, 48, 4128)],
-    "gemv": [(1, 21, 20512), (3, 8200, 64), (5, 40, 18944), (33, 300, 9984), (64, 33, 20480)],
-    "64x64": [(65, 12001, 96), (333, 4863, 896)],
+    "gemv": [(1, 21, 20512), (3, 8200, 64), (5, 40, 18944), (33, 300, 9984), (64, 33, 20480),
+             (16, 24577, 64), (64, 24576, 32)],
+    "64x64": [(65, 12001, 96), (333, 4863, 896), (17, 24577, 160), (48, 60001, 32), (64, 26000, 544)],
     "64x64/s": [(124, 301, 18944), (70, 33, 20512)],
     "128x64": [(1030, 3101, 160), (1400, 2503, 96), (1793, 1666, 544)],
     "128x64/s": [(25700, 60, 1056)],
