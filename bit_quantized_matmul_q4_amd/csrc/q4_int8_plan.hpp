@@ -44,10 +44,12 @@ inline Int8Shape int8_shape(bool dense, int M, int N, int K)
     // 1024 x 3584 x 3584 (224) - / 33.3 / 28.1 / 34.8; 512 x 3584 x 3584 (112) -
     // / 25.9 / 24.5 / 21.9; 124 x 3584 x 18944 (28) - / 34.1 / 33.0 / 30.5.  Tiles
     // taller than the rows multiply padding: 48 x 152064 x 3584 - / 127 / - / 127,
-    // 48 x 152064 x 896 - / 47.1 / - / 42.8, 48 x 32000 x 3584 - / - / 32.8 / 30.6.
+    // 48 x 152064 x 896 - / 47.1 / - / 42.8, 48 x 32000 x 3584 - / - / 32.8 / 30.6;
+    // 65 x 152064 x 3584 153 / 130 / - / 144, 128 x 152064 x 3584 166 / 152 / - / 179,
+    // 128 x 60000 x 896 25.2 / 21.0 / - / 24.2; but 129 x 152064 x 3584 161 / 171.
     const auto count = [&](int bm, int bn) { return (long long)((M + bm - 1) / bm) * ((N + bn - 1) / bn); };
     int at_once;
-    if (M > 64 && count(256, 256) >= 200) {
+    if (M > 128 && count(256, 256) >= 200) {
         s.bm = s.bn = 256;
         at_once = kUnits;
     } else if (M > 64 && count(128, 128) >= 400) {

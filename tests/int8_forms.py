@@ -15,8 +15,8 @@ FORMS = {
     "64x64/s": [(124, 301, 18944), (70, 33, 20512)],
     "128x64": [(1030, 3101, 160), (1400, 2503, 96), (1793, 1666, 544)],
     "128x64/s": [(25700, 60, 1056)],
-    "128x128": [(2050, 3333, 288), (1030, 6401, 608)],
-    "256x256": [(4100, 3301, 160), (3100, 4602, 416), (2600, 5121, 2080)],
+    "128x128": [(65, 51300, 96), (128, 60001, 160), (2050, 3333, 288), (1030, 6401, 608)],
+    "256x256": [(129, 51300, 64), (4100, 3301, 160), (3100, 4602, 416), (2600, 5121, 2080)],
 }
 
 
