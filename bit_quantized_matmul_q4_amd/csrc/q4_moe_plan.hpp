@@ -6,13 +6,16 @@ namespace q4 {
 
 constexpr int kPart = 256;  // k of a part
 
-// Parts of the logits in memory: all of K's for few rows, else one (the sum).
-// The part form fills the card from one row on; from about a tile a compute
-// unit on, the row form needs no room for parts.
+// Parts of the logits in memory: all of K's, or one (the sum) from 2048 tiles
+// of 16 experts by 16 rows on, where a wave a tile fills the card twice.  Router
+// in us, in parts / by rows: 4096 rows x 64 experts x 2048 (1024 tiles) 43.6 /
+// 50.6; 2048 x 128 x 3584 (1024) 60.7 / 72.9; 6000 x 64 x 3584 (1500) 88.8 / 109;
+// 8192 x 64 x 2048 (2048) 79.9 / 79.8; 4096 x 128 x 3584 (2048) 111 / 112; 2048 x
+// 512 x 1024 (4096) 168 / 164; 16384 x 128 x 2048 (8192) 278 / 250.
 inline int logit_parts(int M, int E, int K)
 {
     const long long tiles = (long long)((M + 15) / 16) * ((E + 15) / 16);
-    return tiles >= 1024 ? 1 : (K + kPart - 1) / kPart;
+    return tiles >= 2048 ? 1 : (K + kPart - 1) / kPart;
 }
 
 // Whether the form that keeps a row's whole sum in a wave takes the logits.

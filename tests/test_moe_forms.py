@@ -41,3 +41,11 @@ def test_gpu_shapes_take_their_form(form):
         assert form(M, E, H) == (False, False), (M, E, H)
     for M, E, H, I, topk in BY_ROWS:
         assert form(M, E, H) == (False, True), (M, E, H)
+
+
+def test_logits_where_they_were_measured_faster(form):
+    for M, E, H in ((4096, 64, 2048), (2048, 128, 3584), (6000, 64, 3584), (16384, 8, 3584)):
+        assert not form(M, E, H)[1], (M, E, H)
+    for M, E, H in ((16384, 128, 2048), (2048, 512, 1024), (65536, 8, 3584), (1030, 512, 320), (32760, 3, 288),
+                    (2049, 250, 832)):
+        assert form(M, E, H)[1], (M, E, H)
