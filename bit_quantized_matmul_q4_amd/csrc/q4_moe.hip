@@ -454,8 +454,9 @@ struct Slots<4> {
 
 // Buffer loads: a wave-uniform base with the range of what may be read, a
 // lane's own 32-bit offset and a uniform one, so that a stream costs one
-// register a lane.  An offset of kNowhere is past every range (they stay
-// below 2^29 bytes, the uniform offsets too): it reads zero.
+// register a lane.  A lane's offset of kNowhere is past every range (they stay
+// below 2^29 bytes): it reads zero.  The uniform offset itself stays within the
+// range, so that nothing hangs on how the check takes one past it.
 constexpr uint32_t kNowhere = 1u << 31;
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_of(const void *base, size_t bytes)
 {
@@ -558,6 +559,7 @@ struct Weights {
     {
         const uint32_t lane = threadIdx.x & 63;
         const uint32_t w_at = q < qb ? 16 * lane : kNowhere, s_at = q < qb ? 8 * (lane & 15) : kNowhere;
+        q = min(q, qb - 1);
         codes[0] = load_codes(f.t0.w, w_at, q);
         codes[1] = load_codes(f.t1.w, w_at, q);
         codes[2] = load_codes(f.t2.w, w_at, q);
@@ -595,7 +597,7 @@ struct RowsX {
     struct In {
         __amdgpu_buffer_rsrc_t x, shift;
         uint32_t at, shift_at[WIDE ? R : 1];
-        int nb;
+        int nb, last;
     };
     template <typename ROW>
     static __device__ __forceinline__ In in(const UpIn &u, ROW row, int rows, int nb)
@@ -612,20 +614,21 @@ struct RowsX {
                 in.shift_at[r] = 4 * r + g < rows && u.wide[row(4 * r + g)] ? (uint32_t)row(4 * r + g) * pitch : kNowhere;
         }
         in.nb = nb;
+        in.last = (nb - 1) / 4;
         return in;
     }
     __device__ __forceinline__ void load(const In &in, int q)
     {
-        const int c = threadIdx.x & 15;
+        const int c = threadIdx.x & 15, to = min(q, in.last);
 #pragma unroll
         for (int o = 0; o < R; ++o) {  // (blocks past the end of a short last quad: zero)
             const int b = Slots<R>::block(o, c);
-            x[o] = load16(in.x, 4 * q + b < in.nb ? in.at + 64 * b : kNowhere, 256 * q);
+            x[o] = load16(in.x, 4 * q + b < in.nb ? in.at + 64 * b : kNowhere, 256 * to);
         }
         if constexpr (WIDE)
 #pragma unroll
             for (int r = 0; r < R; ++r)
-                shift[r] = __builtin_amdgcn_raw_buffer_load_b32(in.shift, in.shift_at[r], 4 * q, 0);
+                shift[r] = __builtin_amdgcn_raw_buffer_load_b32(in.shift, in.shift_at[r], 4 * to, 0);
     }
     __device__ __forceinline__ f32x4 dot(int j, u32x4 b) const { return blockdot<false>(x[Slots<R>::operand(j)], b); }
     __device__ __forceinline__ float scale(float d, int r, int j) const
@@ -652,7 +655,7 @@ struct RowsH {
     struct In {
         __amdgpu_buffer_rsrc_t hi, lo, shift;
         uint32_t at, shift_at[R];
-        int nb;
+        int nb, last;
     };
     static __device__ __forceinline__ In in(const DownIn &h, const uint16_t *list, int rows, int nb)
     {
@@ -666,21 +669,22 @@ struct RowsH {
         for (int r = 0; r < R; ++r)
             i.shift_at[r] = 4 * r + g < rows ? (uint32_t)list[4 * r + g] * 4u * h.shifts : kNowhere;
         i.nb = nb;
+        i.last = (nb - 1) / 4;
         return i;
     }
     __device__ __forceinline__ void load(const In &in, int q)
     {
-        const int c = threadIdx.x & 15;
+        const int c = threadIdx.x & 15, to = min(q, in.last);
 #pragma unroll
         for (int o = 0; o < R; ++o) {  // (blocks past the end of a short last quad: zero)
             const int b = Slots<R>::block(o, c);
             const uint32_t at = 4 * q + b < in.nb ? in.at + 64 * b : kNowhere;
-            hi[o] = load16(in.hi, at, 256 * q);
-            lo[o] = load16(in.lo, at, 256 * q);
+            hi[o] = load16(in.hi, at, 256 * to);
+            lo[o] = load16(in.lo, at, 256 * to);
         }
 #pragma unroll
         for (int r = 0; r < R; ++r)
-            shift[r] = load16(in.shift, in.shift_at[r], 16 * q);
+            shift[r] = load16(in.shift, in.shift_at[r], 16 * to);
     }
     __device__ __forceinline__ f32x4 dot(int j, u32x4 b) const
     {
