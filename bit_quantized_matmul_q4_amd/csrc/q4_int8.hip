@@ -171,8 +171,9 @@ __device__ __forceinline__ u32x4 codes_of(const u32x4 (&v)[VECS], const RowScale
 // 32768 with one row a workgroup) and the rest from the L2.
 // PACKED: the packed layout (padding written), else codes [rows][K].
 // grid = row groups (PACKED: of the padded rows, so that padding rows are
-// written too).  Bound by memory latency for few rows (4 us at 124 x 3584), by
-// memory for many: 4096 x 3584 in 12 us, 3.7 TB/s.
+// written too).  Bound by memory latency for few rows (4 us at 8 x 3584, 8 at
+// 124 x 18944), by memory for many: 4096 x 3584 in 15 us, 2.9 TB/s, from rows
+// that no cache holds.
 constexpr int kQuantThreads = 512;
 
 template <int KIND, int RW, bool PACKED>
@@ -347,7 +348,9 @@ __device__ __forceinline__ f32x4 scaled4(i32x4 a, Scale sx, const Scale (&sw)[4]
 // --------------------------------------------------------------- few rows
 // Up to 16 RT rows of x: bound by the bytes of W.  A workgroup owns one tile
 // of 16 columns; its waves take the tile's k64 steps in turn, U at a time,
-// and their integer sums meet in LDS.  18944 x 3584 at 8 rows: 11.8 us, 5.8 TB/s.
+// and their integer sums meet in LDS.  18944 x 3584 at 8 rows: 14.7 to 15.4 us, 4.4
+// to 4.6 TB/s, with weights from memory (a plain read of 1 GiB: 6.3), 11.8 us with
+// weights that the last-level cache holds.
 template <int RT, int YK>
 __global__ __launch_bounds__(512) void q4_int8_gemv_kernel(const int8_t *__restrict__ xq, const float *__restrict__ sx,
                                                            const int8_t *__restrict__ wq, const float *__restrict__ sw,
@@ -410,8 +413,9 @@ __global__ __launch_bounds__(512) void q4_int8_gemv_kernel(const int8_t *__restr
 // A few dense rows in one launch: a workgroup quantizes all of them into LDS (M
 // K bytes) while its first weights are on their way, then multiplies its tile
 // of W.  A wave takes every eighth k64 step, in chunks of eight steps, one
-// chunk ahead of the products.  3584 x 3584 at one row: 5.1 us, of which the
-// launch and two memory latencies (x, then W) are most.
+// chunk ahead of the products.  3584 x 3584 at one row: 5.8 us (5.1 with W in the
+// last-level cache), of which the launch and two memory latencies (x, then W) are
+// most.
 constexpr uint32_t kNowhere = 1u << 31;  // past every tile's range: reads zero, no access
 constexpr int kDecodeWaves = 8, kDecodeChunk = 8;
 
@@ -557,11 +561,12 @@ __device__ __forceinline__ void wait_loads()
 // other: the barrier that frees a stage falls between the halves, when both
 // halves' operands of the step are in registers, so that neither the LDS reads
 // nor the loads of the next stages hold up the matrix cores.
-// 4096 x 18944 x 3584 (256 x 256): 285 us, 1.95 Pop/s.  The products alone, on
-// operands that stay in registers, take 208 us (the card's clock falls under
-// them), with the LDS reads 237, with the loads but no reads 270.  With the 32 x
-// 32 x 32 form of the instruction the whole takes 17 us more, with four waves
-// of 128 x 128 65 us more (copies between register files).
+// 4096 x 18944 x 3584 (256 x 256): 281 to 287 us, 1.94 to 1.98 Pop/s, in a captured
+// replay, 292 to 298 with a tracer beside it.  Taken apart in builds of their own, of then 285
+// us: the products alone, on operands that stay in registers, 208 us (the card's
+// clock falls under them), with the LDS reads 237, with the loads but no reads
+// 270.  With the 32 x 32 x 32 form of the instruction the whole took 17 us more,
+// with four waves of 128 x 128 65 us more (copies between register files).
 template <int BM, int BN, int WM, int WN, int NS, int YK>
 __global__ __launch_bounds__(64 * WM *WN) void q4_int8_gemm_kernel(
     const int8_t *__restrict__ xq, const float *__restrict__ sx, const int8_t *__restrict__ wq,

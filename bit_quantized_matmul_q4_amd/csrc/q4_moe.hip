@@ -411,7 +411,7 @@ __device__ __forceinline__ void choose_rows(const Choice &ch, int m0, int rows, 
 }
 
 // A workgroup a row; with to.x16, the last wave takes the row to binary16 first.
-// 3.6 us at one row of 64 experts, 5.4 at 201 rows of 127: latency.
+// 3.2 us at one row of 64 experts, 5.5 at 201 rows of 127: latency.
 __global__ __launch_bounds__(512) void q4_moe_select_kernel(Choice ch, int *__restrict__ ids,
                                                             float *__restrict__ weights,
                                                             const uint16_t *__restrict__ x, Lifted to, int K)
@@ -935,10 +935,10 @@ __host__ __device__ inline int tree_levels(int L)
 // ahead would take the fifth wave from batches without such a row (128 experts
 // 2048 x 768 at 8 rows: gate/up 23.6 us with four waves, 21.6 with five).
 // Few rows: bound by launch and memory latency (64 experts 2048 x 1024 at one
-// row: gate/up with its choice 9.9 us, down 6.7 us).  Many: by the weights'
+// row: gate/up with its choice 11.1 us, down 6.5 us).  Many: by the weights'
 // stream and the dequantization's issue (47 VALU operations a tile and quad, half of
 // the cycles) that overlap in part: 64 experts 3584 x 1792 at 64 rows, gate/up
-// 94 us (4.9 TB/s), down 68 us (3.4 TB/s); without the products the layer takes
+// 94 us (4.9 TB/s), down 69 us (3.4 TB/s); without the products the layer took
 // 152 of then 205 us.
 template <typename OP, int RM>
 __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(OP::waves(RM)))) void q4_moe_product_kernel(
@@ -1122,7 +1122,11 @@ struct MoeRoom {
 // expert gets on average.  A group takes a weight through its dequantization
 // once, a larger one costs registers: 64 experts 3584 x 1792 with 6 rows each
 // in groups of at most 8 / 16 188 / 168 us, 128 experts 2048 x 768 with 4 rows
-// each 96 / 98 us.
+// each 96 / 98 us.  An average knows nothing of skewed routing, and the launch
+// nothing of the routing at all: 64 rows with 8 of those 128 experts take 90 us
+// with uniform choices (12 rows an expert at most), 127 where expert i is chosen
+// in proportion to 1 / i (44 at most, 105 experts read), 160 where one expert is
+// in every row; 64 rows with 6 of 64 experts 3584 x 1792 166, 179 and 174.
 int row_group(int n, int E)
 {
     const int rows = n / std::min(n, E);
