@@ -320,8 +320,8 @@ int q4_moe_route(const void *x, int x_dtype, const void *router, int router_dtyp
  *     h       = g / (1 + exp(-g)) u
  *     y[m]    = sum_j weights[m][j] (h . dequant(W2[e])^T), in the order of j
  * with binary32 sums throughout.  bfloat16 x is held as binary16 times powers
- * of two, exact down to 2^-23 of the largest of its block of 32 values and
- * off by at most 2^-31 of that below it (in blocks below 2^-125 of the row's
+ * of two, exact down to 2^-19 of the largest of its block of 32 values and
+ * off by at most 2^-27 of that below it (in blocks below 2^-125 of the row's
  * largest value: 2^-164 of that); h keeps 22 bits or more of the largest of
  * each 32 values.  An id outside 0 .. E - 1 (-1, or an expert that another
  * device holds) adds nothing; a row without experts gets zeros; an expert may
