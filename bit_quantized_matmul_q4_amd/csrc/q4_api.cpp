@@ -134,8 +134,8 @@ const char *q4_strerror(int status)
     switch (status) {
     case Q4_OK: return "ok";
     case Q4_ERR_NULL: return "a required pointer is NULL";
-    case Q4_ERR_SHAPE: return "bad shape (need M >= 1, N >= 1, K >= 32, K % 32 == 0, sizes in range)";
-    case Q4_ERR_ALIGN: return "misaligned pointer (x, Wq, quantizer w and codes: 16 B; packed scales: 8 B; y: 4 B; workspace: 256 B)";
+    case Q4_ERR_SHAPE: return "bad shape (need M >= 1, N >= 1, K >= 32, K % 32 == 0, 1 <= topk <= experts, sizes in range)";
+    case Q4_ERR_ALIGN: return "misaligned pointer (x, Wq, router, quantizer w and codes: 16 B; packed scales: 8 B; y, float32 scales, bias, ids, weights: 4 B; 16-bit y: 2 B; workspace: 256 B)";
     case Q4_ERR_ENUM: return "unknown dtype or kernel selector";
     case Q4_ERR_HIP: return "HIP launch error (see q4_last_hip_error)";
     case Q4_ERR_WORKSPACE: return "workspace too small or absent in a call that needs one, or workspace_bytes > 0 with a NULL workspace";

@@ -64,7 +64,8 @@ extern "C" {
 enum q4_status {
     Q4_OK = 0,
     Q4_ERR_NULL = -1,      /* a required pointer is NULL */
-    Q4_ERR_SHAPE = -2,     /* M < 1, N < 1, K < 32, K % 32 != 0, K > 2^25, or a size overflows */
+    Q4_ERR_SHAPE = -2,     /* M < 1, N < 1, K < 32, K % 32 != 0, K > 2^25, topk not in 1 .. experts, or a size
+                              past what its call states or overflowing */
     Q4_ERR_ALIGN = -3,     /* a pointer below the alignment its call states */
     Q4_ERR_ENUM = -4,      /* unknown dtype or kernel selector */
     Q4_ERR_HIP = -5,       /* a HIP call failed (see q4_last_hip_error) */

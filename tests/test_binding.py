@@ -68,3 +68,10 @@ def test_other_builds_of_the_library_are_named(tmp_path, monkeypatch):
         monkeypatch.setattr(_lib, "_lib", None)
         with pytest.raises(ImportError, match=text):
             _lib.load()
+
+
+def test_status_texts_hold_for_every_call(lib):
+    """Shapes and alignments that only the 8-bit product or the expert layer check are in the texts."""
+    shape, align = (lib.q4_strerror(s).decode() for s in (_lib.Q4_ERR_SHAPE, _lib.Q4_ERR_ALIGN))
+    assert "topk" in shape and "experts" in shape
+    assert "router" in align and "ids" in align and "16-bit y" in align
