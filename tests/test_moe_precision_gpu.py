@@ -10,6 +10,7 @@ import pytest
 import torch
 
 import bit_quantized_matmul_q4_amd as q4
+from bit_quantized_matmul_q4_amd import _lib
 from tests import gpu_util as gu
 from tests.test_moe_gpu import U, blocks_of, gen
 
@@ -173,3 +174,37 @@ def test_far_negative_gate(xt):
         check(layer, x.to(xt), 0, "gates")
 
 
+
+
+@pytest.mark.parametrize("M", [1, 6, 70])
+def test_wide_rows_in_a_replayed_graph(M):
+    """One captured layer over inputs with and without wide rows, in a workspace that starts as NaN, eager work between."""
+    H, I, E, topk = 288, 64, 6, 3
+    layer = Codes(E, H, I, M).done()
+    g = gen(M)
+    r = (torch.randn(E, H, generator=g) / H**0.5).bfloat16().cuda()
+    x = torch.randn(M, H, generator=g).bfloat16().cuda()
+    need = int(_lib.load().q4_moe_layer_workspace_bytes(M, E, H, I, topk))
+    ws = torch.full((need,), 255, dtype=torch.uint8, device="cuda")
+    out = torch.empty(M, H, device="cuda")
+    gu.note("moe wide rows in a graph M=%d" % M)
+    q4.moe(x, r, layer.w13, layer.w2, topk, out=out, workspace=ws)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        q4.moe(x, r, layer.w13, layer.w2, topk, out=out, workspace=ws)
+    for i in range(6):
+        new = torch.randn(M, H, generator=g)
+        if i % 2:
+            new[:: 1 + i % 3, 40 + i] = 2.0**(36 + i)
+        x.copy_(new.bfloat16())
+        eager = q4.moe(x, r, layer.w13, layer.w2, topk)
+        torch.cuda.synchronize()
+        ws.fill_(255)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert same(out, eager), i
+
+
+def same(a, b):
+    return torch.equal(a.view(torch.int32), b.view(torch.int32))
