@@ -150,8 +150,8 @@ __device__ __forceinline__ bool below(u16x2 low, int lift)
 }
 
 // bfloat16 x as binary16: the rows' powers of two, which rows are wide, and
-// the wide rows' further powers of two of their blocks (negative: as the
-// products take them back).
+// the further powers of two of their blocks (negative: as the products take them
+// back; 0 in rows that are not wide).
 struct Lifted {
     uint16_t *x16;
     int *lift, *wide;
@@ -229,6 +229,9 @@ __device__ __forceinline__ void lift_row(const uint16_t *x_, const Lifted &to, s
     for (int k = 8 * (lane + 64 * HELD); k < K; k += 512)
         *(u32x4 *)(x16 + k) = lifted(*(const u32x4 *)(x + k), up);
     const bool wide = __any(below(low, up)) && lift_blocks(x, x16, to.shift + m * 4 * quads_of(K), up, K);
+    if (!wide)
+        for (int q = lane; q < quads_of(K); q += 64)
+            ((uint32_t *)to.shift)[m * quads_of(K) + q] = 0;
     if (lane == 0) {
         to.lift[m] = up;
         to.wide[m] = wide;
@@ -590,8 +593,8 @@ struct UpIn {
 };
 
 // The rows' operands of one quad; where WIDE, with the further powers of two of
-// the rows whose values the lane group accumulates (rows that are not wide:
-// none, and the same bits).  row(i): the batch row of row i of the group.
+// the rows whose values the lane group accumulates (2^0 in rows that are not
+// wide, and the same bits).  row(i): the batch row of row i of the group.
 template <int R, bool WIDE>
 struct RowsX {
     u32x4 x[R];
@@ -613,7 +616,7 @@ struct RowsX {
             in.shift = buffer_of(u.shift, (size_t)u.M * pitch);
 #pragma unroll
             for (int r = 0; r < R; ++r)
-                in.shift_at[r] = 4 * r + g < rows && u.wide[row(4 * r + g)] ? (uint32_t)row(4 * r + g) * pitch : kNowhere;
+                in.shift_at[r] = 4 * r + g < rows ? (uint32_t)row(4 * r + g) * pitch : kNowhere;
         }
         in.nb = nb;
         in.last = (nb - 1) / 4;
@@ -703,8 +706,7 @@ struct RowsH {
 // weights by the caller).  The run's part of the tree waits in the wave's own
 // LDS, stack [level][tile][r][lane] (levels that the trailing one-bits of a
 // segment's number name are merged, left operand first), and ends in level 0.
-// AHEAD false: one quad at a time, in fewer registers.
-template <int R, typename ROWS, bool AHEAD>
+template <int R, typename ROWS>
 __device__ __forceinline__ void multiply_run(const FourTiles &tiles, Weights &first, const typename ROWS::In &in, int sa,
                                              int L, const Plan &plan, float *stack)
 {
@@ -754,19 +756,9 @@ __device__ __forceinline__ void multiply_run(const FourTiles &tiles, Weights &fi
             end = ((sa + seg + 1) * plan.G) >> plan.log2S;
         }
     };
-    ROWS xa;
-    xa.load(in, qa);
-    if constexpr (!AHEAD) {
-        for (int q = qa; q < qb; ++q) {
-            multiply(first, xa, q);
-            first.load(tiles, q + 1, qb);
-            xa.load(in, q + 1);
-            issue_fence();
-        }
-        return;
-    }
     Weights second;
-    ROWS xb;
+    ROWS xa, xb;
+    xa.load(in, qa);
     for (int q = qa; q < qb; q += 2) {
         second.load(tiles, q + 1, qb);
         xb.load(in, q + 1);
@@ -802,6 +794,7 @@ __device__ __forceinline__ float join_roots(const Roots &at, int tile, int i, in
 
 // gate and up: a unit is two tiles of gate and two of up, so that it ends with
 // 32 values of h, one block of the down product.
+template <bool BF16>
 struct Up {
     UpIn x;
     uint16_t *hi, *lo;
@@ -812,13 +805,18 @@ struct Up {
     static constexpr int waves(int RM) { return RM == 1 ? 4 : 3; }
     template <int R, bool WIDE>
     using Rows = RowsX<R, WIDE>;
-    static constexpr bool kWide = true;
+    // Groups of 4 and 8 rows carry the powers of two of bfloat16's blocks always
+    // (a load and four operations a tile and quad: 0.4 to 1.3 us a layer), groups
+    // of 16 have no registers for them (27 spilled): a batch with a wide row goes 4
+    // rows at a time there (64 rows of 64 experts 3584 x 1792: 167 -> 238 us).
+    static constexpr bool always(int RM) { return BF16 && RM <= 2; }
+    static constexpr bool asks(int RM) { return BF16 && RM > 2; }
     // what a lane knows of the wide rows of the batch: loaded first, used after
     // the weights are on their way
     __device__ __forceinline__ int wide() const
     {
-        int m = threadIdx.x & 63, any = x.wide && m < x.M ? x.wide[m] : 0;
-        if (x.wide && x.M > 64)
+        int m = threadIdx.x & 63, any = m < x.M ? x.wide[m] : 0;
+        if (x.M > 64)
             for (m += 64; m < x.M; m += 64)
                 any |= x.wide[m];
         return any;
@@ -838,7 +836,7 @@ struct Up {
     // (loaded before the products, used after them)
     __device__ __forceinline__ int before(const uint16_t *list, int rows) const
     {
-        return x.lift && (int)threadIdx.x < rows ? -x.lift[list[threadIdx.x] / topk] : 0;
+        return BF16 && (int)threadIdx.x < rows ? -x.lift[list[threadIdx.x] / topk] : 0;
     }
     // 32 lanes a row: the trees, the activation, the block's power of two
     template <int R>
@@ -889,7 +887,8 @@ struct Down {
     static constexpr int waves(int RM) { return RM == 1 ? 4 : RM == 2 ? 3 : 2; }
     template <int R, bool>
     using Rows = RowsH<R>;
-    static constexpr bool kWide = false;
+    static constexpr bool always(int) { return false; }
+    static constexpr bool asks(int) { return false; }
     __device__ __forceinline__ int wide() const { return 0; }
     __host__ __device__ int units() const { return (H + 63) / 64; }
     // (past the last column: the last tile, its values are not stored)
@@ -931,11 +930,7 @@ __host__ __device__ inline int tree_levels(int L)
 // tiles of one expert a workgroup, its waves on runs of L segments of K.  An
 // expert's rows go 4 RM at a time (the last ones 4, 8 or 16, by how many are
 // left), group r to the workgroup z = r mod Z; the weights of the next group's
-// first quad are on their way while this one's sums are joined.  With a wide
-// row in the batch the rows go 4 at a time, to the same bits: the powers of two
-// of 16 rows do not fit the registers, and where groups are of 4 anyway, a quad
-// ahead would take the fifth wave from batches without such a row (128 experts
-// 2048 x 768 at 8 rows: gate/up 23.6 us with four waves, 21.6 with five).
+// first quad are on their way while this one's sums are joined.
 // Few rows: bound by launch and memory latency (64 experts 2048 x 1024 at one
 // row: gate/up with its choice 11.1 us, down 6.5 us).  Many: by the weights'
 // stream and the dequantization's issue (47 VALU operations a tile and quad, half of
@@ -952,7 +947,7 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(OP::waves(R
     __shared__ int back[16];
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), waves = blockDim.x >> 6;
     const int levels = tree_levels(L);
-    const int wide_lane = op.wide();
+    const int wide_lane = OP::asks(RM) ? op.wide() : 0;
     if (ch.parts) {
         uint64_t *keys = (uint64_t *)part;
         choose_rows<int16_t>(ch, 0, ch.M, keys, (double *)(keys + ch.M * ch.E), found.who, ids, weights,
@@ -966,7 +961,7 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(OP::waves(R
         tiles = op.tiles(wq, scales, e, blockIdx.x, plan.G);
         first.load(tiles, qa, qb);
     });
-    const bool wide = __any(wide_lane);
+    const bool wide = OP::asks(RM) && __any(wide_lane);
     const int most = wide ? 4 : 4 * RM, step = most * gridDim.z;
     for (int r0 = most * blockIdx.z; r0 < count; r0 += step) {
         const int left = min(count - r0, most);
@@ -975,7 +970,7 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(OP::waves(R
             constexpr int R = decltype(r)::value;
             constexpr bool WIDE = decltype(w)::value;
             const int b = op.before(list, left);
-            multiply_run<R, typename OP::template Rows<R, WIDE>, !WIDE || RM != 1>(
+            multiply_run<R, typename OP::template Rows<R, WIDE>>(
                 tiles, first, op.template in<R, WIDE>(list, left, plan.nb), wave * L, L, plan,
                 part + wave * levels * 4 * R * 64);
             if ((int)threadIdx.x < 16)
@@ -987,14 +982,15 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(OP::waves(R
             if (r0 + step < count)
                 __syncthreads();  // the sums are read
         };
-        if (OP::kWide && wide)
-            group(std::integral_constant<int, 1>(), std::integral_constant<bool, OP::kWide>());
+        typedef std::integral_constant<bool, OP::always(RM)> Always;
+        if (OP::asks(RM) && wide)
+            group(std::integral_constant<int, 1>(), std::integral_constant<bool, OP::asks(RM)>());
         else if (RM == 1 || left <= 4)
-            group(std::integral_constant<int, 1>(), std::false_type());
+            group(std::integral_constant<int, 1>(), Always());
         else if (RM == 2 || left <= 8)
-            group(std::integral_constant<int, RM == 1 ? 1 : 2>(), std::false_type());
+            group(std::integral_constant<int, RM == 1 ? 1 : 2>(), Always());
         else
-            group(std::integral_constant<int, RM>(), std::false_type());
+            group(std::integral_constant<int, RM>(), Always());
     }
 }
 
@@ -1183,8 +1179,11 @@ hipError_t products(const Choice &ch, const UpIn &x, int *ids, float *weights, c
                     const uint8_t *w2, const uint16_t *s2, float *y, int I, const MoeRoom &room, hipStream_t stream)
 {
     const int n = ch.M * ch.topk, H = x.H, shifts = MoeRoom::shifts_of(I);
-    const Up up{x, room.hi, room.lo, room.shift, ch.topk, I, shifts};
-    hipError_t e = launch_product(ch, up, ids, weights, w13, s13, make_plan(H), stream);
+    hipError_t e =
+        x.lift ? launch_product(ch, Up<true>{x, room.hi, room.lo, room.shift, ch.topk, I, shifts}, ids, weights, w13,
+                                s13, make_plan(H), stream)
+               : launch_product(ch, Up<false>{x, room.hi, room.lo, room.shift, ch.topk, I, shifts}, ids, weights, w13,
+                                s13, make_plan(H), stream);
     if (e != hipSuccess)
         return e;
     Choice given = ch;

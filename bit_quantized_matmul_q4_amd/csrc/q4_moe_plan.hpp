@@ -34,6 +34,8 @@ inline bool moe_by_rows(int M, int E, int K) { return logit_parts(M, E, K) == 1 
 //   32 x 8       27.7 / 27.9  30.4 / 32.2  55.5 / 56.5
 //   4 x 64       22.4 / 22.3  36.8 / 37.6  80.0 / 76.3
 //   16 x 16      25.3 / 26.8  40.2 / 41.7  64.4 / 64.0
+//   8 x 36       21.8 / 19.8  28.2 / 29.1
+//   32 x 12      28.1 / 25.9  40.1 / 40.8
 //   16 x 32      24.9 / 24.0  45.8 / 41.1  93.5 / 81.7
 //   64 x 4       33.2 / 27.2  43.4 / 44.9  63.2 / 66.5
 //   64 x 8       34.6 / 27.4  41.3 / 41.8  73.5 / 71.4
