@@ -27,7 +27,9 @@ from ._lib import KERNELS, Q4Error
 __all__ = ["Q4Weight", "linear", "linear_noalloc", "linear_grouped", "pack", "pack_nibbles", "quantize", "quantize_pack", "concat_n", "split_n", "packed_sizes", "workspace_bytes", "get_crossover",
            "set_crossover", "segments", "Q4Error", "library_path",
            "Int8Matrix", "quantize_int8", "pack_int8", "quantize_pack_int8", "linear_int8",
-           "moe_route", "moe_experts", "moe"]
+           "moe_route", "moe_experts", "moe",
+           "Mx4Matrix", "quantize_mx4", "pack_mx4", "quantize_pack_mx4", "dequantize_mx4", "linear_mx4",
+           "Norm", "block_norm"]
 
 
 def library_path() -> str:
@@ -418,6 +420,261 @@ def linear_int8(x, w: Int8Matrix, out: torch.Tensor | None = None, out_dtype: to
     _call(dev, "q4_int8_linear", lib.q4_int8_linear, x_ptr, kind, xs_ptr, w.codes.data_ptr(), w.scales.data_ptr(),
           out.data_ptr(), _DTYPES[out.dtype], M, N, K, ws_ptr, ws_len)
     return out
+
+
+@dataclass
+class Mx4Matrix:
+    """A packed matrix in microscaled 4-bit floating point (weights, or
+    activations that several products share): ``codes`` uint8
+    [q4_mx4_code_bytes], ``scales`` uint8 [q4_mx4_scale_bytes], both on one
+    GPU."""
+    codes: torch.Tensor
+    scales: torch.Tensor
+    rows: int
+    K: int
+
+    @property
+    def device(self) -> torch.device:
+        return self.codes.device
+
+
+def _empty_mx4(rows: int, K: int, dev) -> Mx4Matrix:
+    lib = _lib.load()
+    n = lib.q4_mx4_code_bytes(rows, K)
+    if n == 0:
+        raise ValueError("bad shape %d x %d (K must be a positive multiple of 32, at most 131072)" % (rows, K))
+    return Mx4Matrix(torch.empty(n, dtype=torch.uint8, device=dev),
+                     torch.empty(lib.q4_mx4_scale_bytes(rows, K), dtype=torch.uint8, device=dev), rows, K)
+
+
+def _need_mx4(w, name: str, device=None):
+    if not isinstance(w, Mx4Matrix):
+        raise TypeError("%s must be an Mx4Matrix (see pack_mx4)" % name)
+    _need(w.codes, name + ".codes", (torch.uint8,), 1, device)
+    _need(w.scales, name + ".scales", (torch.uint8,), 1, w.codes.device)
+    tiles = -(-w.rows // 16)  # (q4_mx4_code_bytes and q4_mx4_scale_bytes, without the calls)
+    if (w.rows < 1 or w.K < 32 or w.K % 32 or w.codes.numel() != 1024 * tiles * -(-w.K // 128)
+            or w.scales.numel() != 256 * tiles * -(-w.K // 512)):
+        raise ValueError("%s does not hold %d x %d packed codes and scales" % (name, w.rows, w.K))
+
+
+def quantize_mx4(w: torch.Tensor):
+    """Dense rows [R, K] (float32, bfloat16 or float16, on a GPU) -> canonical
+    (codes uint8 [R, K/2], scales uint8 [R, K/32]) for ``pack_mx4``: per block
+    of 32 values of a row one power of two (scale byte - 127), 4-bit
+    floating-point codes (1 sign, 2 exponent, 1 mantissa bit), even k in the
+    low half of a byte.  The largest value of a block lies in 4 .. 8 of its
+    scale; what is over 6 becomes 6, the others round to the nearest, ties to
+    the even code.  A block with an infinity or NaN gets scale byte 255 (NaN)
+    and codes 0 (include/q4.h)."""
+    lib = _lib.load()
+    _need(w, "w", tuple(_DTYPES), 2)
+    R, K = w.shape
+    codes = torch.empty((R, K // 2), dtype=torch.uint8, device=w.device)
+    scales = torch.empty((R, K // 32), dtype=torch.uint8, device=w.device)
+    _call(w.device, "q4_mx4_quantize", lib.q4_mx4_quantize, w.data_ptr(), _DTYPES[w.dtype], codes.data_ptr(),
+          scales.data_ptr(), R, K)
+    return codes, scales
+
+
+def pack_mx4(codes: torch.Tensor, scales: torch.Tensor) -> Mx4Matrix:
+    """codes uint8 [R, K/2] (two a byte, even k low), scales uint8 [R, K/32]
+    -> Mx4Matrix."""
+    lib = _lib.load()
+    _need(codes, "codes", (torch.uint8,), 2)
+    _need(scales, "scales", (torch.uint8,), 2, codes.device)
+    R, K = codes.shape[0], codes.shape[1] * 2
+    if tuple(scales.shape) != (R, K // 32):
+        raise ValueError("scales must be [%d, %d]" % (R, K // 32))
+    m = _empty_mx4(R, K, codes.device)
+    _call(codes.device, "q4_mx4_pack", lib.q4_mx4_pack, codes.data_ptr(), scales.data_ptr(), m.codes.data_ptr(),
+          m.scales.data_ptr(), R, K)
+    return m
+
+
+def quantize_pack_mx4(w: torch.Tensor) -> Mx4Matrix:
+    """quantize_mx4() and pack_mx4() in one kernel: dense rows [R, K] ->
+    Mx4Matrix (a weight, or activations for several ``linear_mx4`` calls)."""
+    lib = _lib.load()
+    _need(w, "w", tuple(_DTYPES), 2)
+    R, K = w.shape
+    m = _empty_mx4(R, K, w.device)
+    _call(w.device, "q4_mx4_quantize_pack", lib.q4_mx4_quantize_pack, w.data_ptr(), _DTYPES[w.dtype],
+          m.codes.data_ptr(), m.scales.data_ptr(), R, K)
+    return m
+
+
+def dequantize_mx4(m: Mx4Matrix, dtype: torch.dtype = torch.float32, out: torch.Tensor | None = None) -> torch.Tensor:
+    """The values [R, K] that a packed matrix stands for, in float32, bfloat16
+    or float16 (``out``'s own type if given): exact in the type they were
+    quantized from."""
+    lib = _lib.load()
+    _need_mx4(m, "m")
+    if out is None:
+        if dtype not in _DTYPES:
+            raise TypeError("dtype must be one of %s" % (tuple(_DTYPES),))
+        out = torch.empty((m.rows, m.K), dtype=dtype, device=m.device)
+    else:
+        _need_out(out, (m.rows, m.K), tuple(_DTYPES), m.device)
+    _call(m.device, "q4_mx4_dequantize", lib.q4_mx4_dequantize, m.codes.data_ptr(), m.scales.data_ptr(),
+          out.data_ptr(), _DTYPES[out.dtype], m.rows, m.K)
+    return out
+
+
+def linear_mx4(x, w: Mx4Matrix, out: torch.Tensor | None = None, out_dtype: torch.dtype = torch.float32,
+               workspace: torch.Tensor | bool | None = True) -> torch.Tensor:
+    """y[m, n] = sum_k x[m, k] w[n, k] of the values that both operands' 4-bit
+    forms stand for, on the current stream of x's device.
+
+    x: bfloat16 or float16 [M, K], quantized block by block within the call, or
+    an Mx4Matrix (``quantize_pack_mx4``, ``block_norm``) that several products
+    share; the bits are the same.  out_dtype: float32, bfloat16 or float16
+    (``out``'s own if given).  workspace: True allocates what the call needs; a
+    uint8 tensor is used as given; False/None for calls that need none.  A
+    row's bits do not depend on the other rows.
+    """
+    lib = _lib.load()
+    if not isinstance(x, Mx4Matrix):
+        _need(x, "x", (torch.bfloat16, torch.float16), 2)
+        M, K = x.shape
+        kind, x_ptr, xs_ptr = _DTYPES[x.dtype], x.data_ptr(), None
+    else:
+        _need_mx4(x, "x")
+        M, K = x.rows, x.K
+        kind, x_ptr, xs_ptr = _lib.Q4_MX4, x.codes.data_ptr(), x.scales.data_ptr()
+    dev = x.device
+    _need_mx4(w, "w", dev)
+    N = w.rows
+    if K != w.K:
+        raise ValueError("x has K=%d, weight has K=%d" % (K, w.K))
+    if out is None:
+        if out_dtype not in _DTYPES:
+            raise TypeError("out_dtype must be one of %s" % (tuple(_DTYPES),))
+        out = torch.empty((M, N), dtype=out_dtype, device=dev)
+    else:
+        _need_out(out, (M, N), tuple(_DTYPES), dev)
+    _keep, ws_ptr, ws_len = _workspace(workspace, lib.q4_mx4_workspace_bytes(M, N, K, kind), dev)
+    _call(dev, "q4_mx4_linear", lib.q4_mx4_linear, x_ptr, kind, xs_ptr, w.codes.data_ptr(), w.scales.data_ptr(),
+          out.data_ptr(), _DTYPES[out.dtype], M, N, K, ws_ptr, ws_len)
+    return out
+
+
+_NORMS = {"rms": _lib.Q4_NORM_RMS, "layer": _lib.Q4_NORM_LAYER}
+
+
+@dataclass
+class Norm:
+    """A norm of ``block_norm``: ``kind`` "rms" (v / sqrt(mean(v^2) + eps)) or
+    "layer" ((v - mean) / sqrt(variance + eps)), times ``weight`` [H] (None:
+    1) plus ``bias`` [H] (None: 0), both of one type."""
+    weight: torch.Tensor | None = None
+    bias: torch.Tensor | None = None
+    kind: str = "rms"
+    eps: float = 1e-6
+
+
+def _norm_side(n, name: str, H: int, dev):
+    """A Norm as the library takes it (None stays None)."""
+    if n is None:
+        return None
+    if not isinstance(n, Norm):
+        raise TypeError("%s must be a Norm or None" % name)
+    if n.kind not in _NORMS:
+        raise ValueError("%s.kind must be one of %s" % (name, sorted(_NORMS)))
+    kind = _lib.Q4_F32
+    for part, t in (("weight", n.weight), ("bias", n.bias)):
+        if t is None:
+            continue
+        _need(t, "%s.%s" % (name, part), tuple(_DTYPES), 1, dev)
+        if t.numel() != H:
+            raise ValueError("%s.%s must be [%d]" % (name, part, H))
+        if part == "bias" and n.weight is not None and t.dtype != n.weight.dtype:
+            raise TypeError("%s.weight and %s.bias must have one dtype" % (name, name))
+        kind = _DTYPES[t.dtype]
+    return _lib.NormSide(None if n.weight is None else n.weight.data_ptr(),
+                         None if n.bias is None else n.bias.data_ptr(), _NORMS[n.kind], kind, n.eps)
+
+
+def block_norm(y: torch.Tensor, residual: torch.Tensor | None = None, post: Norm | None = None,
+               gate: torch.Tensor | None = None, scale: float = 1.0, pre: Norm | None = None,
+               out_dtype: torch.dtype | str = torch.bfloat16, r_out: torch.Tensor | bool | None = None,
+               out: torch.Tensor | Mx4Matrix | bool | None = None):
+    """What stands between two linear layers of a block, in one kernel:
+
+        r = residual + scale gate post(y),    h = pre(r)
+
+    Returns (r, h).  y: a projection's output [M, H] (float32, bfloat16 or
+    float16); residual: the stream [M, H] (None: 0); post, pre: a ``Norm`` or
+    None for none; gate: [H], [M, 1] or [M, H] (None: 1).  r has the residual's
+    type (y's without one, ``r_out``'s if given); ``r_out=residual`` updates
+    the stream in place.  h: ``out_dtype`` float32, bfloat16 or float16
+    (``out``'s own if given), or "mx4" for an Mx4Matrix that ``linear_mx4``
+    takes.  ``r_out=False`` or ``out=False``: that one is not stored (and None).
+    Sums and everything in between are float32; pre takes r before it is
+    rounded.  A row's bits do not depend on the other rows (include/q4.h).
+    """
+    lib = _lib.load()
+    floats = tuple(_DTYPES)
+    _need(y, "y", floats, 2)
+    dev = y.device
+    M, H = y.shape
+    r_dtype = y.dtype
+    if residual is not None:
+        _need(residual, "residual", floats, 2, dev)
+        if residual.shape != y.shape:
+            raise ValueError("residual must be [%d, %d]" % (M, H))
+        r_dtype = residual.dtype
+    if r_out is None:
+        r_out = torch.empty((M, H), dtype=r_dtype, device=dev)
+    elif r_out is False:
+        r_out = None
+    else:
+        _need(r_out, "r_out", floats if residual is None else (r_dtype,), 2, dev)
+        if r_out.shape != y.shape:
+            raise ValueError("r_out must be [%d, %d]" % (M, H))
+    gate_ptr, gate_kind, form = None, _lib.Q4_F32, _lib.Q4_GATE_NONE
+    if gate is not None:
+        if not isinstance(gate, torch.Tensor):
+            raise TypeError("gate must be a torch.Tensor")
+        _need(gate, "gate", floats, 1 if gate.dim() == 1 else 2, dev)
+        shape = tuple(gate.shape)
+        if shape == (H,):
+            form = _lib.Q4_GATE_CHANNEL
+        elif shape == (M, H):
+            form = _lib.Q4_GATE_VALUE
+        elif shape == (M, 1):
+            form = _lib.Q4_GATE_ROW
+        else:
+            raise ValueError("gate must be [%d], [%d, 1] or [%d, %d], got %s" % (H, M, M, H, shape))
+        gate_ptr, gate_kind = gate.data_ptr(), _DTYPES[gate.dtype]
+    post, pre = _norm_side(post, "post", H, dev), _norm_side(pre, "pre", H, dev)
+    if out is False:
+        out = None
+        if r_out is None:
+            raise ValueError("block_norm stores r, h or both")
+    elif out is None and out_dtype == "mx4":
+        out = _empty_mx4(M, H, dev)
+    elif out is None:
+        if out_dtype not in _DTYPES:
+            raise TypeError("out_dtype must be \"mx4\" or one of %s" % (floats,))
+        out = torch.empty((M, H), dtype=out_dtype, device=dev)
+    elif isinstance(out, Mx4Matrix):
+        _need_mx4(out, "out", dev)
+        if (out.rows, out.K) != (M, H):
+            raise ValueError("out must be %d x %d" % (M, H))
+    else:
+        _need_out(out, (M, H), floats, dev)
+    if out is None:
+        h_ptr, h_kind, hs_ptr = None, _lib.Q4_F32, None
+    elif isinstance(out, Mx4Matrix):
+        h_ptr, h_kind, hs_ptr = out.codes.data_ptr(), _lib.Q4_MX4, out.scales.data_ptr()
+    else:
+        h_ptr, h_kind, hs_ptr = out.data_ptr(), _DTYPES[out.dtype], None
+    _call(dev, "q4_block_norm", lib.q4_block_norm, y.data_ptr(), _DTYPES[y.dtype], post, gate_ptr, gate_kind, form,
+          scale, None if residual is None else residual.data_ptr(), None if r_out is None else r_out.data_ptr(),
+          _DTYPES[r_dtype if r_out is None else r_out.dtype], pre, h_ptr, h_kind,
+          hs_ptr, M, H)
+    return r_out, out
 
 
 def _need_route(x, router, topk, bias):

@@ -26,10 +26,20 @@ Q4_F16 = 0
 Q4_BF16 = 1
 Q4_F32 = 2
 Q4_I8 = 3
+Q4_MX4 = 4
 
 Q4_AUTO = 0
 Q4_GEMV = 1
 Q4_GEMM = 2
+
+Q4_NORM_NONE = 0
+Q4_NORM_RMS = 1
+Q4_NORM_LAYER = 2
+
+Q4_GATE_NONE = 0
+Q4_GATE_CHANNEL = 1
+Q4_GATE_ROW = 2
+Q4_GATE_VALUE = 3
 
 KERNELS = {"auto": Q4_AUTO, "gemv": Q4_GEMV, "gemm": Q4_GEMM}
 
@@ -39,6 +49,8 @@ EXPORTS = (
     "q4_int8_packed_bytes", "q4_int8_quantize", "q4_int8_quantize_pack", "q4_int8_pack", "q4_int8_workspace_bytes",
     "q4_int8_linear", "q4_moe_route", "q4_moe_route_workspace_bytes", "q4_moe_experts",
     "q4_moe_experts_workspace_bytes", "q4_moe_layer", "q4_moe_layer_workspace_bytes",
+    "q4_mx4_code_bytes", "q4_mx4_scale_bytes", "q4_mx4_quantize", "q4_mx4_quantize_pack", "q4_mx4_pack",
+    "q4_mx4_dequantize", "q4_mx4_workspace_bytes", "q4_mx4_linear", "q4_block_norm",
     "q4_packed_code_bytes", "q4_packed_scale_bytes",
     "q4_get_crossover", "q4_set_crossover", "q4_segments", "q4_strerror",
     "q4_last_hip_error", "q4_abi_version",
@@ -51,6 +63,12 @@ GROUP_MAX = 8
 class GroupItem(ctypes.Structure):
     """q4_group_item (include/q4.h)."""
     _fields_ = [("Wq", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("y", ctypes.c_void_p), ("N", ctypes.c_int)]
+
+
+class NormSide(ctypes.Structure):
+    """q4_norm (include/q4.h)."""
+    _fields_ = [("weight", ctypes.c_void_p), ("bias", ctypes.c_void_p), ("kind", ctypes.c_int),
+                ("dtype", ctypes.c_int), ("eps", ctypes.c_float)]
 
 
 class Q4Error(RuntimeError):
@@ -115,6 +133,23 @@ def _declare(lib):
     lib.q4_moe_layer.restype = i
     lib.q4_moe_layer_workspace_bytes.argtypes = [i, i, i, i, i]
     lib.q4_moe_layer_workspace_bytes.restype = sz
+    for f in (lib.q4_mx4_code_bytes, lib.q4_mx4_scale_bytes):
+        f.argtypes = [i, i]
+        f.restype = sz
+    for f in (lib.q4_mx4_quantize, lib.q4_mx4_quantize_pack):
+        f.argtypes = [vp, i, vp, vp, i, i, vp]
+        f.restype = i
+    lib.q4_mx4_pack.argtypes = [vp, vp, vp, vp, i, i, vp]
+    lib.q4_mx4_pack.restype = i
+    lib.q4_mx4_dequantize.argtypes = [vp, vp, vp, i, i, i, vp]
+    lib.q4_mx4_dequantize.restype = i
+    lib.q4_mx4_workspace_bytes.argtypes = [i, i, i, i]
+    lib.q4_mx4_workspace_bytes.restype = sz
+    lib.q4_mx4_linear.argtypes = [vp, i, vp, vp, vp, vp, i, i, i, i, vp, sz, vp]
+    lib.q4_mx4_linear.restype = i
+    side = ctypes.POINTER(NormSide)
+    lib.q4_block_norm.argtypes = [vp, i, side, vp, i, i, ctypes.c_float, vp, vp, i, side, vp, i, vp, i, i, vp]
+    lib.q4_block_norm.restype = i
     lib.q4_get_crossover.argtypes = []
     lib.q4_get_crossover.restype = i
     lib.q4_set_crossover.argtypes = [i]

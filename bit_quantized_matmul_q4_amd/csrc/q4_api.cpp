@@ -110,6 +110,19 @@ int check_moe(long long M, long long E, long long K, long long topk)
     return Q4_OK;
 }
 
+// Shapes of the microscaled 4-bit form and its product.
+int check_mx4(long long rows, long long N, long long K)
+{
+    if (rows < 1 || N < 1 || K < 32 || K % 32 != 0 || K > Q4_MX4_MAX_K)
+        return Q4_ERR_SHAPE;
+    const long long lim = 1LL << 24;
+    if (rows > lim || N > lim || rows > (1LL << 36) / N)
+        return Q4_ERR_SHAPE;
+    return Q4_OK;
+}
+
+bool is_float(int dtype) { return dtype == Q4_F16 || dtype == Q4_BF16 || dtype == Q4_F32; }
+
 // The launchers' element kinds.
 int elem_kind(int dtype) { return dtype == Q4_F32 ? 2 : dtype == Q4_BF16 ? 1 : 0; }
 
@@ -134,9 +147,9 @@ const char *q4_strerror(int status)
     switch (status) {
     case Q4_OK: return "ok";
     case Q4_ERR_NULL: return "a required pointer is NULL";
-    case Q4_ERR_SHAPE: return "bad shape (need M >= 1, N >= 1, K >= 32, K % 32 == 0, 1 <= topk <= experts, sizes in range)";
-    case Q4_ERR_ALIGN: return "misaligned pointer (x, Wq, router, quantizer w and codes: 16 B; packed scales: 8 B; y, float32 scales, bias, ids, weights: 4 B; 16-bit y: 2 B; workspace: 256 B)";
-    case Q4_ERR_ENUM: return "unknown dtype or kernel selector";
+    case Q4_ERR_SHAPE: return "bad shape (need M >= 1, N >= 1, K >= 32, K % 32 == 0, 1 <= topk <= experts, eps >= 0, sizes in range)";
+    case Q4_ERR_ALIGN: return "misaligned pointer (x, Wq, router, quantizer w and codes: 16 B; packed scales: 8 B, microscaled 4 B; y, float32 scales, bias, ids, weights: 4 B; 16-bit y: 2 B; q4_block_norm: its elements'; workspace: 256 B)";
+    case Q4_ERR_ENUM: return "unknown dtype, kernel selector, norm kind or gate form";
     case Q4_ERR_HIP: return "HIP launch error (see q4_last_hip_error)";
     case Q4_ERR_WORKSPACE: return "workspace too small or absent in a call that needs one, or workspace_bytes > 0 with a NULL workspace";
     case Q4_ERR_SCRATCH: return "the call needs more than the library's fixed scratch buffer (Q4_SCRATCH_BYTES)";
@@ -437,6 +450,162 @@ int q4_int8_linear(const void *x, int x_dtype, const float *x_scales, const void
     return hip_status(q4::launch_int8_linear(x, x_dtype == Q4_I8 ? -1 : elem_kind(x_dtype), x_scales,
                                              (const int8_t *)Wq, w_scales, y, elem_kind(y_dtype), M, N, K, workspace,
                                              (hipStream_t)stream));
+}
+
+size_t q4_mx4_code_bytes(int rows, int K)
+{
+    return check_mx4(rows, 1, K) == Q4_OK ? q4::mx4_code_bytes(rows, K) : 0;
+}
+
+size_t q4_mx4_scale_bytes(int rows, int K)
+{
+    return check_mx4(rows, 1, K) == Q4_OK ? q4::mx4_scale_bytes(rows, K) : 0;
+}
+
+static int mx4_quantize(const void *w, int w_dtype, uint8_t *codes, uint8_t *scales, bool packed, int rows, int K,
+                        void *stream)
+{
+    if (!w || !codes || !scales)
+        return Q4_ERR_NULL;
+    if (!is_float(w_dtype))
+        return Q4_ERR_ENUM;
+    const int sh = check_mx4(rows, 1, K);
+    if (sh != Q4_OK)
+        return sh;
+    if (!aligned(w, 16) || !aligned(codes, 16) || (packed && !aligned(scales, 4)))
+        return Q4_ERR_ALIGN;
+    return hip_status(q4::launch_mx4_quantize(w, elem_kind(w_dtype), codes, scales, packed, rows, K,
+                                              (hipStream_t)stream));
+}
+
+int q4_mx4_quantize(const void *w, int w_dtype, uint8_t *codes, uint8_t *scales, int rows, int K, void *stream)
+{
+    return mx4_quantize(w, w_dtype, codes, scales, false, rows, K, stream);
+}
+
+int q4_mx4_quantize_pack(const void *w, int w_dtype, void *packed, void *packed_scales, int rows, int K, void *stream)
+{
+    return mx4_quantize(w, w_dtype, (uint8_t *)packed, (uint8_t *)packed_scales, true, rows, K, stream);
+}
+
+int q4_mx4_pack(const uint8_t *codes, const uint8_t *scales, void *packed, void *packed_scales, int rows, int K,
+                void *stream)
+{
+    if (!codes || !scales || !packed || !packed_scales)
+        return Q4_ERR_NULL;
+    const int sh = check_mx4(rows, 1, K);
+    if (sh != Q4_OK)
+        return sh;
+    if (!aligned(codes, 16) || !aligned(packed, 16) || !aligned(packed_scales, 4))
+        return Q4_ERR_ALIGN;
+    return hip_status(q4::launch_mx4_pack(codes, scales, (uint8_t *)packed, (uint8_t *)packed_scales, rows, K,
+                                          (hipStream_t)stream));
+}
+
+int q4_mx4_dequantize(const void *packed, const void *packed_scales, void *w, int w_dtype, int rows, int K,
+                      void *stream)
+{
+    if (!packed || !packed_scales || !w)
+        return Q4_ERR_NULL;
+    if (!is_float(w_dtype))
+        return Q4_ERR_ENUM;
+    const int sh = check_mx4(rows, 1, K);
+    if (sh != Q4_OK)
+        return sh;
+    if (!aligned(packed, 16) || !aligned(packed_scales, 4) || !aligned(w, 16))
+        return Q4_ERR_ALIGN;
+    return hip_status(q4::launch_mx4_dequantize((const uint8_t *)packed, (const uint8_t *)packed_scales, w,
+                                                elem_kind(w_dtype), rows, K, (hipStream_t)stream));
+}
+
+size_t q4_mx4_workspace_bytes(int M, int N, int K, int x_dtype)
+{
+    if (check_mx4(M, N, K) != Q4_OK || (x_dtype != Q4_F16 && x_dtype != Q4_BF16 && x_dtype != Q4_MX4))
+        return 0;
+    return q4::mx4_workspace_bytes(x_dtype != Q4_MX4, M, N, K);
+}
+
+int q4_mx4_linear(const void *x, int x_dtype, const void *x_scales, const void *Wq, const void *w_scales, void *y,
+                  int y_dtype, int M, int N, int K, void *workspace, size_t workspace_bytes, void *stream)
+{
+    if (!x || !Wq || !w_scales || !y || (x_dtype == Q4_MX4 && !x_scales))
+        return Q4_ERR_NULL;
+    if ((x_dtype != Q4_F16 && x_dtype != Q4_BF16 && x_dtype != Q4_MX4) || !is_float(y_dtype))
+        return Q4_ERR_ENUM;
+    const int sh = check_mx4(M, N, K);
+    if (sh != Q4_OK)
+        return sh;
+    if (!aligned(x, 16) || (x_dtype == Q4_MX4 && !aligned(x_scales, 4)) || !aligned(Wq, 16) || !aligned(w_scales, 4) ||
+        !aligned(y, y_dtype == Q4_F32 ? 4 : 2))
+        return Q4_ERR_ALIGN;
+    if (workspace_bytes > 0 && !workspace)
+        return Q4_ERR_WORKSPACE;
+    if (workspace && !aligned(workspace, 256))
+        return Q4_ERR_ALIGN;
+    if (workspace_bytes < q4::mx4_workspace_bytes(x_dtype != Q4_MX4, M, N, K))
+        return Q4_ERR_WORKSPACE;
+    return hip_status(q4::launch_mx4_linear(x, x_dtype == Q4_MX4 ? -1 : elem_kind(x_dtype), (const uint8_t *)x_scales,
+                                            (const uint8_t *)Wq, (const uint8_t *)w_scales, y, elem_kind(y_dtype), M, N,
+                                            K, workspace, (hipStream_t)stream));
+}
+
+// Alignment of an element type's arrays where no wider one is asked for.
+static uintptr_t elem_align(int dtype) { return dtype == Q4_F32 ? 4 : 2; }
+
+static int check_norm(const q4_norm *n, q4::NormSide *out)
+{
+    *out = q4::NormSide{};
+    if (!n || n->kind == Q4_NORM_NONE)
+        return Q4_OK;
+    if ((n->kind != Q4_NORM_RMS && n->kind != Q4_NORM_LAYER) || !is_float(n->dtype))
+        return Q4_ERR_ENUM;
+    if (!(n->eps >= 0.f && n->eps <= 3.4028235e38f))
+        return Q4_ERR_SHAPE;
+    if (!aligned(n->weight, elem_align(n->dtype)) || !aligned(n->bias, elem_align(n->dtype)))
+        return Q4_ERR_ALIGN;
+    *out = q4::NormSide{n->weight, n->bias, n->kind, elem_kind(n->dtype), n->eps};
+    return Q4_OK;
+}
+
+int q4_block_norm(const void *y, int y_dtype, const q4_norm *post, const void *gate, int gate_dtype, int gate_form,
+                  float scale, const void *residual, void *r, int r_dtype, const q4_norm *pre, void *h, int h_dtype,
+                  void *h_scales, int M, int H, void *stream)
+{
+    if (!y || (!r && !h) || (gate_form != Q4_GATE_NONE && !gate) || (h && h_dtype == Q4_MX4 && !h_scales))
+        return Q4_ERR_NULL;
+    if (!is_float(y_dtype) || ((residual || r) && !is_float(r_dtype)) ||
+        (h && !is_float(h_dtype) && h_dtype != Q4_MX4) || gate_form < Q4_GATE_NONE || gate_form > Q4_GATE_VALUE ||
+        (gate_form != Q4_GATE_NONE && !is_float(gate_dtype)))
+        return Q4_ERR_ENUM;
+    const bool mx4 = h && h_dtype == Q4_MX4;
+    if (M < 1 || H < 1 || M > (1 << 20) || H > Q4_NORM_MAX_H || (mx4 && H % 32 != 0))
+        return Q4_ERR_SHAPE;
+    if (!aligned(y, elem_align(y_dtype)) || ((residual || r) && (!aligned(residual, elem_align(r_dtype)) ||
+                                                                 !aligned(r, elem_align(r_dtype)))) ||
+        (gate_form != Q4_GATE_NONE && !aligned(gate, elem_align(gate_dtype))) ||
+        (mx4 ? !aligned(h, 16) || !aligned(h_scales, 4) : h && !aligned(h, elem_align(h_dtype))))
+        return Q4_ERR_ALIGN;
+    q4::NormArgs a{};
+    int st = check_norm(post, &a.post);
+    if (st == Q4_OK)
+        st = check_norm(pre, &a.pre);
+    if (st != Q4_OK)
+        return st;
+    a.y = y;
+    a.residual = residual;
+    a.gate = gate;
+    a.r = r;
+    a.h = h;
+    a.h_scales = mx4 ? (uint8_t *)h_scales : nullptr;
+    a.y_type = elem_kind(y_dtype);
+    a.r_type = elem_kind(r_dtype);
+    a.h_type = mx4 ? 0 : elem_kind(h_dtype);
+    a.gate_type = elem_kind(gate_dtype);
+    a.gate_form = gate_form;
+    a.scale = scale;
+    a.M = M;
+    a.H = H;
+    return hip_status(q4::launch_block_norm(a, (hipStream_t)stream));
 }
 
 size_t q4_moe_route_workspace_bytes(int M, int E, int K)

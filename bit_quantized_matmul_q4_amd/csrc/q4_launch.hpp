@@ -80,6 +80,43 @@ hipError_t launch_moe_layer(const void *x, int x_kind, const void *router, int r
                             int M, int E, int H, int I, int topk, int renormalize, void *workspace, hipStream_t stream);
 size_t moe_layer_workspace_bytes(int M, int E, int H, int I, int topk);
 
+// The microscaled 4-bit form and its product (q4_mx4.hip).  Element kinds as
+// above.
+// Dense rows [rows][K] -> codes and scale bytes (canonical or packed).
+hipError_t launch_mx4_quantize(const void *x, int kind, uint8_t *codes, uint8_t *scales, bool packed, int rows, int K,
+                               hipStream_t stream);
+// Canonical -> packed; packed -> values [rows][K].
+hipError_t launch_mx4_pack(const uint8_t *codes, const uint8_t *scales, uint8_t *packed, uint8_t *tiles, int rows,
+                           int K, hipStream_t stream);
+hipError_t launch_mx4_dequantize(const uint8_t *codes, const uint8_t *scales, void *y, int kind, int rows, int K,
+                                 hipStream_t stream);
+size_t mx4_code_bytes(int rows, int K);
+size_t mx4_scale_bytes(int rows, int K);
+// y = x . W^T; x_kind -1: x is packed codes with x_scales; 0 or 1: dense
+// rows, quantized in the call (the workspace holds mx4_workspace_bytes).
+hipError_t launch_mx4_linear(const void *x, int x_kind, const uint8_t *x_scales, const uint8_t *wq, const uint8_t *ws,
+                             void *y, int y_kind, int M, int N, int K, void *workspace, hipStream_t stream);
+size_t mx4_workspace_bytes(bool dense, int M, int N, int K);
+
+// The norms around a block (q4_norm.hip).  Types: element kinds as above.
+struct NormSide {
+    const void *weight, *bias;  // [H] of `type`, either may be NULL
+    int kind;                   // 0 none, 1 rms, 2 layer
+    int type;
+    float eps;
+};
+struct NormArgs {
+    const void *y, *residual, *gate;  // residual may be NULL
+    void *r, *h;                      // either may be NULL
+    uint8_t *h_scales;                // not NULL: h is packed microscaled 4-bit rows
+    NormSide post, pre;
+    int y_type, r_type, h_type, gate_type;
+    int gate_form;  // 0 none, 1 [H], 2 [M], 3 [M][H]
+    float scale;
+    int M, H;
+};
+hipError_t launch_block_norm(const NormArgs &args, hipStream_t stream);
+
 // Sizes of the tiled layout.
 size_t packed_code_bytes(int N, int K);
 size_t packed_scale_bytes(int N, int K);

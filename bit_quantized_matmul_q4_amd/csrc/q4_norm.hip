@@ -1,0 +1,389 @@
+// q4_norm.hip -- what stands between two linear layers of a block, in one
+// pass over the rows, for gfx950 (MI355X):
+//
+//     r[m] = residual[m] + scale gate[m] post(y[m])
+//     h[m] = pre(r[m])
+//
+// post and pre are norms (or none):
+//     rms    v / sqrt(mean(v^2) + eps) weight + bias
+//     layer  (v - mean(v)) / sqrt(mean((v - mean(v))^2) + eps) weight + bias
+// Everything between the loads and the stores is binary32: pre sees r before
+// it is rounded to its stored type, and h is rounded once, to a float type or
+// to the packed microscaled 4-bit form (q4_mx4_device.hpp).
+//
+// A workgroup owns a row and holds it in registers, eight neighbouring values
+// a lane and piece, so that every value is read and written once.  The shape
+// of the sums is a function of H alone: a row's bits depend on neither M nor
+// the row's place.  A sum of squares that leaves binary32's range is taken
+// again on values divided by a power of two (finite_row).
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "q4_launch.hpp"
+#include "q4_mx4_device.hpp"
+
+namespace q4 {
+
+namespace {
+
+using namespace mx4;
+
+// Sixteen bytes at any address of their elements' alignment.
+typedef u32x4 __attribute__((aligned(2))) u32x4_any;
+
+// Eight values as loaded: binary32 in both vectors, 16-bit types in the first.
+struct Raw {
+    u32x4 v[2];
+};
+
+// Values at .. at + 7 of an array of a type (0 binary16, 1 bfloat16, 2
+// binary32), those from `left` on zero.
+__device__ __forceinline__ Raw load8(const void *p, int kind, size_t at, int left)
+{
+    Raw r = {{{0, 0, 0, 0}, {0, 0, 0, 0}}};
+    if (left >= 8) {
+        if (kind == 2) {
+            r.v[0] = *(const u32x4_any *)((const float *)p + at);
+            r.v[1] = *(const u32x4_any *)((const float *)p + at + 4);
+        } else {
+            r.v[0] = *(const u32x4_any *)((const uint16_t *)p + at);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (i < left) {
+                if (kind == 2)
+                    r.v[i / 4][i % 4] = ((const uint32_t *)p)[at + i];
+                else
+                    r.v[0][i / 2] |= (uint32_t)((const uint16_t *)p)[at + i] << (16 * (i & 1));
+            }
+    }
+    return r;
+}
+
+__device__ __forceinline__ void values8(const Raw &r, int kind, float (&f)[8])
+{
+    if (kind == 2) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            f[i] = __builtin_bit_cast(float, (uint32_t)r.v[i / 4][i % 4]);
+    } else if (kind == 1) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            f[i] = __builtin_bit_cast(float, i & 1 ? r.v[0][i / 2] & 0xFFFF0000u : r.v[0][i / 2] << 16);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            f[i] = (float)__builtin_bit_cast(f16x2, (uint32_t)r.v[0][i / 2])[i & 1];
+    }
+}
+
+__device__ __forceinline__ void store8(void *p, int kind, size_t at, int left, const float (&f)[8])
+{
+    if (kind == 2) {
+        float *o = (float *)p + at;
+        if (left >= 8) {
+            u32x4 a, b;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                a[i] = __builtin_bit_cast(uint32_t, f[i]);
+                b[i] = __builtin_bit_cast(uint32_t, f[i + 4]);
+            }
+            *(u32x4_any *)o = a;
+            *(u32x4_any *)(o + 4) = b;
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (i < left)
+                    o[i] = f[i];
+        }
+        return;
+    }
+    uint16_t *o = (uint16_t *)p + at;
+    u32x4 w;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if (kind == 1)
+            w[i] = __builtin_bit_cast(uint32_t, (bf16x2){(__bf16)f[2 * i], (__bf16)f[2 * i + 1]});
+        else
+            w[i] = __builtin_bit_cast(uint32_t, (f16x2){(_Float16)f[2 * i], (_Float16)f[2 * i + 1]});
+    }
+    if (left >= 8) {
+        *(u32x4_any *)o = w;
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (i < left)
+                o[i] = (uint16_t)(w[i / 2] >> (16 * (i & 1)));
+    }
+}
+
+// Sum over the row's T threads, the same bits in each: pairs within a wave,
+// then the waves in order.  `part` belongs to this sum alone.
+template <int T>
+__device__ __forceinline__ float row_sum(float v, float *part)
+{
+#pragma unroll
+    for (int d = 1; d < 64; d *= 2)
+        v += __shfl_xor(v, d);
+    if constexpr (T > 64) {
+        if ((threadIdx.x & 63) == 0)
+            part[threadIdx.x >> 6] = v;
+        __syncthreads();
+        v = part[0];
+#pragma unroll
+        for (int w = 1; w < T / 64; ++w)
+            v += part[w];
+    }
+    return v;
+}
+
+template <int T>
+__device__ __forceinline__ float row_max(float v, float *part)
+{
+#pragma unroll
+    for (int d = 1; d < 64; d *= 2)
+        v = __builtin_fmaxf(v, __shfl_xor(v, d));
+    if constexpr (T > 64) {
+        if ((threadIdx.x & 63) == 0)
+            part[threadIdx.x >> 6] = v;
+        __syncthreads();
+        v = part[0];
+#pragma unroll
+        for (int w = 1; w < T / 64; ++w)
+            v = __builtin_fmaxf(v, part[w]);
+    }
+    return v;
+}
+
+constexpr int kMaxWaves = 16;
+constexpr int kNormSums = 5;  // sums and maxima of one norm
+typedef float Parts[kMaxWaves];
+
+// The row's mean (0 for rms) as a binary32 number and what that is off by, and
+// the mean square about both.  Values past H are zero and stay out of the sums.
+struct Moments {
+    float mean, rest, square;
+};
+
+template <int T, int C>
+__device__ __forceinline__ Moments moments(float (&v)[C][8], bool layer, int H, Parts *part)
+{
+    Moments m = {0.f, 0.f, 0.f};
+    const float over = 1.f / (float)H;
+    if (layer) {
+        float s = 0.f;
+#pragma unroll
+        for (int i = 0; i < C; ++i) {
+            const float *f = v[i];
+            s += ((f[0] + f[1]) + (f[2] + f[3])) + ((f[4] + f[5]) + (f[6] + f[7]));
+        }
+        m.mean = row_sum<T>(s, part[0]) * over;
+    }
+    float s = 0.f, left = 0.f;
+#pragma unroll
+    for (int i = 0; i < C; ++i) {
+        const int at = 8 * ((int)threadIdx.x + i * T);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const float d = at + e < H ? v[i][e] - m.mean : 0.f;
+            s = __builtin_fmaf(d, d, s);
+            left += d;
+        }
+    }
+    m.square = row_sum<T>(s, part[1]) * over;
+    if (layer) {
+        m.rest = row_sum<T>(left, part[2]) * over;
+        const float square = m.square - m.rest * m.rest;
+        m.square = square < 0.f ? 0.f : square;  // (NaN stays)
+    }
+    return m;
+}
+
+// v := the norm of v before weight and bias.  Where the sums leave binary32's
+// range (a value over 2^63 or so; or all so small that their squares vanish,
+// and eps no larger), the row is divided by the power of two of its largest
+// value first, and the root is taken in binary64.  Infinities and NaN take the
+// plain way: finite values over an infinite root are 0.
+template <int T, int C>
+__device__ __forceinline__ void normalize(float (&v)[C][8], int kind, float eps, int H, Parts *part)
+{
+    const bool layer = kind == 2;
+    Moments m = moments<T, C>(v, layer, H, part);
+    float inv = 1.f / __builtin_sqrtf(m.square + eps);
+    if (!(m.square < __builtin_inff()) || (m.square < 0x1p-80f && eps < 0x1p-40f)) {
+        float top = 0.f;
+        bool nan = false;
+#pragma unroll
+        for (int i = 0; i < C; ++i)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                top = __builtin_fmaxf(top, __builtin_fabsf(v[i][e]));
+                nan |= v[i][e] != v[i][e];
+            }
+        top = row_max<T>(nan ? __builtin_inff() : top, part[3]);
+        if (top > 0.f && top < __builtin_inff()) {
+            const int k = __builtin_amdgcn_frexp_expf(top);
+#pragma unroll
+            for (int i = 0; i < C; ++i)
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    v[i][e] = __builtin_ldexpf(v[i][e], -k);
+            __syncthreads();  // (the first sums are read)
+            m = moments<T, C>(v, layer, H, part);
+            inv = (float)(1.0 / __builtin_sqrt((double)m.square + __builtin_ldexp((double)eps, -2 * k)));
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < C; ++i)
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            v[i][e] = ((v[i][e] - m.mean) - m.rest) * inv;
+}
+
+template <int C>
+__device__ __forceinline__ void affine(float (&v)[C][8], const NormSide &n, int H, int T)
+{
+#pragma unroll
+    for (int i = 0; i < C; ++i) {
+        const int at = 8 * ((int)threadIdx.x + i * T);
+        if (at >= H)
+            continue;
+        if (n.weight) {
+            float w[8];
+            values8(load8(n.weight, n.type, at, H - at), n.type, w);
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                v[i][e] *= w[e];
+        }
+        if (n.bias) {
+            float b[8];
+            values8(load8(n.bias, n.type, at, H - at), n.type, b);
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                v[i][e] += b[e];
+        }
+    }
+}
+
+// One row a workgroup of T threads, C pieces of eight values a thread.
+template <int T, int C>
+__global__ __launch_bounds__(T) void q4_block_norm_kernel(const NormArgs a)
+{
+    __shared__ Parts part[2 * kNormSums];
+    const int H = a.H, tid = threadIdx.x;
+    const size_t row = blockIdx.x;
+    if (row >= (size_t)a.M) {  // a padding row of the packed form
+        for (int k = 8 * tid; k < mx4_groups(H) * 512; k += 8 * T) {
+            if (k < mx4_steps(H) * 128)
+                *(uint32_t *)((uint8_t *)a.h + mx4_code_at(row, k, H)) = 0;
+            if (k % 32 == 0)
+                a.h_scales[mx4_scale_at(row, k, H)] = 0;
+        }
+        return;
+    }
+    Raw ry[C], rr[C];
+#pragma unroll
+    for (int i = 0; i < C; ++i) {
+        const int at = 8 * (tid + i * T);
+        const size_t p = row * H + at;
+        ry[i] = load8(a.y, a.y_type, p, H - at);
+        rr[i] = a.residual ? load8(a.residual, a.r_type, p, H - at) : Raw{};
+    }
+    float v[C][8];
+#pragma unroll
+    for (int i = 0; i < C; ++i)
+        values8(ry[i], a.y_type, v[i]);
+    if (a.post.kind) {
+        normalize<T, C>(v, a.post.kind, a.post.eps, H, part);
+        affine<C>(v, a.post, H, T);
+    }
+    float row_gate = a.scale;
+    if (a.gate_form == 2) {
+        float g[8];
+        values8(load8(a.gate, a.gate_type, row, 1), a.gate_type, g);
+        row_gate *= g[0];
+    }
+#pragma unroll
+    for (int i = 0; i < C; ++i) {
+        const int at = 8 * (tid + i * T);
+        float f[8], g[8];
+        values8(rr[i], a.r_type, f);
+        if (a.gate_form & 1) {  // 1: a gate a channel, 3: one a value
+            values8(load8(a.gate, a.gate_type, a.gate_form == 1 ? at : row * H + at, H - at), a.gate_type, g);
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                g[e] *= row_gate;
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                g[e] = row_gate;
+        }
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            v[i][e] = at + e < H ? __builtin_fmaf(g[e], v[i][e], f[e]) : 0.f;
+        if (a.r && at < H)
+            store8(a.r, a.r_type, row * H + at, H - at, v[i]);
+    }
+    if (!a.h)
+        return;
+    if (a.pre.kind) {
+        normalize<T, C>(v, a.pre.kind, a.pre.eps, H, part + kNormSums);
+        affine<C>(v, a.pre, H, T);
+    }
+    if (!a.h_scales) {
+#pragma unroll
+        for (int i = 0; i < C; ++i) {
+            const int at = 8 * (tid + i * T);
+            if (at < H)
+                store8(a.h, a.h_type, row * H + at, H - at, v[i]);
+        }
+        return;
+    }
+    // the packed form: a block is a quad of lanes (H is a multiple of 32)
+#pragma unroll
+    for (int i = 0; i < C; ++i) {
+        const int k = 8 * (tid + i * T);
+        u32x4 bits[2];
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            bits[e / 4][e % 4] = __builtin_bit_cast(uint32_t, v[i][e]);
+        const uint32_t byte = scale_byte(top_of_quad(top8<2>(bits)));
+        if (k < H) {
+            *(uint32_t *)((uint8_t *)a.h + mx4_code_at(row, k, H)) = codes8<2>(bits, byte);
+            if (k % 32 == 0)
+                a.h_scales[mx4_scale_at(row, k, H)] = (uint8_t)byte;
+        }
+    }
+    for (int k = H + 8 * tid; k < mx4_groups(H) * 512; k += 8 * T) {
+        if (k < mx4_steps(H) * 128)
+            *(uint32_t *)((uint8_t *)a.h + mx4_code_at(row, k, H)) = 0;
+        if (k % 32 == 0)
+            a.h_scales[mx4_scale_at(row, k, H)] = 0;
+    }
+}
+
+}  // namespace
+
+hipError_t launch_block_norm(const NormArgs &a, hipStream_t stream)
+{
+    const int pieces = (a.H + 7) / 8;
+    const dim3 grid((unsigned)(a.h_scales ? (a.M + 15) / 16 * 16 : a.M));
+    if (pieces <= 64)
+        hipLaunchKernelGGL((q4_block_norm_kernel<64, 1>), grid, dim3(64), 0, stream, a);
+    else if (pieces <= 128)
+        hipLaunchKernelGGL((q4_block_norm_kernel<128, 1>), grid, dim3(128), 0, stream, a);
+    else if (pieces <= 256)
+        hipLaunchKernelGGL((q4_block_norm_kernel<256, 1>), grid, dim3(256), 0, stream, a);
+    else if (pieces <= 512)
+        hipLaunchKernelGGL((q4_block_norm_kernel<512, 1>), grid, dim3(512), 0, stream, a);
+    else if (pieces <= 1024)
+        hipLaunchKernelGGL((q4_block_norm_kernel<512, 2>), grid, dim3(512), 0, stream, a);
+    else if (pieces <= 2048)
+        hipLaunchKernelGGL((q4_block_norm_kernel<1024, 2>), grid, dim3(1024), 0, stream, a);
+    else
+        hipLaunchKernelGGL((q4_block_norm_kernel<1024, 4>), grid, dim3(1024), 0, stream, a);
+    return hipGetLastError();
+}
+
+}  // namespace q4

@@ -64,10 +64,10 @@ extern "C" {
 enum q4_status {
     Q4_OK = 0,
     Q4_ERR_NULL = -1,      /* a required pointer is NULL */
-    Q4_ERR_SHAPE = -2,     /* M < 1, N < 1, K < 32, K % 32 != 0, K > 2^25, topk not in 1 .. experts, or a size
-                              past what its call states or overflowing */
+    Q4_ERR_SHAPE = -2,     /* M < 1, N < 1, K < 32, K % 32 != 0, K > 2^25, topk not in 1 .. experts, a bad eps, or
+                              a size past what its call states or overflowing */
     Q4_ERR_ALIGN = -3,     /* a pointer below the alignment its call states */
-    Q4_ERR_ENUM = -4,      /* unknown dtype or kernel selector */
+    Q4_ERR_ENUM = -4,      /* unknown dtype, kernel selector, norm kind or gate form */
     Q4_ERR_HIP = -5,       /* a HIP call failed (see q4_last_hip_error) */
     Q4_ERR_WORKSPACE = -6, /* workspace_bytes non-zero with a NULL workspace, or (calls that need one) too small */
     Q4_ERR_SCRATCH = -7    /* the call needs more than Q4_SCRATCH_BYTES of scratch */
@@ -76,9 +76,11 @@ enum q4_status {
 /* Size of the fixed per-device scratch buffer q4_linear_noalloc uses. */
 #define Q4_SCRATCH_BYTES (4u << 20)
 
-/* Q4_F32: quantizer inputs, 8-bit outputs and router weights only; Q4_I8:
- * packed 8-bit rows as the x of q4_int8_linear only. */
-enum q4_dtype { Q4_F16 = 0, Q4_BF16 = 1, Q4_F32 = 2, Q4_I8 = 3 };
+/* Q4_F32: quantizer inputs, 8-bit and microscaled 4-bit outputs, router
+ * weights and q4_block_norm only; Q4_I8: packed 8-bit rows as the x of
+ * q4_int8_linear only; Q4_MX4: packed microscaled 4-bit rows as the x of
+ * q4_mx4_linear and the h of q4_block_norm only. */
+enum q4_dtype { Q4_F16 = 0, Q4_BF16 = 1, Q4_F32 = 2, Q4_I8 = 3, Q4_MX4 = 4 };
 
 enum q4_kernel {
     Q4_AUTO = 0, /* the crossover rule (see q4_get_crossover) picks the kernel */
@@ -354,6 +356,120 @@ size_t q4_moe_layer_workspace_bytes(int M, int E, int H, int I, int topk); /* 0 
 int q4_moe_layer(const void *x, int x_dtype, const void *router, int router_dtype, const float *bias, const void *W13,
                  const void *s13, const void *W2, const void *s2, float *y, int M, int E, int H, int I, int topk,
                  int renormalize, void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * The matrix product in microscaled 4-bit floating point, both operands in
+ * blocks of 32 along K with one power of two a block:
+ *
+ *     y[m][n] = sum_b 2^(ex[m][b] + ew[n][b]) sum_{k in b} cx[m][k] cw[n][k]
+ *
+ * A code is a sign, 2 exponent bits and 1 mantissa bit: bits 0..2 stand for
+ * 0, 0.5, 1, 1.5, 2, 3, 4, 6, bit 3 is the sign.  A scale is a byte E + 127
+ * for 2^E; 255 stands for NaN: every product with that block is NaN.  (The
+ * element and scale types of the Open Compute Project's microscaling formats,
+ * version 1.0, that it calls E2M1 and E8M0.)  K is a multiple of 32, at most
+ * Q4_MX4_MAX_K; rows and N are at most 2^24, rows N at most 2^36.
+ *
+ * The sum is binary32, one chain over steps of 128 k in order: a row's bits
+ * depend on that row and W alone (not on M, the row's place or the kernel).  A
+ * step's error is at most 2^-23 of the magnitudes that it adds.  A sum past
+ * binary32 becomes an infinity.
+ *
+ * Canonical form: codes [rows][K / 2] (even k in bits 0..3 of a byte, odd k in
+ * bits 4..7), scales [rows][K / 32], row-major.
+ * Packed form: codes in tiles of 16 rows by 128 k, order [ceil(rows/16)]
+ * [ceil(K/128)], 1024 bytes each: byte 16 (16 g + c) + j of tile (t, q) holds
+ * row 16 t + c, k = 128 q + 32 g + 2 j (bits 0..3) and the next k (bits 4..7).
+ * Scales in tiles of 16 rows by 512 k, order [ceil(rows/16)][ceil(K/512)], 256
+ * bytes each: byte 4 (16 g + c) + s of tile (t, q) is that of row 16 t + c and
+ * the block k = 512 q + 128 s + 32 g (c in 0..15, g and s in 0..3).  Entries
+ * past the rows or past K are zero.
+ *
+ * Quantizer, for each block: a = max |w|; E = max(floor(log2 a) - 2, -127) (the
+ * largest value lies in 4 .. 8 times 2^E); codes are w / 2^E rounded to the
+ * nearest, ties to the even code, what is over 6 to 6, signs kept (-0 too).  A
+ * block of zeros gets scale byte 0; one that holds an infinity or a NaN gets
+ * 255 and codes 0.
+ *   w        [rows][K], w_dtype Q4_F32, Q4_BF16 or Q4_F16; 16-byte aligned
+ *   codes, scales          canonical; codes 16-byte aligned
+ *   packed, packed_scales  q4_mx4_code_bytes / q4_mx4_scale_bytes(rows, K)
+ *                          bytes; 16-byte / 4-byte aligned
+ * q4_mx4_dequantize gives the values back, rounded to w_dtype (exact in Q4_F32
+ * up to 2^128, and in the type they were quantized from).
+ */
+#define Q4_MX4_MAX_K (1 << 17)
+size_t q4_mx4_code_bytes(int rows, int K);  /* 0 for a bad shape */
+size_t q4_mx4_scale_bytes(int rows, int K); /* 0 for a bad shape */
+int q4_mx4_quantize(const void *w, int w_dtype, uint8_t *codes, uint8_t *scales, int rows, int K, void *stream);
+int q4_mx4_quantize_pack(const void *w, int w_dtype, void *packed, void *packed_scales, int rows, int K, void *stream);
+int q4_mx4_pack(const uint8_t *codes, const uint8_t *scales, void *packed, void *packed_scales, int rows, int K,
+                void *stream);
+int q4_mx4_dequantize(const void *packed, const void *packed_scales, void *w, int w_dtype, int rows, int K,
+                      void *stream);
+
+/*
+ * The product.
+ *   x         x_dtype Q4_BF16 or Q4_F16: dense rows [M][K], quantized within
+ *             the call (the same codes and scales as q4_mx4_quantize_pack);
+ *             x_scales is not read.  x_dtype Q4_MX4: packed rows with their
+ *             packed x_scales, quantized once for several products (or written
+ *             by q4_block_norm).  16-byte aligned, packed scales 4-byte
+ *   Wq        packed rows of W, 16-byte aligned; w_scales packed, 4-byte
+ *   y         [M][N] row-major, y_dtype Q4_F32 (4-byte aligned), Q4_BF16 or
+ *             Q4_F16 (2-byte aligned; 16-byte alignment and N % 4 == 0 give
+ *             wider stores), overwritten
+ *   workspace device scratch of at least q4_mx4_workspace_bytes(M, N, K,
+ *             x_dtype) bytes, 256-byte aligned, as for q4_int8_linear
+ */
+size_t q4_mx4_workspace_bytes(int M, int N, int K, int x_dtype); /* 0 for a bad shape */
+int q4_mx4_linear(const void *x, int x_dtype, const void *x_scales, const void *Wq, const void *w_scales, void *y,
+                  int y_dtype, int M, int N, int K, void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * What stands between two linear layers of a model's block, for each row:
+ *
+ *     r = residual + scale gate post(y)
+ *     h = pre(r)
+ *
+ * y is a projection's output, post a norm after it (or none), residual the
+ * stream it goes to, pre the norm before the next projection (or none), h that
+ * projection's input.  Norms, with mean() over the row's H values:
+ *     Q4_NORM_RMS    v / sqrt(mean(v^2) + eps) weight + bias
+ *     Q4_NORM_LAYER  (v - mean(v)) / sqrt(mean((v - mean(v))^2) + eps) weight + bias
+ * Everything in between is binary32: r is rounded to its type once, and pre
+ * takes it unrounded; h is rounded once.  A row's bits depend on that row (and
+ * H) alone.  Sums of squares do not overflow or vanish where the result does
+ * not.  An infinity or NaN in a row makes that row's results what the formulas
+ * give, and no other row's.
+ *   y         y_dtype, [M][H]
+ *   post, pre NULL or kind Q4_NORM_NONE: no norm.  weight and bias of dtype
+ *             [H], either NULL (1, and 0)
+ *   gate      gate_dtype; gate_form Q4_GATE_NONE: 1 (gate is not read);
+ *             _CHANNEL: [H]; _ROW: [M]; _VALUE: [M][H]
+ *   residual  r_dtype, [M][H], or NULL: 0
+ *   r         r_dtype, [M][H], overwritten, or NULL: not stored.  It may be
+ *             the residual itself (all of it: the stream in place)
+ *   h         [M][H], overwritten, or NULL: not computed (not both r and h).
+ *             h_dtype Q4_MX4: packed rows for q4_mx4_linear with h_scales (the
+ *             bits of q4_mx4_quantize_pack on the Q4_F32 h), else h_scales is
+ *             not read
+ * Types are Q4_F32, Q4_BF16 or Q4_F16; pointers need their element's alignment
+ * (packed h 16 bytes, h_scales 4).  M <= 2^20, H <= Q4_NORM_MAX_H, a multiple
+ * of 32 for packed h; eps >= 0 and finite (Q4_ERR_SHAPE otherwise).
+ */
+#define Q4_NORM_MAX_H 32768
+enum q4_norm_kind { Q4_NORM_NONE = 0, Q4_NORM_RMS = 1, Q4_NORM_LAYER = 2 };
+enum q4_gate_form { Q4_GATE_NONE = 0, Q4_GATE_CHANNEL = 1, Q4_GATE_ROW = 2, Q4_GATE_VALUE = 3 };
+typedef struct q4_norm {
+    const void *weight;
+    const void *bias;
+    int kind;
+    int dtype;
+    float eps;
+} q4_norm;
+int q4_block_norm(const void *y, int y_dtype, const q4_norm *post, const void *gate, int gate_dtype, int gate_form,
+                  float scale, const void *residual, void *r, int r_dtype, const q4_norm *pre, void *h, int h_dtype,
+                  void *h_scales, int M, int H, void *stream);
 
 /* Bytes of the packed codes and packed scales of an N x K matrix (0 for a
  * bad shape).  Pure host computation.  (Library layout; pages silent.) */
