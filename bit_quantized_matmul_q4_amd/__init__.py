@@ -306,6 +306,7 @@ class Int8Matrix:
 
 
 _DTYPES = {torch.float32: _lib.Q4_F32, torch.bfloat16: _lib.Q4_BF16, torch.float16: _lib.Q4_F16}
+_FLOATS, _HALVES, _BYTES = tuple(_DTYPES), (torch.bfloat16, torch.float16), (torch.uint8,)
 
 
 def _int8_bytes(rows: int, K: int) -> int:
@@ -438,23 +439,30 @@ class Mx4Matrix:
         return self.codes.device
 
 
+def _mx4_bytes(rows: int, K: int):
+    """(q4_mx4_code_bytes, q4_mx4_scale_bytes), without the calls; (0, 0) for a bad shape."""
+    if not (1 <= rows <= 1 << 24 and 32 <= K <= 131072) or K % 32:
+        return 0, 0
+    tiles = (rows + 15) // 16
+    return 1024 * tiles * ((K + 127) // 128), 256 * tiles * ((K + 511) // 512)
+
+
 def _empty_mx4(rows: int, K: int, dev) -> Mx4Matrix:
-    lib = _lib.load()
-    n = lib.q4_mx4_code_bytes(rows, K)
-    if n == 0:
+    codes, scales = _mx4_bytes(rows, K)
+    if codes == 0:
         raise ValueError("bad shape %d x %d (K must be a positive multiple of 32, at most 131072)" % (rows, K))
-    return Mx4Matrix(torch.empty(n, dtype=torch.uint8, device=dev),
-                     torch.empty(lib.q4_mx4_scale_bytes(rows, K), dtype=torch.uint8, device=dev), rows, K)
+    return Mx4Matrix(torch.empty(codes, dtype=torch.uint8, device=dev),
+                     torch.empty(scales, dtype=torch.uint8, device=dev), rows, K)
 
 
 def _need_mx4(w, name: str, device=None):
     if not isinstance(w, Mx4Matrix):
         raise TypeError("%s must be an Mx4Matrix (see pack_mx4)" % name)
-    _need(w.codes, name + ".codes", (torch.uint8,), 1, device)
-    _need(w.scales, name + ".scales", (torch.uint8,), 1, w.codes.device)
-    tiles = -(-w.rows // 16)  # (q4_mx4_code_bytes and q4_mx4_scale_bytes, without the calls)
-    if (w.rows < 1 or w.K < 32 or w.K % 32 or w.codes.numel() != 1024 * tiles * -(-w.K // 128)
-            or w.scales.numel() != 256 * tiles * -(-w.K // 512)):
+    codes, scales = w.codes, w.scales
+    _need(codes, name + ".codes", _BYTES, 1, device)
+    _need(scales, name + ".scales", _BYTES, 1, codes.device)
+    c, s = _mx4_bytes(w.rows, w.K)
+    if c == 0 or codes.numel() != c or scales.numel() != s:
         raise ValueError("%s does not hold %d x %d packed codes and scales" % (name, w.rows, w.K))
 
 
@@ -468,7 +476,7 @@ def quantize_mx4(w: torch.Tensor):
     the even code.  A block with an infinity or NaN gets scale byte 255 (NaN)
     and codes 0 (include/q4.h)."""
     lib = _lib.load()
-    _need(w, "w", tuple(_DTYPES), 2)
+    _need(w, "w", _FLOATS, 2)
     R, K = w.shape
     codes = torch.empty((R, K // 2), dtype=torch.uint8, device=w.device)
     scales = torch.empty((R, K // 32), dtype=torch.uint8, device=w.device)
@@ -496,7 +504,7 @@ def quantize_pack_mx4(w: torch.Tensor) -> Mx4Matrix:
     """quantize_mx4() and pack_mx4() in one kernel: dense rows [R, K] ->
     Mx4Matrix (a weight, or activations for several ``linear_mx4`` calls)."""
     lib = _lib.load()
-    _need(w, "w", tuple(_DTYPES), 2)
+    _need(w, "w", _FLOATS, 2)
     R, K = w.shape
     m = _empty_mx4(R, K, w.device)
     _call(w.device, "q4_mx4_quantize_pack", lib.q4_mx4_quantize_pack, w.data_ptr(), _DTYPES[w.dtype],
@@ -515,7 +523,7 @@ def dequantize_mx4(m: Mx4Matrix, dtype: torch.dtype = torch.float32, out: torch.
             raise TypeError("dtype must be one of %s" % (tuple(_DTYPES),))
         out = torch.empty((m.rows, m.K), dtype=dtype, device=m.device)
     else:
-        _need_out(out, (m.rows, m.K), tuple(_DTYPES), m.device)
+        _need_out(out, (m.rows, m.K), _FLOATS, m.device)
     _call(m.device, "q4_mx4_dequantize", lib.q4_mx4_dequantize, m.codes.data_ptr(), m.scales.data_ptr(),
           out.data_ptr(), _DTYPES[out.dtype], m.rows, m.K)
     return out
@@ -535,14 +543,15 @@ def linear_mx4(x, w: Mx4Matrix, out: torch.Tensor | None = None, out_dtype: torc
     """
     lib = _lib.load()
     if not isinstance(x, Mx4Matrix):
-        _need(x, "x", (torch.bfloat16, torch.float16), 2)
+        _need(x, "x", _HALVES, 2)
         M, K = x.shape
         kind, x_ptr, xs_ptr = _DTYPES[x.dtype], x.data_ptr(), None
+        dev = x.device
     else:
         _need_mx4(x, "x")
         M, K = x.rows, x.K
         kind, x_ptr, xs_ptr = _lib.Q4_MX4, x.codes.data_ptr(), x.scales.data_ptr()
-    dev = x.device
+        dev = x.codes.device
     _need_mx4(w, "w", dev)
     N = w.rows
     if K != w.K:
@@ -552,8 +561,9 @@ def linear_mx4(x, w: Mx4Matrix, out: torch.Tensor | None = None, out_dtype: torc
             raise TypeError("out_dtype must be one of %s" % (tuple(_DTYPES),))
         out = torch.empty((M, N), dtype=out_dtype, device=dev)
     else:
-        _need_out(out, (M, N), tuple(_DTYPES), dev)
-    _keep, ws_ptr, ws_len = _workspace(workspace, lib.q4_mx4_workspace_bytes(M, N, K, kind), dev)
+        _need_out(out, (M, N), _FLOATS, dev)
+    need = 0 if xs_ptr is not None else lib.q4_mx4_workspace_bytes(M, N, K, kind)
+    _keep, ws_ptr, ws_len = _workspace(workspace, need, dev)
     _call(dev, "q4_mx4_linear", lib.q4_mx4_linear, x_ptr, kind, xs_ptr, w.codes.data_ptr(), w.scales.data_ptr(),
           out.data_ptr(), _DTYPES[out.dtype], M, N, K, ws_ptr, ws_len)
     return out
@@ -579,20 +589,27 @@ def _norm_side(n, name: str, H: int, dev):
         return None
     if not isinstance(n, Norm):
         raise TypeError("%s must be a Norm or None" % name)
-    if n.kind not in _NORMS:
+    kind = _NORMS.get(n.kind)
+    if kind is None:
         raise ValueError("%s.kind must be one of %s" % (name, sorted(_NORMS)))
-    kind = _lib.Q4_F32
-    for part, t in (("weight", n.weight), ("bias", n.bias)):
-        if t is None:
-            continue
-        _need(t, "%s.%s" % (name, part), tuple(_DTYPES), 1, dev)
-        if t.numel() != H:
-            raise ValueError("%s.%s must be [%d]" % (name, part, H))
-        if part == "bias" and n.weight is not None and t.dtype != n.weight.dtype:
+    weight, bias, dtype = n.weight, n.bias, _lib.Q4_F32
+    if weight is not None:
+        _need(weight, name + ".weight", _FLOATS, 1, dev)
+        if weight.numel() != H:
+            raise ValueError("%s.weight must be [%d]" % (name, H))
+        dtype = _DTYPES[weight.dtype]
+        weight_ptr = weight.data_ptr()
+    else:
+        weight_ptr = None
+    if bias is not None:
+        _need(bias, name + ".bias", _FLOATS, 1, dev)
+        if bias.numel() != H:
+            raise ValueError("%s.bias must be [%d]" % (name, H))
+        if weight is not None and bias.dtype != weight.dtype:
             raise TypeError("%s.weight and %s.bias must have one dtype" % (name, name))
-        kind = _DTYPES[t.dtype]
-    return _lib.NormSide(None if n.weight is None else n.weight.data_ptr(),
-                         None if n.bias is None else n.bias.data_ptr(), _NORMS[n.kind], kind, n.eps)
+        dtype = _DTYPES[bias.dtype]
+        return _lib.NormSide(weight_ptr, bias.data_ptr(), kind, dtype, n.eps)
+    return _lib.NormSide(weight_ptr, None, kind, dtype, n.eps)
 
 
 def block_norm(y: torch.Tensor, residual: torch.Tensor | None = None, post: Norm | None = None,
@@ -614,66 +631,67 @@ def block_norm(y: torch.Tensor, residual: torch.Tensor | None = None, post: Norm
     rounded.  A row's bits do not depend on the other rows (include/q4.h).
     """
     lib = _lib.load()
-    floats = tuple(_DTYPES)
-    _need(y, "y", floats, 2)
+    _need(y, "y", _FLOATS, 2)
     dev = y.device
-    M, H = y.shape
-    r_dtype = y.dtype
+    shape = y.shape
+    M, H = shape
+    res_ptr, like = None, y
     if residual is not None:
-        _need(residual, "residual", floats, 2, dev)
-        if residual.shape != y.shape:
+        _need(residual, "residual", _FLOATS, 2, dev)
+        if residual.shape != shape:
             raise ValueError("residual must be [%d, %d]" % (M, H))
-        r_dtype = residual.dtype
+        res_ptr, like = residual.data_ptr(), residual
+    r_dtype = like.dtype
     if r_out is None:
-        r_out = torch.empty((M, H), dtype=r_dtype, device=dev)
+        r_out = torch.empty_like(like)
     elif r_out is False:
         r_out = None
     else:
-        _need(r_out, "r_out", floats if residual is None else (r_dtype,), 2, dev)
-        if r_out.shape != y.shape:
+        _need(r_out, "r_out", _FLOATS if residual is None else (r_dtype,), 2, dev)
+        if r_out.shape != shape:
             raise ValueError("r_out must be [%d, %d]" % (M, H))
+        r_dtype = r_out.dtype
     gate_ptr, gate_kind, form = None, _lib.Q4_F32, _lib.Q4_GATE_NONE
     if gate is not None:
         if not isinstance(gate, torch.Tensor):
             raise TypeError("gate must be a torch.Tensor")
-        _need(gate, "gate", floats, 1 if gate.dim() == 1 else 2, dev)
-        shape = tuple(gate.shape)
-        if shape == (H,):
+        _need(gate, "gate", _FLOATS, 1 if gate.dim() == 1 else 2, dev)
+        if gate.shape == (H,):
             form = _lib.Q4_GATE_CHANNEL
-        elif shape == (M, H):
+        elif gate.shape == shape:
             form = _lib.Q4_GATE_VALUE
-        elif shape == (M, 1):
+        elif gate.shape == (M, 1):
             form = _lib.Q4_GATE_ROW
         else:
-            raise ValueError("gate must be [%d], [%d, 1] or [%d, %d], got %s" % (H, M, M, H, shape))
+            raise ValueError("gate must be [%d], [%d, 1] or [%d, %d], got %s" % (H, M, M, H, tuple(gate.shape)))
         gate_ptr, gate_kind = gate.data_ptr(), _DTYPES[gate.dtype]
     post, pre = _norm_side(post, "post", H, dev), _norm_side(pre, "pre", H, dev)
+    h_ptr, h_kind, hs_ptr = None, _lib.Q4_F32, None
     if out is False:
         out = None
         if r_out is None:
             raise ValueError("block_norm stores r, h or both")
-    elif out is None and out_dtype == "mx4":
-        out = _empty_mx4(M, H, dev)
-    elif out is None:
-        if out_dtype not in _DTYPES:
-            raise TypeError("out_dtype must be \"mx4\" or one of %s" % (floats,))
-        out = torch.empty((M, H), dtype=out_dtype, device=dev)
-    elif isinstance(out, Mx4Matrix):
-        _need_mx4(out, "out", dev)
-        if (out.rows, out.K) != (M, H):
-            raise ValueError("out must be %d x %d" % (M, H))
     else:
-        _need_out(out, (M, H), floats, dev)
-    if out is None:
-        h_ptr, h_kind, hs_ptr = None, _lib.Q4_F32, None
-    elif isinstance(out, Mx4Matrix):
-        h_ptr, h_kind, hs_ptr = out.codes.data_ptr(), _lib.Q4_MX4, out.scales.data_ptr()
-    else:
-        h_ptr, h_kind, hs_ptr = out.data_ptr(), _DTYPES[out.dtype], None
+        if out is None:
+            if out_dtype in _DTYPES:
+                out = torch.empty_like(y, dtype=out_dtype)
+            elif out_dtype == "mx4":
+                out = _empty_mx4(M, H, dev)
+            else:
+                raise TypeError("out_dtype must be \"mx4\" or one of %s" % (_FLOATS,))
+        elif isinstance(out, Mx4Matrix):
+            _need_mx4(out, "out", dev)
+            if (out.rows, out.K) != (M, H):
+                raise ValueError("out must be %d x %d" % (M, H))
+        else:
+            _need_out(out, (M, H), _FLOATS, dev)
+        if isinstance(out, Mx4Matrix):
+            h_ptr, h_kind, hs_ptr = out.codes.data_ptr(), _lib.Q4_MX4, out.scales.data_ptr()
+        else:
+            h_ptr, h_kind = out.data_ptr(), _DTYPES[out.dtype]
     _call(dev, "q4_block_norm", lib.q4_block_norm, y.data_ptr(), _DTYPES[y.dtype], post, gate_ptr, gate_kind, form,
-          scale, None if residual is None else residual.data_ptr(), None if r_out is None else r_out.data_ptr(),
-          _DTYPES[r_dtype if r_out is None else r_out.dtype], pre, h_ptr, h_kind,
-          hs_ptr, M, H)
+          scale, res_ptr, None if r_out is None else r_out.data_ptr(), _DTYPES[r_dtype], pre, h_ptr, h_kind, hs_ptr,
+          M, H)
     return r_out, out
 
 

@@ -37,7 +37,8 @@ struct Raw {
 };
 
 // Values at .. at + 7 of an array of a type (0 binary16, 1 bfloat16, 2
-// binary32), those from `left` on zero.
+// binary32), those from `left` on zero.  A row's last values come one by one,
+// all of them on their way at once.
 __device__ __forceinline__ Raw load8(const void *p, int kind, size_t at, int left)
 {
     Raw r = {{{0, 0, 0, 0}, {0, 0, 0, 0}}};
@@ -48,15 +49,23 @@ __device__ __forceinline__ Raw load8(const void *p, int kind, size_t at, int lef
         } else {
             r.v[0] = *(const u32x4_any *)((const uint16_t *)p + at);
         }
-    } else {
+    } else if (left > 0) {
+        uint32_t d[8];
+        if (kind == 2) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-            if (i < left) {
-                if (kind == 2)
-                    r.v[i / 4][i % 4] = ((const uint32_t *)p)[at + i];
-                else
-                    r.v[0][i / 2] |= (uint32_t)((const uint16_t *)p)[at + i] << (16 * (i & 1));
-            }
+            for (int i = 0; i < 8; ++i)
+                d[i] = ((const uint32_t *)p)[at + min(i, left - 1)];
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                r.v[i / 4][i % 4] = i < left ? d[i] : 0;
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                d[i] = ((const uint16_t *)p)[at + min(i, left - 1)];
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                r.v[0][i / 2] |= (i < left ? d[i] : 0) << (16 * (i & 1));
+        }
     }
     return r;
 }
@@ -118,47 +127,77 @@ __device__ __forceinline__ void store8(void *p, int kind, size_t at, int left, c
     }
 }
 
-// Sum over the row's T threads, the same bits in each: pairs within a wave,
-// then the waves in order.  `part` belongs to this sum alone.
-template <int T>
-__device__ __forceinline__ float row_sum(float v, float *part)
+// Sum of a wave's lanes, in every lane: neighbours within 16, then the four 16s.
+__device__ __forceinline__ float lanes(float v, int l)
 {
-#pragma unroll
-    for (int d = 1; d < 64; d *= 2)
-        v += __shfl_xor(v, d);
-    if constexpr (T > 64) {
-        if ((threadIdx.x & 63) == 0)
-            part[threadIdx.x >> 6] = v;
-        __syncthreads();
-        v = part[0];
-#pragma unroll
-        for (int w = 1; w < T / 64; ++w)
-            v += part[w];
-    }
-    return v;
+    return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), l));
+}
+template <int CTRL>
+__device__ __forceinline__ float moved(float v)
+{
+    return __builtin_bit_cast(float, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, v), CTRL, 0xF, 0xF, true));
+}
+__device__ __forceinline__ float wave_sum(float v)
+{
+    v += moved<0xB1>(v);   // lanes 1 0 3 2
+    v += moved<0x4E>(v);   // lanes 2 3 0 1
+    v += moved<0x141>(v);  // eight mirrored
+    v += moved<0x140>(v);  // sixteen mirrored
+    return (lanes(v, 0) + lanes(v, 16)) + (lanes(v, 32) + lanes(v, 48));
+}
+__device__ __forceinline__ float wave_max(float v)
+{
+    v = __builtin_fmaxf(v, moved<0xB1>(v));
+    v = __builtin_fmaxf(v, moved<0x4E>(v));
+    v = __builtin_fmaxf(v, moved<0x141>(v));
+    v = __builtin_fmaxf(v, moved<0x140>(v));
+    return __builtin_fmaxf(__builtin_fmaxf(lanes(v, 0), lanes(v, 16)), __builtin_fmaxf(lanes(v, 32), lanes(v, 48)));
 }
 
-template <int T>
-__device__ __forceinline__ float row_max(float v, float *part)
-{
-#pragma unroll
-    for (int d = 1; d < 64; d *= 2)
-        v = __builtin_fmaxf(v, __shfl_xor(v, d));
-    if constexpr (T > 64) {
-        if ((threadIdx.x & 63) == 0)
-            part[threadIdx.x >> 6] = v;
-        __syncthreads();
-        v = part[0];
-#pragma unroll
-        for (int w = 1; w < T / 64; ++w)
-            v = __builtin_fmaxf(v, part[w]);
-    }
-    return v;
-}
-
+// What the waves of a row pass to each other: each use has a place of its own,
+// so that one barrier is enough.
 constexpr int kMaxWaves = 16;
-constexpr int kNormSums = 5;  // sums and maxima of one norm
+constexpr int kNormSums = 4;  // sums and maxima of one norm
 typedef float Parts[kMaxWaves];
+
+// Sums over the row's T threads, the same bits in each: within the waves, then
+// the waves in order.
+template <int T, int N>
+__device__ __forceinline__ void row_sums(float (&v)[N], Parts *part)
+{
+#pragma unroll
+    for (int n = 0; n < N; ++n)
+        v[n] = wave_sum(v[n]);
+    if constexpr (T > 64) {
+        if ((threadIdx.x & 63) == 0)
+#pragma unroll
+            for (int n = 0; n < N; ++n)
+                part[n][threadIdx.x >> 6] = v[n];
+        __syncthreads();
+#pragma unroll
+        for (int n = 0; n < N; ++n) {
+            v[n] = part[n][0];
+#pragma unroll
+            for (int w = 1; w < T / 64; ++w)
+                v[n] += part[n][w];
+        }
+    }
+}
+template <int T>
+__device__ __forceinline__ float row_max(float v, Parts *part)
+{
+    v = wave_max(v);
+    if constexpr (T > 64) {
+        if ((threadIdx.x & 63) == 0)
+            part[0][threadIdx.x >> 6] = v;
+        __syncthreads();
+        v = part[0][0];
+#pragma unroll
+        for (int w = 1; w < T / 64; ++w)
+            v = __builtin_fmaxf(v, part[0][w]);
+    }
+    return v;
+}
 
 // The row's mean (0 for rms) as a binary32 number and what that is off by, and
 // the mean square about both.  Values past H are zero and stay out of the sums.
@@ -169,35 +208,37 @@ struct Moments {
 template <int T, int C>
 __device__ __forceinline__ Moments moments(float (&v)[C][8], bool layer, int H, Parts *part)
 {
-    Moments m = {0.f, 0.f, 0.f};
     const float over = 1.f / (float)H;
+    float mean = 0.f;
     if (layer) {
-        float s = 0.f;
+        float s[1] = {0.f};
 #pragma unroll
         for (int i = 0; i < C; ++i) {
             const float *f = v[i];
-            s += ((f[0] + f[1]) + (f[2] + f[3])) + ((f[4] + f[5]) + (f[6] + f[7]));
+            s[0] += ((f[0] + f[1]) + (f[2] + f[3])) + ((f[4] + f[5]) + (f[6] + f[7]));
         }
-        m.mean = row_sum<T>(s, part[0]) * over;
+        row_sums<T>(s, part);
+        mean = s[0] * over;
     }
-    float s = 0.f, left = 0.f;
+    float s[2] = {0.f, 0.f};  // of the squares and of what is left about the rounded mean
 #pragma unroll
     for (int i = 0; i < C; ++i) {
         const int at = 8 * ((int)threadIdx.x + i * T);
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-            const float d = at + e < H ? v[i][e] - m.mean : 0.f;
-            s = __builtin_fmaf(d, d, s);
-            left += d;
+            const float d = at + e < H ? v[i][e] - mean : 0.f;
+            s[0] = __builtin_fmaf(d, d, s[0]);
+            s[1] += d;
         }
     }
-    m.square = row_sum<T>(s, part[1]) * over;
-    if (layer) {
-        m.rest = row_sum<T>(left, part[2]) * over;
-        const float square = m.square - m.rest * m.rest;
-        m.square = square < 0.f ? 0.f : square;  // (NaN stays)
+    if (!layer) {
+        float q[1] = {s[0]};
+        row_sums<T>(q, part + 1);
+        return Moments{0.f, 0.f, q[0] * over};
     }
-    return m;
+    row_sums<T>(s, part + 1);
+    const float rest = s[1] * over, square = s[0] * over - rest * rest;
+    return Moments{mean, rest, square < 0.f ? 0.f : square};  // (NaN stays)
 }
 
 // v := the norm of v before weight and bias.  Where the sums leave binary32's
@@ -221,7 +262,7 @@ __device__ __forceinline__ void normalize(float (&v)[C][8], int kind, float eps,
                 top = __builtin_fmaxf(top, __builtin_fabsf(v[i][e]));
                 nan |= v[i][e] != v[i][e];
             }
-        top = row_max<T>(nan ? __builtin_inff() : top, part[3]);
+        top = row_max<T>(nan ? __builtin_inff() : top, part + 3);
         if (top > 0.f && top < __builtin_inff()) {
             const int k = __builtin_amdgcn_frexp_expf(top);
 #pragma unroll
@@ -241,27 +282,33 @@ __device__ __forceinline__ void normalize(float (&v)[C][8], int kind, float eps,
             v[i][e] = ((v[i][e] - m.mean) - m.rest) * inv;
 }
 
-template <int C>
-__device__ __forceinline__ void affine(float (&v)[C][8], const NormSide &n, int H, int T)
+// v := v weight + bias at the thread's pieces.
+template <int T, int C>
+__device__ __forceinline__ void affine(float (&v)[C][8], const NormSide &n, int H)
 {
+    Raw w[C], b[C];
 #pragma unroll
     for (int i = 0; i < C; ++i) {
         const int at = 8 * ((int)threadIdx.x + i * T);
-        if (at >= H)
-            continue;
+        if (n.weight)
+            w[i] = load8(n.weight, n.type, at, H - at);
+        if (n.bias)
+            b[i] = load8(n.bias, n.type, at, H - at);
+    }
+#pragma unroll
+    for (int i = 0; i < C; ++i) {
+        float f[8];
         if (n.weight) {
-            float w[8];
-            values8(load8(n.weight, n.type, at, H - at), n.type, w);
+            values8(w[i], n.type, f);
 #pragma unroll
             for (int e = 0; e < 8; ++e)
-                v[i][e] *= w[e];
+                v[i][e] *= f[e];
         }
         if (n.bias) {
-            float b[8];
-            values8(load8(n.bias, n.type, at, H - at), n.type, b);
+            values8(b[i], n.type, f);
 #pragma unroll
             for (int e = 0; e < 8; ++e)
-                v[i][e] += b[e];
+                v[i][e] += f[e];
         }
     }
 }
@@ -282,35 +329,62 @@ __global__ __launch_bounds__(T) void q4_block_norm_kernel(const NormArgs a)
         }
         return;
     }
-    Raw ry[C], rr[C];
+    // the row's own values are on their way before the first sum (of four pieces a
+    // thread y alone); weights, which all rows share, are loaded where they are
+    // needed: held in registers over the sums they left half as many waves, 4096 x
+    // 4864 in 77 us against 48
+    constexpr bool EARLY = C <= 2;
+    Raw y[C], residual[C], gate[C];
+    const auto load_rest = [&] {
+#pragma unroll
+        for (int i = 0; i < C; ++i) {
+            const int at = 8 * (tid + i * T);
+            if (a.residual)
+                residual[i] = load8(a.residual, a.r_type, row * H + at, H - at);
+            if (a.gate_form & 1)  // 1: a gate a channel, 3: one a value
+                gate[i] = load8(a.gate, a.gate_type, a.gate_form == 1 ? at : row * H + at, H - at);
+        }
+    };
 #pragma unroll
     for (int i = 0; i < C; ++i) {
         const int at = 8 * (tid + i * T);
-        const size_t p = row * H + at;
-        ry[i] = load8(a.y, a.y_type, p, H - at);
-        rr[i] = a.residual ? load8(a.residual, a.r_type, p, H - at) : Raw{};
+        y[i] = load8(a.y, a.y_type, row * H + at, H - at);
     }
+    if constexpr (EARLY)
+        load_rest();
+    Raw row_gate_bits = {};
+    if (a.gate_form == 2)
+        row_gate_bits = load8(a.gate, a.gate_type, row, 1);
+    const bool post = a.post.kind, pre = a.pre.kind && a.h;
     float v[C][8];
 #pragma unroll
     for (int i = 0; i < C; ++i)
-        values8(ry[i], a.y_type, v[i]);
-    if (a.post.kind) {
+        values8(y[i], a.y_type, v[i]);
+    if (post) {
         normalize<T, C>(v, a.post.kind, a.post.eps, H, part);
-        affine<C>(v, a.post, H, T);
+        affine<T, C>(v, a.post, H);
     }
+    if constexpr (!EARLY)
+        load_rest();
     float row_gate = a.scale;
     if (a.gate_form == 2) {
         float g[8];
-        values8(load8(a.gate, a.gate_type, row, 1), a.gate_type, g);
+        values8(row_gate_bits, a.gate_type, g);
         row_gate *= g[0];
     }
 #pragma unroll
     for (int i = 0; i < C; ++i) {
         const int at = 8 * (tid + i * T);
         float f[8], g[8];
-        values8(rr[i], a.r_type, f);
-        if (a.gate_form & 1) {  // 1: a gate a channel, 3: one a value
-            values8(load8(a.gate, a.gate_type, a.gate_form == 1 ? at : row * H + at, H - at), a.gate_type, g);
+        if (a.residual) {
+            values8(residual[i], a.r_type, f);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                f[e] = 0.f;
+        }
+        if (a.gate_form & 1) {
+            values8(gate[i], a.gate_type, g);
 #pragma unroll
             for (int e = 0; e < 8; ++e)
                 g[e] *= row_gate;
@@ -327,9 +401,9 @@ __global__ __launch_bounds__(T) void q4_block_norm_kernel(const NormArgs a)
     }
     if (!a.h)
         return;
-    if (a.pre.kind) {
+    if (pre) {
         normalize<T, C>(v, a.pre.kind, a.pre.eps, H, part + kNormSums);
-        affine<C>(v, a.pre, H, T);
+        affine<T, C>(v, a.pre, H);
     }
     if (!a.h_scales) {
 #pragma unroll
@@ -367,22 +441,36 @@ __global__ __launch_bounds__(T) void q4_block_norm_kernel(const NormArgs a)
 
 hipError_t launch_block_norm(const NormArgs &a, hipStream_t stream)
 {
-    const int pieces = (a.H + 7) / 8;
+    const int pieces = (a.H + 7) / 8, waves = (pieces + 63) / 64;
     const dim3 grid((unsigned)(a.h_scales ? (a.M + 15) / 16 * 16 : a.M));
-    if (pieces <= 64)
-        hipLaunchKernelGGL((q4_block_norm_kernel<64, 1>), grid, dim3(64), 0, stream, a);
-    else if (pieces <= 128)
-        hipLaunchKernelGGL((q4_block_norm_kernel<128, 1>), grid, dim3(128), 0, stream, a);
-    else if (pieces <= 256)
-        hipLaunchKernelGGL((q4_block_norm_kernel<256, 1>), grid, dim3(256), 0, stream, a);
-    else if (pieces <= 512)
-        hipLaunchKernelGGL((q4_block_norm_kernel<512, 1>), grid, dim3(512), 0, stream, a);
-    else if (pieces <= 1024)
-        hipLaunchKernelGGL((q4_block_norm_kernel<512, 2>), grid, dim3(512), 0, stream, a);
-    else if (pieces <= 2048)
-        hipLaunchKernelGGL((q4_block_norm_kernel<1024, 2>), grid, dim3(1024), 0, stream, a);
+    const auto go = [&](auto kernel, int threads) { hipLaunchKernelGGL(kernel, grid, dim3(threads), 0, stream, a); };
+    // one piece a thread up to 8192 values, in whole waves
+    if (waves <= 1)
+        go(q4_block_norm_kernel<64, 1>, 64);
+    else if (waves <= 2)
+        go(q4_block_norm_kernel<128, 1>, 128);
+    else if (waves <= 3)
+        go(q4_block_norm_kernel<192, 1>, 192);
+    else if (waves <= 4)
+        go(q4_block_norm_kernel<256, 1>, 256);
+    else if (waves <= 5)
+        go(q4_block_norm_kernel<320, 1>, 320);
+    else if (waves <= 6)
+        go(q4_block_norm_kernel<384, 1>, 384);
+    else if (waves <= 7)
+        go(q4_block_norm_kernel<448, 1>, 448);
+    else if (waves <= 8)
+        go(q4_block_norm_kernel<512, 1>, 512);
+    else if (waves <= 10)
+        go(q4_block_norm_kernel<640, 1>, 640);
+    else if (waves <= 12)
+        go(q4_block_norm_kernel<768, 1>, 768);
+    else if (waves <= 16)
+        go(q4_block_norm_kernel<1024, 1>, 1024);
+    else if (waves <= 32)
+        go(q4_block_norm_kernel<1024, 2>, 1024);
     else
-        hipLaunchKernelGGL((q4_block_norm_kernel<1024, 4>), grid, dim3(1024), 0, stream, a);
+        go(q4_block_norm_kernel<1024, 4>, 1024);
     return hipGetLastError();
 }
 
