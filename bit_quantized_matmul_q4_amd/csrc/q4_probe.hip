@@ -27,6 +27,7 @@
 #include "q4_device.hpp"
 #include "q4_int8_plan.hpp"
 #include "q4_moe_plan.hpp"
+#include "q4_mx4_plan.hpp"
 
 namespace {
 
@@ -322,6 +323,16 @@ int q4probe_int8_form(int dense, int M, int N, int K, int *form)
     form[3] = s.bn;
     form[4] = s.split;
     form[5] = q4::quant_rows(M);
+    return 0;
+}
+
+// The same for the microscaled 4-bit product: {quantized within the product,
+// kernel}.
+int q4probe_mx4_form(int dense, int M, int N, int K, int *form)
+{
+    const q4::Mx4Shape s = q4::mx4_shape(dense != 0, M, N, K);
+    form[0] = s.fused;
+    form[1] = (int)s.kernel;
     return 0;
 }
 
