@@ -186,6 +186,8 @@ def load(path: str | None = None):
     global _lib
     if path is not None:
         return _open(path)
+    if _lib is not None:  # (set once)
+        return _lib
     with _lock:
         if _lib is None:
             if not os.path.exists(LIB_PATH):
