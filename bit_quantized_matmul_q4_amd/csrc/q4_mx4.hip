@@ -41,6 +41,9 @@ typedef int i32x8 __attribute__((ext_vector_type(8)));
 // A workgroup takes 16 rows by 512 k, a wave four of the rows: 16 lanes a row
 // and step of 128 k, eight values a lane, so that a block is a quad of lanes.
 // A lane with the first part of a block ends with its bytes of four steps.
+// Bound by the reads: 18944 x 3584 packed from binary32 in 57.6 us (5.3 TB/s read
+// and written), from bfloat16 in 34.5 (5.0).  Binary32 in whole lines a load
+// (four values a lane, a block eight lanes) took 57.7.
 // PACKED: the packed form (padding written), else codes [rows][K / 2] and
 // scales [rows][K / 32].
 template <int KIND, bool PACKED>
@@ -87,7 +90,8 @@ __global__ __launch_bounds__(256) void q4_mx4_quantize_kernel(const void *__rest
 }
 
 // Canonical codes [rows][K / 2] and scales [rows][K / 32] -> packed; a wave
-// one row tile by 512 k.
+// one row tile by 512 k.  18944 x 3584 in 14.5 us (5.0 TB/s read and written;
+// with stores that are to be kept 20.7).
 __global__ __launch_bounds__(256) void q4_mx4_pack_kernel(const uint8_t *__restrict__ codes,
                                                           const uint8_t *__restrict__ scales,
                                                           uint8_t *__restrict__ packed, uint8_t *__restrict__ tiles,
@@ -108,7 +112,7 @@ __global__ __launch_bounds__(256) void q4_mx4_pack_kernel(const uint8_t *__restr
                 bytes |= (uint32_t)scales[row * (K / 32) + k / 32] << (8 * s);
             }
             if (step < steps)
-                *(u32x4 *)(packed + (tile * steps + step) * 1024 + 16 * lane) = v;
+                __builtin_nontemporal_store(v, (u32x4 *)(packed + (tile * steps + step) * 1024 + 16 * lane));
         }
         *(uint32_t *)(tiles + (size_t)unit * 256 + 4 * lane) = bytes;
     }
@@ -134,14 +138,20 @@ __device__ __forceinline__ float code_value(uint32_t code, uint32_t byte)
     return byte == 255 ? __builtin_nanf("") : code & 8 ? -v : v;
 }
 
-// Packed -> values [rows][K], the quantizer's lanes.
+// Packed -> values [rows][K]: 16 lanes a row and step of 128 k, as the
+// quantizer, 16 bytes a lane and store, so that a store fills whole lines.  Bound
+// by the stores, which are marked as not to be kept: 18944 x 3584 to bfloat16
+// took 43 us with ordinary ones, 33 so (5.2 TB/s); to binary32, with a lane's
+// eight values in two stores of which each fills half of every line, 79 and 109
+// us, in whole lines 50 (6.1 TB/s).
 template <int KIND>
 __global__ __launch_bounds__(256) void q4_mx4_dequantize_kernel(const uint8_t *__restrict__ codes,
                                                                 const uint8_t *__restrict__ scales,
                                                                 void *__restrict__ y, int rows, int K, unsigned units)
 {
-    constexpr int SIZE = KIND == 2 ? 4 : 2;
-    const int lane = threadIdx.x & 63, p = lane & 15, g = p >> 2;
+    constexpr int SIZE = KIND == 2 ? 4 : 2, PER = 16 / SIZE, PARTS = 8 / PER;  // values a store, stores a step
+    typedef std::conditional_t<KIND == 2, uint16_t, uint32_t> Codes;           // PER of them
+    const int lane = threadIdx.x & 63, p = lane & 15;
     const int groups = mx4_groups(K), steps = mx4_steps(K);
     const int c = (threadIdx.x >> 6) * 4 + (lane >> 4);
     for (unsigned unit = blockIdx.x; unit < units; unit += gridDim.x) {
@@ -149,37 +159,37 @@ __global__ __launch_bounds__(256) void q4_mx4_dequantize_kernel(const uint8_t *_
         const int group = (int)(unit % groups);
         if (row >= (size_t)rows)
             continue;
-        const uint32_t bytes = *(const uint32_t *)(scales + (size_t)unit * 256 + 64 * g + 4 * c);
-        uint32_t w[4];
+        uint32_t bytes[PARTS], w[4][PARTS];
 #pragma unroll
-        for (int s = 0; s < 4; ++s) {
-            const int step = 4 * group + s;
-            w[s] = step < steps
-                       ? *(const uint32_t *)(codes + (tile * steps + step) * 1024 + 256 * g + 16 * c + 4 * (p & 3))
-                       : 0;
-        }
+        for (int i = 0; i < PARTS; ++i) {
+            const int k = PER * (16 * i + p);  // in its step
+            bytes[i] = *(const uint32_t *)(scales + (size_t)unit * 256 + k / 32 * 64 + 4 * c);
 #pragma unroll
-        for (int s = 0; s < 4; ++s) {
-            const int k = 512 * group + 128 * s + 8 * p;
-            if (k >= K)
-                continue;
-            float f[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-                f[i] = code_value((w[s] >> (4 * i)) & 15, (bytes >> (8 * s)) & 255);
-            char *out = (char *)y + (row * K + k) * SIZE;
-            if constexpr (KIND == 2) {
-                *(f32x4 *)out = (f32x4){f[0], f[1], f[2], f[3]};
-                *((f32x4 *)out + 1) = (f32x4){f[4], f[5], f[6], f[7]};
-            } else {
-                u32x4 o;
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    o[i] = KIND == 1 ? bf16_bits(f[2 * i]) | bf16_bits(f[2 * i + 1]) << 16
-                                     : f16_bits(f[2 * i]) | f16_bits(f[2 * i + 1]) << 16;
-                *(u32x4 *)out = o;
+            for (int s = 0; s < 4; ++s) {
+                const int step = min(4 * group + s, steps - 1);
+                w[s][i] =
+                    *(const Codes *)(codes + (tile * steps + step) * 1024 + k / 32 * 256 + 16 * c + k % 32 / 2);
             }
         }
+#pragma unroll
+        for (int s = 0; s < 4; ++s)
+#pragma unroll
+            for (int i = 0; i < PARTS; ++i) {
+                const int k = 512 * group + 128 * s + PER * (16 * i + p);
+                if (k >= K)
+                    continue;
+                float f[PER];
+#pragma unroll
+                for (int e = 0; e < PER; ++e)
+                    f[e] = code_value((w[s][i] >> (4 * e)) & 15, (bytes[i] >> (8 * s)) & 255);
+                u32x4 o;
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    o[e] = KIND == 2   ? __builtin_bit_cast(uint32_t, f[e])
+                           : KIND == 1 ? bf16_bits(f[2 * e % PER]) | bf16_bits(f[(2 * e + 1) % PER]) << 16
+                                       : f16_bits(f[2 * e % PER]) | f16_bits(f[(2 * e + 1) % PER]) << 16;
+                __builtin_nontemporal_store(o, (u32x4 *)((char *)y + (row * K + k) * SIZE));
+            }
     }
 }
 
