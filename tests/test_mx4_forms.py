@@ -18,7 +18,8 @@ def probe():
 def test_shapes_take_their_form(form):
     for M, N, K in FORMS[form]:
         assert form_of(True, M, N, K) == form, (M, N, K)
-        assert form_of(False, M, N, K) == form.replace("/q", ""), (M, N, K)
+        packed = form_of(False, M, N, K)  # (the relay loads packed rows beside W, and is faster up to more columns)
+        assert packed == form.replace("/q", "") or (form, packed) == ("wide/q", "relay"), (M, N, K)
 
 
 def test_every_form_is_named():
