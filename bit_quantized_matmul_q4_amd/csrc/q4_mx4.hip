@@ -739,11 +739,14 @@ __global__ __launch_bounds__(256, 2) void q4_mx4_gemm_kernel(
     // step's pieces of x (and the next group's scale bytes), and let this step's
     // place go.  The scale bytes' place is read at a group's start and filled again
     // after its first step.  Loads and reads stand between the products, which go
-    // on meanwhile.  (Past the last step: what is read is not used.)
-    const auto step = [&](auto u, int s) {
+    // on meanwhile.  (Past the last step: what is read is not used.)  END, the
+    // steps after the last whole group: no step is three later, W has arrived or is on
+    // its way, and none of its loads counts (loads that nothing uses are not there).
+    const auto step = [&](auto u, auto end, int s) {
         constexpr int U = u.value;
+        constexpr bool END = end.value;
         asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-        wait_loads<PER + TN + (U == 1 || U == 2 ? SC : 0)>();
+        wait_loads<PER + (END ? 0 : TN) + (U == 1 || U == 2 ? SC : 0)>();
         __builtin_amdgcn_s_barrier();
         asm volatile("" ::: "memory");
         from = from + STAGE == NS * STAGE ? 0 : from + STAGE;
@@ -760,9 +763,9 @@ __global__ __launch_bounds__(256, 2) void q4_mx4_gemm_kernel(
                 if (j < TN)
                     sw_next[j] = read_ws(j);
             }
-            if (j < TN)
+            if (j < TN && !END)
                 load_w((U + AHEAD) & 3, j, s + AHEAD);
-            else if (j - TN < PER)
+            else if (j >= TN && j - TN < PER)
                 fetch(j - TN);
             if (U == 0 && j == TM - 1)
                 fetch_scales();
@@ -782,17 +785,17 @@ __global__ __launch_bounds__(256, 2) void q4_mx4_gemm_kernel(
     int s = 0;
 #pragma clang loop unroll(disable)
     for (; s + 4 <= steps; s += 4) {  // (no branch: the compiler counts the loads in flight)
-        step(I0{}, s);
-        step(I1{}, s + 1);
-        step(I2{}, s + 2);
-        step(I3{}, s + 3);
+        step(I0{}, std::false_type{}, s);
+        step(I1{}, std::false_type{}, s + 1);
+        step(I2{}, std::false_type{}, s + 2);
+        step(I3{}, std::false_type{}, s + 3);
     }
     if (s < steps) {
-        step(I0{}, s);
+        step(I0{}, std::true_type{}, s);
         if (s + 1 < steps)
-            step(I1{}, s + 1);
+            step(I1{}, std::true_type{}, s + 1);
         if (s + 2 < steps)
-            step(I2{}, s + 2);
+            step(I2{}, std::true_type{}, s + 2);
     }
     // (what was loaded past the end is in place before LDS holds outputs)
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
@@ -948,19 +951,26 @@ __global__ __launch_bounds__(64 * WN) void q4_mx4_mid_kernel(
     asm volatile("" ::: "memory");
     read_x(0, 0);
     read_xs(0);
-    const auto group = [&](auto buf, auto other, int q) {
+    // END, the groups from which none is A later: no loads of W, and none of them
+    // counts (loads that nothing uses are not there)
+    const auto group = [&](auto buf, auto other, auto end, int q) {
+        constexpr bool END = end.value;
+        const auto load = [&](auto u) {
+            if constexpr (!END)
+                load_w(buf, u, q + A);
+        };
         read_x(1, 1);
         multiply(buf, I0{});
-        load_w(buf, I0{}, q + A);
+        load(I0{});
         read_x(0, 2);
         multiply(buf, I1{});
-        load_w(buf, I1{}, q + A);
+        load(I1{});
         read_x(1, 3);
         multiply(buf, I2{});
-        load_w(buf, I2{}, q + A);
+        load(I2{});
         // every wave is done with this group's place, and the next group is here
         asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-        wait_loads<(NS - 2) * (PER + SC + 5 * TN) + 5 * TN>();
+        wait_loads<(NS - 2) * (PER + SC) + (END ? 0 : (NS - 1) * 5 * TN)>();
         __builtin_amdgcn_s_barrier();
         asm volatile("" ::: "memory");
         fetch(q + NS);
@@ -968,8 +978,9 @@ __global__ __launch_bounds__(64 * WN) void q4_mx4_mid_kernel(
         read_x(0, 0);
         read_xs(other.value & 1);
         multiply(buf, I3{});
-        load_w(buf, I3{}, q + A);
-        load_ws(buf, q + A);
+        load(I3{});
+        if constexpr (!END)
+            load_ws(buf, q + A);
     };
     const auto last = [&](auto buf, int q) {  // of one to four steps
         read_x(1, 1);
@@ -986,11 +997,11 @@ __global__ __launch_bounds__(64 * WN) void q4_mx4_mid_kernel(
     int q = 0;
 #pragma clang loop unroll(disable)
     for (; q + A < groups; q += A) {  // (no branch: the compiler counts the loads in flight)
-        group(I0{}, I1{}, q);
-        group(I1{}, std::integral_constant<int, 2 % A>{}, q + 1);
+        group(I0{}, I1{}, std::false_type{}, q);
+        group(I1{}, std::integral_constant<int, 2 % A>{}, std::false_type{}, q + 1);
         if constexpr (A == 4) {
-            group(I2{}, I3{}, q + 2);
-            group(I3{}, I0{}, q + 3);
+            group(I2{}, I3{}, std::false_type{}, q + 2);
+            group(I3{}, I0{}, std::false_type{}, q + 3);
         }
     }
     const auto end = [&](auto buf, auto other) {  // false: the last group
@@ -998,7 +1009,7 @@ __global__ __launch_bounds__(64 * WN) void q4_mx4_mid_kernel(
             last(buf, q + buf.value);
             return false;
         }
-        group(buf, other, q + buf.value);
+        group(buf, other, std::true_type{}, q + buf.value);
         return true;
     };
     if (end(I0{}, I1{}) && end(I1{}, std::integral_constant<int, 2 % A>{})) {

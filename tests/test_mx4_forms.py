@@ -42,3 +42,14 @@ def test_groups_and_last_steps_are_covered():
         assert 1 in groups and {g % 2 for g in groups} == {0, 1}, (form, groups)
         last = {(-(-K // 128) - 1) % 4 + 1 for _, _, K in shapes}
         assert last == {1, 2, 3, 4}, (form, last)
+
+
+def test_last_steps_after_several_groups_are_covered():
+    """And one to four steps in the last group where whole groups come before it, in odd and even numbers."""
+    for form, shapes in FORMS.items():
+        if "x" not in form:
+            continue
+        met = {(min(-(-K // 512), 4), (-(-K // 128) - 1) % 4 + 1) for _, _, K in shapes if K > 512}
+        assert {last for _, last in met} == {1, 2, 3, 4}, (form, met)
+        assert {last for groups, last in met if groups >= 3} == {1, 2, 3, 4}, (form, met)
+
