@@ -2,6 +2,8 @@
 the kernel they take (tests/mx4_forms.py; the rule itself is checked on the
 CPU), with the bounds of test_mx4_gpu.py; and the form at the largest rows,
 columns and lengths that the library takes."""
+import random
+
 import pytest
 import torch
 
@@ -95,6 +97,33 @@ def test_not_a_number_stays_in_its_row_and_column(form, shape):
     want[M - 1] = True
     want[:, 0::64] = True
     assert torch.equal(y, want)
+
+
+def at_random(seed):
+    """A shape over the whole range (the logarithm of each size spread evenly), products of 8e10 at most."""
+    rng = random.Random(seed)
+    while True:
+        M, N, K = (int(round(2 ** rng.uniform(0, top))) for top in (12, 15.5, 9.6))
+        if 1 << 20 <= M * N * 32 * K <= 8e10:
+            return M, N, 32 * K
+
+
+@pytest.mark.parametrize("seed", range(96))
+def test_shapes_at_random(seed):
+    """Against the sums in 64 bits; the same bits from packed rows, from a row alone and from a second call."""
+    M, N, K = at_random(seed)
+    yt = ("f32", "bf16", "f16")[seed % 3]
+    gu.note("linear_mx4 M=%d N=%d K=%d -> %s: %s" % (M, N, K, yt, form_of(True, M, N, K)))
+    x = torch.randn(M, K, device=gu.DEV, generator=cuda_gen(seed)).to(DTYPES["f16" if seed & 1 else "bf16"])
+    xq = q4.quantize_pack_mx4(x)
+    w = q4.quantize_pack_mx4(torch.randn(N, K, device=gu.DEV, generator=cuda_gen(seed + 1000)) / K ** 0.5)
+    y = q4.linear_mx4(x, w, out_dtype=DTYPES[yt])
+    m = seed % M
+    for what, other, of in (("again", q4.linear_mx4(x, w, out_dtype=DTYPES[yt]), y),
+                            ("packed", q4.linear_mx4(xq, w, out_dtype=DTYPES[yt]), y),
+                            ("a row", q4.linear_mx4(x[m:m + 1].contiguous(), w, out_dtype=DTYPES[yt]), y[m:m + 1])):
+        assert torch.equal(other, of), what
+    check_on_gpu(y, q4.dequantize_mx4(xq).double(), q4.dequantize_mx4(w).double(), yt, (M, N, K))
 
 
 # ---------------------------------------------------------------- the limits
