@@ -99,6 +99,31 @@ def test_not_a_number_stays_in_its_row_and_column(form, shape):
     assert torch.equal(y, want)
 
 
+@pytest.mark.parametrize("form,shape", [(f, s[-1]) for f, s in FORMS.items()], ids=list(FORMS))
+def test_captured_beside_another_stream(form, shape):
+    """Replays of a captured call on new inputs, while another stream runs the same shape; each against an eager call."""
+    M, N, K = shape
+    gu.note("linear_mx4 captured, two streams, %s M=%d N=%d K=%d" % (form, M, N, K))
+    w = q4.quantize_pack_mx4(torch.randn(N, K, device=gu.DEV, generator=cuda_gen(1)) / K ** 0.5)
+    xs = [torch.randn(M, K, device=gu.DEV, generator=cuda_gen(2 + i)).bfloat16() for i in range(4)]
+    want = [q4.linear_mx4(x, w) for x in xs]
+    x = xs[0].clone()
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        y = q4.linear_mx4(x, w)
+    other = torch.cuda.Stream()
+    for i in (1, 2, 3, 0):
+        x.copy_(xs[i])
+        torch.cuda.synchronize()
+        graph.replay()
+        with torch.cuda.stream(other):
+            beside = [q4.linear_mx4(xs[j], w) for j in (i - 1, i)]
+        torch.cuda.synchronize()
+        assert torch.equal(y, want[i])
+        assert torch.equal(beside[0], want[i - 1]) and torch.equal(beside[1], want[i])
+
+
 def at_random(seed):
     """A shape over the whole range (the logarithm of each size spread evenly), products of 8e10 at most."""
     rng = random.Random(seed)
