@@ -627,8 +627,9 @@ def block_norm(y: torch.Tensor, residual: torch.Tensor | None = None, post: Norm
     the stream in place.  h: ``out_dtype`` float32, bfloat16 or float16
     (``out``'s own if given), or "mx4" for an Mx4Matrix that ``linear_mx4``
     takes.  ``r_out=False`` or ``out=False``: that one is not stored (and None).
-    Sums and everything in between are float32; pre takes r before it is
-    rounded.  A row's bits do not depend on the other rows (include/q4.h).
+    Sums and everything in between are float32 (the mean's sum of a layer norm
+    float64); pre takes r before it is rounded.  A row's bits do not depend on
+    the other rows (include/q4.h).
     """
     lib = _lib.load()
     _need(y, "y", _FLOATS, 2)

@@ -7,9 +7,10 @@
 // post and pre are norms (or none):
 //     rms    v / sqrt(mean(v^2) + eps) weight + bias
 //     layer  (v - mean(v)) / sqrt(mean((v - mean(v))^2) + eps) weight + bias
-// Everything between the loads and the stores is binary32: pre sees r before
-// it is rounded to its stored type, and h is rounded once, to a float type or
-// to the packed microscaled 4-bit form (q4_mx4_device.hpp).
+// Everything between the loads and the stores is binary32 (a mean's sum
+// binary64): pre sees r before it is rounded to its stored type, and h is
+// rounded once, to a float type or to the packed microscaled 4-bit form
+// (q4_mx4_device.hpp).
 //
 // A workgroup owns a row and holds it in registers, eight neighbouring values
 // a lane and piece, so that every value is read and written once.  The shape
@@ -147,7 +148,21 @@ __device__ __forceinline__ float moved(float v)
 {
     return __builtin_bit_cast(float, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, v), CTRL, 0xF, 0xF, true));
 }
-__device__ __forceinline__ float wave_sum(float v)
+typedef int i32x2 __attribute__((ext_vector_type(2)));
+__device__ __forceinline__ double lanes(double v, int l)
+{
+    const i32x2 w = __builtin_bit_cast(i32x2, v);
+    return __builtin_bit_cast(double, (i32x2){__builtin_amdgcn_readlane(w.x, l), __builtin_amdgcn_readlane(w.y, l)});
+}
+template <int CTRL>
+__device__ __forceinline__ double moved(double v)
+{
+    const i32x2 w = __builtin_bit_cast(i32x2, v);
+    return __builtin_bit_cast(double, (i32x2){__builtin_amdgcn_mov_dpp(w.x, CTRL, 0xF, 0xF, true),
+                                              __builtin_amdgcn_mov_dpp(w.y, CTRL, 0xF, 0xF, true)});
+}
+template <typename V>
+__device__ __forceinline__ V wave_sum(V v)
 {
     v += moved<0xB1>(v);   // lanes 1 0 3 2
     v += moved<0x4E>(v);   // lanes 2 3 0 1
@@ -164,91 +179,85 @@ __device__ __forceinline__ float wave_max(float v)
     return __builtin_fmaxf(__builtin_fmaxf(lanes(v, 0), lanes(v, 16)), __builtin_fmaxf(lanes(v, 32), lanes(v, 48)));
 }
 
-// What the waves of a row pass to each other: each use has a place of its own,
-// so that one barrier is enough.
+// What the waves of a row pass to each other in one norm: each use has a place
+// of its own, so that one barrier is enough.
 constexpr int kMaxWaves = 16;
-constexpr int kNormSums = 4;  // sums and maxima of one norm
-typedef float Parts[kMaxWaves];
+struct Parts {
+    double sum[kMaxWaves];
+    float square[kMaxWaves], top[kMaxWaves];
+};
 
-// Sums over the row's T threads, the same bits in each: within the waves, then
+// Sum over the row's T threads, the same bits in each: within the waves, then
 // the waves in order.
-template <int T, int N>
-__device__ __forceinline__ void row_sums(float (&v)[N], Parts *part)
+template <int T, typename V>
+__device__ __forceinline__ V row_sum(V v, V *part)
 {
-#pragma unroll
-    for (int n = 0; n < N; ++n)
-        v[n] = wave_sum(v[n]);
+    v = wave_sum(v);
     if constexpr (T > 64) {
         if ((threadIdx.x & 63) == 0)
-#pragma unroll
-            for (int n = 0; n < N; ++n)
-                part[n][threadIdx.x >> 6] = v[n];
+            part[threadIdx.x >> 6] = v;
         __syncthreads();
+        v = part[0];
 #pragma unroll
-        for (int n = 0; n < N; ++n) {
-            v[n] = part[n][0];
-#pragma unroll
-            for (int w = 1; w < T / 64; ++w)
-                v[n] += part[n][w];
-        }
+        for (int w = 1; w < T / 64; ++w)
+            v += part[w];
     }
+    return v;
 }
 template <int T>
-__device__ __forceinline__ float row_max(float v, Parts *part)
+__device__ __forceinline__ float row_max(float v, float *part)
 {
     v = wave_max(v);
     if constexpr (T > 64) {
         if ((threadIdx.x & 63) == 0)
-            part[0][threadIdx.x >> 6] = v;
+            part[threadIdx.x >> 6] = v;
         __syncthreads();
-        v = part[0][0];
+        v = part[0];
 #pragma unroll
         for (int w = 1; w < T / 64; ++w)
-            v = __builtin_fmaxf(v, part[0][w]);
+            v = __builtin_fmaxf(v, part[w]);
     }
     return v;
 }
 
 // The row's mean (0 for rms) as a binary32 number and what that is off by, and
-// the mean square about both.  Values past H are zero and stay out of the sums.
+// the mean square about both.  The mean is summed in binary64, where a sum of
+// equal values is exact, and what is left about its binary32 number comes from
+// the sum itself: in a row of equal values every difference is 0, and in one
+// of nearly equal values none is more than a few roundings of its own off.
+// Values past H are zero and stay out of the squares.
 struct Moments {
     float mean, rest, square;
 };
 
 template <int T, int C>
-__device__ __forceinline__ Moments moments(float (&v)[C][8], bool layer, int H, Parts *part)
+__device__ __forceinline__ Moments moments(float (&v)[C][8], bool layer, int H, Parts &part)
 {
-    const float over = 1.f / (float)H;
-    float mean = 0.f;
+    float mean = 0.f, rest = 0.f;
     if (layer) {
-        float s[1] = {0.f};
+        const double count = (double)H, over = 1.0 / count;
+        double s = 0.0;
 #pragma unroll
         for (int i = 0; i < C; ++i) {
             const float *f = v[i];
-            s[0] += ((f[0] + f[1]) + (f[2] + f[3])) + ((f[4] + f[5]) + (f[6] + f[7]));
+            s += (((double)f[0] + (double)f[1]) + ((double)f[2] + (double)f[3])) +
+                 (((double)f[4] + (double)f[5]) + ((double)f[6] + (double)f[7]));
         }
-        row_sums<T>(s, part);
-        mean = s[0] * over;
+        s = row_sum<T>(s, part.sum);
+        mean = (float)(s * over);
+        rest = (float)(__builtin_fma(-count, (double)mean, s) * over);
     }
-    float s[2] = {0.f, 0.f};  // of the squares and of what is left about the rounded mean
+    float s = 0.f;
 #pragma unroll
     for (int i = 0; i < C; ++i) {
         const int at = 8 * ((int)threadIdx.x + i * T);
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-            const float d = at + e < H ? v[i][e] - mean : 0.f;
-            s[0] = __builtin_fmaf(d, d, s[0]);
-            s[1] += d;
+            const float d = at + e < H ? (v[i][e] - mean) - rest : 0.f;
+            s = __builtin_fmaf(d, d, s);
         }
     }
-    if (!layer) {
-        float q[1] = {s[0]};
-        row_sums<T>(q, part + 1);
-        return Moments{0.f, 0.f, q[0] * over};
-    }
-    row_sums<T>(s, part + 1);
-    const float rest = s[1] * over, square = s[0] * over - rest * rest;
-    return Moments{mean, rest, square < 0.f ? 0.f : square};  // (NaN stays)
+    return Moments{mean, rest, row_sum<T>(s, part.square) * (1.f / (float)H)};
 }
 
 // v := the norm of v before weight and bias.  Where the sums leave binary32's
@@ -257,7 +266,7 @@ __device__ __forceinline__ Moments moments(float (&v)[C][8], bool layer, int H, 
 // value first, and the root is taken in binary64.  Infinities and NaN take the
 // plain way: finite values over an infinite root are 0.
 template <int T, int C>
-__device__ __forceinline__ void normalize(float (&v)[C][8], int kind, float eps, int H, Parts *part)
+__device__ __forceinline__ void normalize(float (&v)[C][8], int kind, float eps, int H, Parts &part)
 {
     const bool layer = kind == 2;
     Moments m = moments<T, C>(v, layer, H, part);
@@ -272,7 +281,7 @@ __device__ __forceinline__ void normalize(float (&v)[C][8], int kind, float eps,
                 top = __builtin_fmaxf(top, __builtin_fabsf(v[i][e]));
                 nan |= v[i][e] != v[i][e];
             }
-        top = row_max<T>(nan ? __builtin_inff() : top, part + 3);
+        top = row_max<T>(nan ? __builtin_inff() : top, part.top);
         if (top > 0.f && top < __builtin_inff()) {
             const int k = __builtin_amdgcn_frexp_expf(top);
 #pragma unroll
@@ -283,6 +292,10 @@ __device__ __forceinline__ void normalize(float (&v)[C][8], int kind, float eps,
             __syncthreads();  // (the first sums are read)
             m = moments<T, C>(v, layer, H, part);
             inv = (float)(1.0 / __builtin_sqrt((double)m.square + __builtin_ldexp((double)eps, -2 * k)));
+            // (past binary32 only where all values are equal, since others differ by
+            // 2^-25 or more here: 0 by a finite number, and 0 / 0 where eps is 0)
+            if (eps > 0.f)
+                inv = __builtin_fminf(inv, 0x1.fffffep127f);
         }
     }
 #pragma unroll
@@ -327,7 +340,7 @@ __device__ __forceinline__ void affine(float (&v)[C][8], const NormSide &n, int 
 template <int T, int C>
 __global__ __launch_bounds__(T) void q4_block_norm_kernel(const NormArgs a)
 {
-    __shared__ Parts part[2 * kNormSums];
+    __shared__ Parts part[2];  // post's and pre's
     const int H = a.H, tid = threadIdx.x;
     const size_t row = blockIdx.x;
     if (row >= (size_t)a.M) {  // a padding row of the packed form
@@ -371,7 +384,7 @@ __global__ __launch_bounds__(T) void q4_block_norm_kernel(const NormArgs a)
     for (int i = 0; i < C; ++i)
         values8(y[i], a.y_type, v[i]);
     if (post) {
-        normalize<T, C>(v, a.post.kind, a.post.eps, H, part);
+        normalize<T, C>(v, a.post.kind, a.post.eps, H, part[0]);
         affine<T, C>(v, a.post, H);
     }
     if constexpr (!EARLY)
@@ -412,7 +425,7 @@ __global__ __launch_bounds__(T) void q4_block_norm_kernel(const NormArgs a)
     if (!a.h)
         return;
     if (pre) {
-        normalize<T, C>(v, a.pre.kind, a.pre.eps, H, part + kNormSums);
+        normalize<T, C>(v, a.pre.kind, a.pre.eps, H, part[1]);
         affine<T, C>(v, a.pre, H);
     }
     if (!a.h_scales) {

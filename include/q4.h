@@ -436,11 +436,13 @@ int q4_mx4_linear(const void *x, int x_dtype, const void *x_scales, const void *
  * projection's input.  Norms, with mean() over the row's H values:
  *     Q4_NORM_RMS    v / sqrt(mean(v^2) + eps) weight + bias
  *     Q4_NORM_LAYER  (v - mean(v)) / sqrt(mean((v - mean(v))^2) + eps) weight + bias
- * Everything in between is binary32: r is rounded to its type once, and pre
- * takes it unrounded; h is rounded once.  A row's bits depend on that row (and
- * H) alone.  Sums of squares do not overflow or vanish where the result does
- * not.  An infinity or NaN in a row makes that row's results what the formulas
- * give, and no other row's.
+ * Everything in between is binary32 (a layer norm's mean is summed in
+ * binary64): r is rounded to its type once, and pre takes it unrounded; h is
+ * rounded once.  A row's bits depend on that row (and H) alone.  Sums of
+ * squares do not overflow or vanish where the result does not; a layer norm of
+ * equal values is 0 before weight and bias, however large they are (with eps
+ * 0: 0 / 0, NaN).  An infinity or NaN in a row makes that row's results what the
+ * formulas give, and no other row's.
  *   y         y_dtype, [M][H]
  *   post, pre NULL or kind Q4_NORM_NONE: no norm.  weight and bias of dtype
  *             [H], either NULL (1, and 0)
