@@ -261,17 +261,18 @@ __device__ __forceinline__ Moments moments(float (&v)[C][8], bool layer, int H, 
 }
 
 // v := the norm of v before weight and bias.  Where the sums leave binary32's
-// range (a value over 2^63 or so; or all so small that their squares vanish,
-// and eps no larger), the row is divided by the power of two of its largest
-// value first, and the root is taken in binary64.  Infinities and NaN take the
+// range (a value over 2^63 or so, or an eps next to the largest number; or all
+// so small that their squares vanish, and eps no larger), the row is divided by
+// the power of two of its largest value first, and the root is taken in binary64.  Infinities and NaN take the
 // plain way: finite values over an infinite root are 0.
 template <int T, int C>
 __device__ __forceinline__ void normalize(float (&v)[C][8], int kind, float eps, int H, Parts &part)
 {
     const bool layer = kind == 2;
     Moments m = moments<T, C>(v, layer, H, part);
-    float inv = 1.f / __builtin_sqrtf(m.square + eps);
-    if (!(m.square < __builtin_inff()) || (m.square < 0x1p-80f && eps < 0x1p-40f)) {
+    const float under = m.square + eps;
+    float inv = 1.f / __builtin_sqrtf(under);
+    if (!(under < __builtin_inff()) || (m.square < 0x1p-80f && eps < 0x1p-40f)) {
         float top = 0.f;
         bool nan = false;
 #pragma unroll

@@ -1,5 +1,6 @@
 """The norms around a block where their statistics leave the ordinary range, on
-the GPU: rows of equal and of nearly equal values.
+the GPU: rows of equal and of nearly equal values, and an eps next to the
+largest number.
 
 A layer norm of equal values is exactly 0 (then weight and bias): every
 difference from the mean is 0, and so is their square's mean, whatever the row's
@@ -113,3 +114,20 @@ def test_nearly_equal_values(H, exponent):
         # multiple of 2^-149, so that every difference is off by 2^-150 at most (a subtraction there is exact).
         e = torch.full_like(d, 2.0 ** -150 if eps > 2.0 ** -40 else 0.0)
         check(h, norm64(d, n), norm_error(d, e, n), (H, exponent, eps))
+
+
+@pytest.mark.parametrize("kind", ["rms", "layer"])
+@pytest.mark.parametrize("H", [1, 2, 3, 8, 40, 896, 3584])
+def test_large_eps(kind, H):
+    """An eps up to the largest number, beside squares that reach the rest of the range or none of it."""
+    g = gen(H)
+    base = torch.randn(12, H, generator=g)
+    base = base / base.abs().max(1, keepdim=True).values
+    size = torch.tensor([0.0, 1e-30, 1.0, 1e10, 1e17, 1e18, 5e18, 1e19, 1.8e19, 2.5e19, 1e25, 3e38], dtype=torch.float64)
+    y = (base.double() * size[:, None]).float()
+    for eps in (1.0, 1e30, 1e37, 1.7e38, 3.3e38, torch.finfo(torch.float32).max):
+        gu.note("%s H=%d eps %g" % (kind, H, eps))
+        n = {"kind": kind, "weight": None, "bias": None, "eps": eps}
+        h = run(y, None, None, None, 1.0, n, out_dtype=torch.float32)[1]
+        n["eps"] = torch.tensor(eps, dtype=torch.float32).double().item()
+        check(h, norm64(y.double(), n), norm_error(y.double(), torch.zeros_like(y).double(), n), (kind, H, eps))
