@@ -65,30 +65,44 @@ inline Mx4Shape mx4_shape(bool dense, int M, int N, int K)
     }
     // A workgroup's chain of steps takes its time however small its tile, and what
     // passes through L2 grows as tiles shrink: the smallest tile that gives every
-    // compute unit one workgroup at most, the largest where none does; rows are not
-    // mostly padding.  Measured (us on packed rows, 128 x 256 / 128 x 128 / 64 x 128 /
-    // 64 x 64 / 32 x 64 / 32 x 32 / 16 x 32; y bfloat16):
-    //   512 x 18944 x 3584  34.2 / 39.8 / 39.1 / 47.3 / 60.3 / 67.0 / 98.4
-    //   200 x 18944 x 3584  19.9 / 26.4 / 22.5 / 22.9 / 28.2 / 33.9 / 44.4
-    //   512 x 8192 x 3584   18.3 / 15.9 / 18.0 / 21.6 / 27.2 / 30.8 / 43.9
-    //   1024 x 3584 x 3584  15.6 / 14.7 / 16.5 / 20.0 / 23.3 / 26.6 / 37.1
-    //   124 x 18944 x 3584  20.2 / 16.2 / 19.4 / 18.3 / 20.2 / 22.9 / 30.3
-    //   4000 x 896 x 896    11.0 /  8.1 /  7.5 /  9.1 /  9.2 / 11.4 / 18.9
-    //   512 x 4096 x 3584   15.5 / 13.2 /  9.7 / 11.6 / 13.7 / 16.4 / 21.9
-    //   333 x 4863 x 896    10.9 / 10.5 /  7.2 /  7.3 /  8.0 /  8.8 / 11.5
-    //   300 x 3584 x 18944  66.3 / 42.5 / 32.9 / 30.4 / 40.8 / 44.6 / 57.1
-    //   64 x 18944 x 3584   19.6 / 14.6 / 12.9 / 15.0 / 15.4 / 15.2 / 18.8
-    //   100 x 8192 x 3584   18.6 / 13.2 / 10.0 /  8.4 /  9.3 / 10.3 / 14.8
-    //   256 x 4096 x 8192   35.4 / 22.3 / 16.6 / 12.9 / 16.0 / 18.3 / 26.1
-    //   124 x 3584 x 18944  71.6 / 45.5 / 34.3 / 25.0 / 19.5 / 23.5 / 30.9
-    //   40 x 8192 x 8192    34.1 / 20.9 / 17.5 / 13.1 / 11.3 / 12.4 / 14.6
-    //   64 x 4096 x 8192    33.3 / 20.7 / 17.4 / 12.5 / 10.0 /  8.9 /  9.7
-    //   64 x 3584 x 3584    15.3 / 10.6 /  7.5 /  5.7 /  4.7 /  4.5 /  4.9
-    //   100 x 1024 x 8192   27.3 / 19.0 / 11.7 /  8.7 /  6.8 /  6.7 /  5.4
-    //   32 x 3584 x 3584    15.3 / 10.2 /  7.0 /  5.5 /  4.7 /  4.5 /  3.9
-    //   32 x 16384 x 3584   18.9 / 12.9 / 11.3 /  9.1 /  8.9 /  9.5 / 11.2
-    //   32 x 18944 x 3584   19.5 / 14.1 / 11.7 / 12.9 / 12.3 / 11.4 / 13.0
-    //   20 x 152064 x 896   23.4 / 29.0 / 19.9 / 21.7 / 19.0 / 20.8 / 30.0
+    // compute unit one workgroup at most; where none does, the largest of whose
+    // rows more than half are there, except that up to 32 rows take 32 x 32 while
+    // that is three workgroups a compute unit or fewer.  Measured (us on packed rows,
+    // 128 x 256 / 128 x 128 / 64 x 128 / 64 x 64 / 32 x 64 / 32 x 32 / 16 x 32; y bfloat16;
+    // replays of 24 captured calls or more over up to 24 sets of operands, 700 MB where
+    // they reach it, so that W comes from memory; the seven in turn, median of 9; two
+    // runs differ by up to 5%; the rule is within 9% of the best of each line):
+    //   512 x 18944 x 3584  31.5 / 40.5 / 38.9 / 47.3 / 60.1 / 66.2 / 98.2
+    //   200 x 18944 x 3584  19.1 / 26.4 / 22.4 / 22.7 / 28.2 / 33.8 / 44.1
+    //   512 x 8192 x 3584   18.4 / 15.4 / 18.0 / 21.5 / 27.1 / 30.9 / 43.7
+    //   1024 x 3584 x 3584  17.0 / 14.7 / 16.9 / 20.2 / 24.0 / 27.1 / 38.2
+    //   124 x 18944 x 3584  19.7 / 16.1 / 19.1 / 18.3 / 19.9 / 22.7 / 30.1
+    //   100 x 65536 x 3584  28.3 / 36.2 / 37.5 / 43.0 / 53.8 / 63.0 / 85.1
+    //   100 x 32768 x 3584  21.2 / 19.4 / 21.0 / 23.5 / 28.7 / 33.6 / 44.9
+    //   4000 x 896 x 896    10.9 /  8.0 /  7.5 /  9.0 /  9.1 / 11.1 / 18.2
+    //   512 x 4096 x 3584   16.6 / 13.1 /  9.9 / 11.7 / 14.9 / 17.6 / 23.6
+    //   333 x 4863 x 896    11.1 / 10.5 /  7.2 /  7.3 /  8.0 /  8.7 / 11.5
+    //   300 x 3584 x 18944  66.1 / 42.9 / 33.1 / 30.8 / 40.6 / 44.7 / 56.9
+    //   64 x 18944 x 3584   18.8 / 14.1 / 12.6 / 15.0 / 15.1 / 15.0 / 18.6
+    //   64 x 65536 x 3584   29.4 / 33.1 / 29.1 / 31.4 / 36.8 / 42.2 / 54.4
+    //   40 x 100000 x 3584  42.0 / 52.3 / 45.5 / 45.4 / 51.2 / 56.4 / 67.4
+    //   100 x 8192 x 3584   18.5 / 13.4 / 10.1 /  8.2 /  9.4 / 10.4 / 15.0
+    //   256 x 4096 x 8192   35.3 / 22.7 / 16.8 / 12.9 / 16.3 / 18.7 / 26.6
+    //   124 x 3584 x 18944  71.4 / 46.1 / 34.4 / 24.9 / 19.3 / 23.5 / 30.7
+    //   40 x 8192 x 8192    33.4 / 20.5 / 17.2 / 12.7 / 11.2 / 12.3 / 14.5
+    //   64 x 4096 x 8192    33.0 / 20.6 / 17.3 / 12.5 / 10.1 /  9.0 /  9.8
+    //   64 x 3584 x 3584    15.2 / 10.5 /  7.5 /  5.7 /  4.7 /  4.5 /  4.9
+    //   100 x 1024 x 8192   27.1 / 19.0 / 11.8 /  8.8 /  7.0 /  6.7 /  5.4
+    //   32 x 3584 x 3584    15.3 / 10.2 /  6.9 /  5.4 /  4.7 /  4.5 /  3.8
+    //   32 x 16384 x 3584   18.3 / 12.5 / 10.8 /  8.8 /  8.5 /  9.1 / 10.9
+    //   32 x 18944 x 3584   18.6 / 13.1 / 11.3 / 12.7 / 12.1 / 11.2 / 12.9
+    //   32 x 24576 x 3584   19.2 / 14.4 / 12.7 / 13.8 / 13.2 / 12.6 / 15.4
+    //   20 x 24576 x 896     9.5 /  6.9 /  5.6 /  5.8 /  5.5 /  5.3 /  7.1
+    //   32 x 25600 x 3584   19.4 / 14.7 / 12.9 / 14.0 / 13.5 / 14.2 / 16.4
+    //   20 x 25600 x 896     9.6 /  7.1 /  5.8 /  5.9 /  5.6 /  5.8 /  7.9
+    //   20 x 25600 x 8192   36.2 / 24.9 / 22.2 / 24.3 / 23.4 / 25.7 / 29.6
+    //   32 x 32760 x 3584   20.3 / 16.5 / 14.8 / 15.5 / 14.8 / 15.7 / 20.0
+    //   20 x 152064 x 896   23.7 / 28.8 / 20.0 / 21.7 / 19.0 / 21.0 / 30.3
     const struct {
         Mx4Kernel kernel;
         int bm, bn;
@@ -98,10 +112,10 @@ inline Mx4Shape mx4_shape(bool dense, int M, int N, int K)
     for (const auto &t : tiles)
         if (2 * M > t.bm && mx4_tile_count(M, N, t.bm, t.bn) <= kMx4Units)
             return Mx4Shape{false, t.kernel};
-    const auto largest = M > 64                                 ? Mx4Kernel::tile128x256
-                         : M > 32                               ? Mx4Kernel::tile64x128
-                         : mx4_tile_count(M, N, 32, 32) >= 1024 ? Mx4Kernel::tile32x64
-                                                                : Mx4Kernel::tile32x32;
+    const auto largest = M > 64                                         ? Mx4Kernel::tile128x256
+                         : M > 32                                       ? Mx4Kernel::tile64x128
+                         : mx4_tile_count(M, N, 32, 32) > 3 * kMx4Units ? Mx4Kernel::tile32x64
+                                                                        : Mx4Kernel::tile32x32;
     return Mx4Shape{false, largest};
 }
 
