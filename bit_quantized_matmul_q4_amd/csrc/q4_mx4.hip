@@ -41,9 +41,11 @@ typedef int i32x8 __attribute__((ext_vector_type(8)));
 // A workgroup takes 16 rows by 512 k, a wave four of the rows: 16 lanes a row
 // and step of 128 k, eight values a lane, so that a block is a quad of lanes.
 // A lane with the first part of a block ends with its bytes of four steps.
-// Bound by the reads: 18944 x 3584 packed from binary32 in 57.6 us (5.3 TB/s read
-// and written), from bfloat16 in 34.5 (5.0).  Binary32 in whole lines a load
-// (four values a lane, a block eight lanes) took 57.7.
+// Bound by the reads: 18944 x 3584 packed from binary32 in 56 to 58 us a replayed
+// call (5.3 to 5.5 TB/s read and written; 53 under a tracer, which leaves out the
+// time between two kernels), from bfloat16 in 32 (5.4); to the canonical form 59
+// and 33.  Binary32 in whole lines a load (four values a lane, a block eight
+// lanes) took 57.7 where this took 57.6.
 // PACKED: the packed form (padding written), else codes [rows][K / 2] and
 // scales [rows][K / 32].
 template <int KIND, bool PACKED>
@@ -143,7 +145,8 @@ __device__ __forceinline__ float code_value(uint32_t code, uint32_t byte)
 // by the stores, which are marked as not to be kept: 18944 x 3584 to bfloat16
 // took 43 us with ordinary ones, 33 so (5.2 TB/s); to binary32, with a lane's
 // eight values in two stores of which each fills half of every line, 79 and 109
-// us, in whole lines 50 (6.1 TB/s).
+// us, in whole lines 50 (6.1 TB/s): codes from the last-level cache, where the
+// quantizer leaves them; from memory they are 35 and 62 us.
 template <int KIND>
 __global__ __launch_bounds__(256) void q4_mx4_dequantize_kernel(const uint8_t *__restrict__ codes,
                                                                 const uint8_t *__restrict__ scales,
@@ -502,7 +505,7 @@ __device__ __forceinline__ f32x4 multiply_run(const Run<X> &r, f32x4 acc, const 
 // stand in LDS; packed ones are loaded beside W (staged like the dense ones they
 // took 5.5 us at 16 x 3584 x 3584, beside W 4.2).  Bound by the launch and the
 // loads' latency, or W's bytes: 1 x 3584 x 3584 with the quantization 5.0 us, 8 x
-// 18944 x 3584 on packed rows 8.4 (4.3 TB/s).
+// 18944 x 3584 on packed rows 9.5 (3.8 TB/s; 8.4 with W in the last-level cache).
 template <int KIND, int YK>
 __global__ __launch_bounds__(64 * kFewWaves) void q4_mx4_relay_kernel(const void *__restrict__ x,
                                                                       const uint8_t *__restrict__ xs,
@@ -622,8 +625,9 @@ __global__ __launch_bounds__(64 * kFewWaves) void q4_mx4_wide_kernel(const void 
 // beside the other's products.  A wave reads the operands of a step from LDS
 // while it multiplies the one before: the barrier that frees a step's place
 // falls when its operands are in registers.  4096 x 18944 x 3584 to bfloat16 takes
-// 133 to 143 us (3.9 to 4.2 PF/s; from registers alone the matrix cores reach
-// 6.9): without the stores 126, without W's loads too 105, the products alone 91.
+// 153 to 155 us with operands from memory and 133 with operands in the last-level
+// cache (3.6 and 4.2 PF/s; from registers alone the matrix cores reach 6.9); so
+// measured, without the stores 126, without W's loads too 105, the products alone 91.
 // 256 x 256 with both operands in LDS, in workgroups that stay and take tile
 // after tile, took 148, W two steps ahead instead of three 145.
 template <int YK>
@@ -825,8 +829,9 @@ __global__ __launch_bounds__(256, 2) void q4_mx4_gemm_kernel(
 // group stands before its last products, when their operands are in registers.
 // Bound by the chain of groups (a barrier, LDS and dependent products each) and
 // by what passes through L2 (x for each column of tiles, W for each row):
-// 124 x 3584 x 18944 in 13.6 us on 224 workgroups of 32 x 64, 0.37 us a group; 124 x
-// 18944 x 3584 in 13.5 on 148 of 128 x 128.
+// 124 x 3584 x 18944 in 19.4 us on 224 workgroups of 32 x 64, 0.52 us a group, and 124 x
+// 18944 x 3584 in 16.2 on 148 of 128 x 128, with W from memory (13.6, 0.37 a group, and
+// 13.5 with W in the last-level cache).
 template <int TM, int TN, int WN, int A, int YK>
 __global__ __launch_bounds__(64 * WN) void q4_mx4_mid_kernel(
     const void *__restrict__ xq_, const uint8_t *__restrict__ xs, const uint8_t *__restrict__ wq,
