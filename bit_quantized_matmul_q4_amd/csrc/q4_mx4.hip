@@ -7,10 +7,12 @@
 // instruction v_mfma_scale_f32_16x16x128 takes both operands and their scales
 // as they are stored.  A row's sum is one chain of such instructions over its
 // steps of 128 k, in order, from +0, in every kernel: its bits depend on the
-// row and W alone, not on M, the row's place or the kernel.  A step adds its
-// 128 products to the sum with an error of about 2^-24 of the magnitudes that
-// it adds; sums of a few thousand products of like size stay exact, since a
-// product is a multiple of a quarter of its block's scales.
+// row and W alone, not on M, the row's place or the kernel.  A step adds its four
+// blocks one after another, each exactly and then within 2^-23 of the sum's size;
+// a block all of whose products stand 2^28 or more below the sum is lost (measured:
+// 1 and 128 products of 36 2^-32 give 1, 18 2^-24 off).  Sums of a few thousand products
+// of like size stay exact, since a product is a multiple of a quarter of its
+// block's scales.
 //
 // Packed layout of both operands (q4.h): codes in tiles of 16 rows by 128 k,
 // order [ceil(rows / 16)][ceil(K / 128)], 1024 bytes each; lane l = 16 g + c

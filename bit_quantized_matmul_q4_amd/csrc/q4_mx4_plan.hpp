@@ -55,8 +55,8 @@ inline Mx4Shape mx4_shape(bool dense, int M, int N, int K)
         // wide: 18944 x 3584 at 1 / 4 rows 10.8 / 10.6, 14.7 / 13.0; 152064 x 896 26.0 /
         // 14.6; 3584 x 3584 5.0 / 5.5; a run of steps that holds all of K leaves the
         // relay one wave: 4864 x 896 3.7 / 3.4.  Packed rows, which the relay loads
-        // beside W: 18944 x 3584 9.6 / 11.1, 32768 x 3584 13.9 / 13.4, 65536 x 3584 24.6 /
-        // 23.8; 4864 x 896 2.9 / 3.3, 16384 x 896 4.3 / 4.0, 152064 x 896 22.4 / 14.6.
+        // beside W: 18944 x 3584 9.4 / 10.9, 32768 x 3584 13.5 / 13.1, 65536 x 3584 22.8 /
+        // 22.7; 4864 x 896 2.9 / 3.3, 16384 x 896 4.3 / 4.0, 152064 x 896 22.4 / 14.6.
         const bool few_steps = mx4_steps(K) <= 8;
         const bool many = s.fused ? N >= 16384 || few_steps : N >= 32768 || (N >= 16384 && few_steps);
         if (many && mx4_few_lds(M, K) <= 60 * 1024)
